@@ -247,6 +247,44 @@ te_status te_layernorm_fp8(const void* x, te_dtype in_dtype, int64_t rows, int64
                            void* ln_out, float* mu, float* rsigma, float* amax_out, float* scale_inv_out,
                            void* stream);
 
+/* ---- RMSNorm ---------------------------------------------------------------------
+ * The norm in front of a layer's linears, with the residual's addition, and its output in
+ * 8 bits as the FP8 / MXFP8 GEMMs read it:
+ *   s = x + residual (residual NULL: s = x);  rsigma = 1 / sqrt(mean(s^2) + eps);
+ *   y = (s * rsigma) * gamma, in fp32.
+ * x, residual, res_out: in_dtype (TE_BF16 or TE_F32), [rows, cols]; gamma device fp32 [cols].
+ * Any number of rows; cols % 16 == 0 (MXFP8 % 32), cols <= 16384; eps >= 0.  Outputs, each
+ * rounded once from the fp32 value (y to bf16 and y to 8 bits are separate roundings):
+ *   res_out (nullable)  s, the next residual; may be x or residual itself;
+ *   y       (nullable)  bf16, the operand of the BF16 GEMMs and of Wgrad's quantized col copy;
+ *   rsigma  (nullable)  fp32 [rows], kept with s for the backward pass.
+ * te_rmsnorm_fp8: q_row (nullable) = fmt(fl32(y * *scale)), saturating (fmt TE_E4M3 or
+ *   TE_E5M2, DelayedScaling's scale from the history); amax_out (nullable) = max |y| in fp32
+ *   (0 for no rows, NaN if a y is NaN); scale_inv_out (nullable) = fl32(1 / *scale).  `scale`
+ *   may be NULL where neither q_row nor scale_inv_out is asked for.
+ * te_rmsnorm_mxfp8: q_row, s_row as te_quantize_mxfp8 writes its row copy of y (scales in the
+ *   tensor-core layout, padding zero); both are required. */
+te_status te_rmsnorm_fp8(const void* x, te_dtype in_dtype, int64_t rows, int64_t cols, const void* residual,
+                         const float* gamma, float eps, te_dtype fmt, const float* scale, uint8_t* q_row, void* y,
+                         void* res_out, float* rsigma, float* amax_out, float* scale_inv_out, void* stream);
+te_status te_rmsnorm_mxfp8(const void* x, te_dtype in_dtype, int64_t rows, int64_t cols, const void* residual,
+                           const float* gamma, float eps, uint8_t* q_row, uint8_t* s_row, void* y, void* res_out,
+                           float* rsigma, void* stream);
+
+/* Its backward pass.  dy bf16 [rows, cols] (the gradient of y); s (the forward pass's res_out,
+ * or x where there was no residual), dres and dx in_dtype; rsigma fp32 [rows].  With
+ * xhat = s * rsigma and p = dy * gamma (fp32):
+ *   dx = rsigma * (p - xhat * mean(p * xhat)) + dres      (dres nullable: the gradient that
+ *        arrives on res_out) -- the gradient of x and of residual alike; dx may be dres or s;
+ *   dgamma fp32 [cols] = sum over the rows of dy * xhat (overwritten; 0 for no rows).
+ * workspace: device memory of at least te_rmsnorm_bwd_workspace_bytes(rows, cols) bytes
+ * (at most 512 rows of fp32 partial sums), 16-byte aligned, no initial contents needed.  The
+ * partial sums are added in a fixed order, so the result does not depend on timing. */
+size_t te_rmsnorm_bwd_workspace_bytes(int64_t rows, int64_t cols);
+te_status te_rmsnorm_bwd(const void* dy, const void* s, te_dtype in_dtype, int64_t rows, int64_t cols,
+                         const float* gamma, const float* rsigma, const void* dres, void* dx, float* dgamma,
+                         float* workspace, size_t workspace_bytes, void* stream);
+
 /* ---- GEMMs ----------------------------------------------------------------------
  * Common: A [M, K], B [N, K] contraction-major; D [M, N] row-major of out_dtype
  * (TE_BF16, round-to-nearest-even, or TE_F32); bias (nullable) device fp32 [N];

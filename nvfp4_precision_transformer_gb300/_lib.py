@@ -48,6 +48,11 @@ SIGNATURES = {
     "te_dbias_workspace_bytes": (ctypes.c_size_t, [_i64, _i64]),
     "te_quantize_fp8_dbias": (_st, [_vp, _int, _i64, _i64, _int, _vp, _int, _vp, _vp, _vp, _vp, _vp, _vp,
                                     ctypes.c_size_t, _vp]),
+    "te_rmsnorm_fp8": (_st, [_vp, _int, _i64, _i64, _vp, _vp, ctypes.c_float, _int, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                             _vp]),
+    "te_rmsnorm_mxfp8": (_st, [_vp, _int, _i64, _i64, _vp, _vp, ctypes.c_float, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "te_rmsnorm_bwd_workspace_bytes": (ctypes.c_size_t, [_i64, _i64]),
+    "te_rmsnorm_bwd": (_st, [_vp, _vp, _int, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
     "te_quantize_nvfp4": (_st, [_vp, _int, _i64, _i64, _u32, _u32, _u64, _u64, _vp, _vp,
                                 _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "te_gemm_bf16": (_st, [_vp, _int, _vp, _int, _vp, _vp, _int, _int, _i64, _i64, _i64, _vp]),
@@ -177,6 +182,79 @@ def te_layernorm_fp8(x, gamma, beta, eps: float, fmt: int, scale, q_row, ln_out=
     _check("te_layernorm_fp8", lib().te_layernorm_fp8(
         _ptr(x), _in_dtype(x), r, c, _ptr(gamma), _ptr(beta), float(eps), fmt, _ptr(scale), _ptr(q_row),
         _ptr(ln_out), _ptr(mu), _ptr(rsigma), _ptr(amax_out), _ptr(scale_inv_out), _stream(stream)))
+
+
+def _need(fn: str, name: str, t, dtype, shape, optional: bool = False):
+    """Refuses a tensor that the call would misread: not on the GPU, not contiguous, of another
+    dtype (one, or a tuple of them) or size.  `shape` may be an element count (at least so many)."""
+    if t is None:
+        if optional:
+            return None
+        raise TypeError(f"{fn}: {name} is required")
+    if t.dtype is not dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
+        raise TypeError(f"{fn}: {name} is {t.dtype}, expected {dtype}")
+    if t.numel() < shape if isinstance(shape, int) else t.shape != shape:
+        raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {shape}")
+    if not t.is_contiguous():
+        raise ValueError(f"{fn}: {name} is not contiguous")
+    if not t.is_cuda:
+        raise ValueError(f"{fn}: {name} is not on the GPU")
+    return t.data_ptr()
+
+
+def _norm_operands(fn, x, gamma, residual, res_out, y, rsigma):
+    import torch
+    if x.dim() != 2:
+        raise ValueError(f"{fn}: x has shape {tuple(x.shape)}, expected [rows, cols]")
+    shape = x.shape
+    px = _need(fn, "x", x, (torch.bfloat16, torch.float32), shape)
+    dt = x.dtype
+    return (px, _in_dtype(x), shape[0], shape[1], _need(fn, "residual", residual, dt, shape, True),
+            _need(fn, "gamma", gamma, torch.float32, shape[1:]), _need(fn, "res_out", res_out, dt, shape, True),
+            _need(fn, "y", y, torch.bfloat16, shape, True), _need(fn, "rsigma", rsigma, torch.float32, shape[:1], True))
+
+
+def te_rmsnorm_fp8(x, gamma, eps: float, fmt: int, scale=None, q_row=None, residual=None, res_out=None, y=None,
+                   rsigma=None, amax_out=None, scale_inv_out=None, stream=None):
+    """RMSNorm of x (+ residual), its output in FP8 with a per-tensor scale (and / or y in bf16)."""
+    import torch
+    fn, f32 = "te_rmsnorm_fp8", torch.float32
+    px, dt, r, c, pres, pg, pro, py, prs = _norm_operands(fn, x, gamma, residual, res_out, y, rsigma)
+    _check(fn, lib().te_rmsnorm_fp8(
+        px, dt, r, c, pres, pg, float(eps), fmt, _need(fn, "scale", scale, f32, 1, True),
+        _need(fn, "q_row", q_row, torch.uint8, x.shape, True), py, pro, prs,
+        _need(fn, "amax_out", amax_out, f32, 1, True), _need(fn, "scale_inv_out", scale_inv_out, f32, 1, True),
+        _stream(stream)))
+
+
+def te_rmsnorm_mxfp8(x, gamma, eps: float, q_row, s_row, residual=None, res_out=None, y=None, rsigma=None, stream=None):
+    """RMSNorm of x (+ residual), its output in MXFP8 (E4M3 codes, E8M0 scales in the tensor-core layout)."""
+    import torch
+    fn = "te_rmsnorm_mxfp8"
+    px, dt, r, c, pres, pg, pro, py, prs = _norm_operands(fn, x, gamma, residual, res_out, y, rsigma)
+    _check(fn, lib().te_rmsnorm_mxfp8(
+        px, dt, r, c, pres, pg, float(eps), _need(fn, "q_row", q_row, torch.uint8, x.shape),
+        _need(fn, "s_row", s_row, torch.uint8, te_scale_bytes(E8M0, r, c)), py, pro, prs, _stream(stream)))
+
+
+def te_rmsnorm_bwd_workspace_bytes(rows: int, cols: int) -> int:
+    return int(lib().te_rmsnorm_bwd_workspace_bytes(rows, cols))
+
+
+def te_rmsnorm_bwd(dy, s, gamma, rsigma, dx, dgamma, workspace, dres=None, stream=None):
+    """Gradients of te_rmsnorm_*: dx (of x and of the residual) and dgamma."""
+    import torch
+    fn, f32 = "te_rmsnorm_bwd", torch.float32
+    if s.dim() != 2:
+        raise ValueError(f"{fn}: s has shape {tuple(s.shape)}, expected [rows, cols]")
+    shape, dt = s.shape, s.dtype
+    ps = _need(fn, "s", s, (torch.bfloat16, f32), shape)
+    pw = _need(fn, "workspace", workspace, f32, 0)
+    _check(fn, lib().te_rmsnorm_bwd(
+        _need(fn, "dy", dy, torch.bfloat16, shape), ps, _in_dtype(s), shape[0], shape[1],
+        _need(fn, "gamma", gamma, f32, shape[1:]), _need(fn, "rsigma", rsigma, f32, shape[:1]),
+        _need(fn, "dres", dres, dt, shape, True), _need(fn, "dx", dx, dt, shape),
+        _need(fn, "dgamma", dgamma, f32, shape[1:]), pw, workspace.numel() * 4, _stream(stream)))
 
 
 def te_quantize_mxfp8(x, q_row=None, s_row=None, q_col=None, s_col=None, stream=None):

@@ -1,0 +1,507 @@
+// Root-mean-square norm with the residual's addition and an 8-bit output, and its gradient.
+//
+//   forward   s = x + residual;  rsigma = 1 / sqrt(mean(s^2) + eps);  y = (s * rsigma) * gamma
+//             outputs: s, y in bf16, y in FP8 (per-tensor scale) or MXFP8 (1 x 32 blocks), rsigma
+//   backward  xhat = s * rsigma, p = dy * gamma:
+//             ds = rsigma * (p - xhat * mean(p * xhat)) (+ the residual stream's own gradient)
+//             dgamma = sum over the rows of dy * xhat
+//
+// Both are bound by HBM.  A row belongs to WPR warps (1 to 16: 1024 columns a warp), each lane
+// holding up to four chunks of eight columns in registers, so every tensor is read once; the
+// row's sum is a butterfly over the lanes and one exchange through shared memory between the
+// row's warps.  Groups walk the rows with the grid's stride, and gamma comes from L1.  All sums
+// are fp32 in a fixed order, so results do not depend on timing.
+#include <cuda_bf16.h>
+#include <math.h>
+
+#include "common.cuh"
+#include "convert.cuh"
+
+namespace te {
+namespace {
+
+constexpr int kCh = 4;                       // chunks of eight columns per lane
+constexpr int kWarpCols = 32 * 8 * kCh;      // columns of a row per warp
+constexpr int64_t kMaxCols = 16 * kWarpCols;
+constexpr int64_t kMaxPartials = 512;        // rows of partial column sums in the workspace
+
+// Warps of a CTA when a row takes `wpr` of them, and the rows that it works on at a time.
+__host__ __device__ constexpr int cta_warps(int wpr) { return wpr < 8 ? 8 : wpr; }
+__host__ __device__ constexpr int cta_rows(int wpr) { return cta_warps(wpr) / wpr; }
+
+// Eight consecutive elements, as loaded.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<__nv_bfloat16> {
+  uint4 a;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ float2 pair(int i) const {
+    const uint32_t w = i == 0 ? a.x : (i == 1 ? a.y : (i == 2 ? a.z : a.w));
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  }
+};
+template <>
+struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = *reinterpret_cast<const float4*>(p);
+    b = *reinterpret_cast<const float4*>(p + 4);
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ float2 pair(int i) const {
+    return i == 0 ? make_float2(a.x, a.y) : (i == 1 ? make_float2(a.z, a.w)
+                                                     : (i == 2 ? make_float2(b.x, b.y) : make_float2(b.z, b.w)));
+  }
+};
+
+__device__ __forceinline__ uint32_t bf16x2(float2 v) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float2 (&v)[4]) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(bf16x2(v[0]), bf16x2(v[1]), bf16x2(v[2]), bf16x2(v[3]));
+}
+__device__ __forceinline__ void store8(float* p, const float2 (&v)[4]) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+}
+__device__ __forceinline__ void ldg8(const float* p, float2 (&v)[4]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  v[0] = make_float2(a.x, a.y), v[1] = make_float2(a.z, a.w);
+  v[2] = make_float2(b.x, b.y), v[3] = make_float2(b.z, b.w);
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+  return v;
+}
+
+// Sum over the WPR warps of a row, in warp order.  `red` has two slots (`turn` alternates
+// between them), so that one barrier a row is enough.
+template <int WPR>
+__device__ __forceinline__ float row_sum(float v, float (*red)[WPR], int turn, int grp, int wr, int lane) {
+  v = warp_sum(v);
+  if (WPR == 1) return v;
+  if (lane == 0) red[turn][wr] = v;
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "n"(32 * WPR) : "memory");
+  float t = red[turn][0];
+#pragma unroll
+  for (int w = 1; w < WPR; ++w) t = __fadd_rn(t, red[turn][w]);
+  return t;
+}
+
+struct NormArgs {
+  const void* x;
+  const void* res;
+  const float* gamma;
+  float eps;
+  int64_t rows, cols;
+  __nv_bfloat16* y;
+  void* res_out;
+  float* rsigma;
+  uint8_t* q;
+  const float* scale;      // FP8
+  int e5m2;
+  unsigned int* amax;
+  float* scale_inv;
+  int amax_whole;          // 1: the grid is one CTA, which writes the amax itself
+  uint8_t* s_row;          // MXFP8
+  int64_t kpad, rpad;
+};
+
+// The maximum of |y| is kept as bits (ordered as the non-negative floats are), so a NaN, whose
+// bits are above infinity's, is not lost.
+template <typename T, int WPR, bool MX>
+__global__ void __launch_bounds__(32 * cta_warps(WPR), WPR <= 8 ? 2 : 1) rmsnorm_kernel(const NormArgs a) {
+  constexpr int GR = cta_rows(WPR);
+  __shared__ float red[GR][2][WPR];
+  __shared__ unsigned int top[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int grp = warp / WPR, wr = warp % WPR;
+  const int64_t C = a.cols;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * GR;
+  const T* x = static_cast<const T*>(a.x);
+  const T* res = static_cast<const T*>(a.res);
+  const int col0 = (wr * kCh * 32 + lane) * 8;   // chunk t starts at col0 + 256 t
+  const float sc = !MX && a.scale ? *a.scale : 1.0f;
+  unsigned int lmax = 0;
+
+  Raw8<T> rx[kCh], rr[kCh];
+  auto load = [&](int64_t row) {
+#pragma unroll
+    for (int t = 0; t < kCh; ++t) {
+      const int col = col0 + 256 * t;
+      rx[t].zero();
+      rr[t].zero();
+      if (row < a.rows && col < C) {
+        rx[t].load(x + row * C + col);
+        if (res) rr[t].load(res + row * C + col);
+      }
+    }
+  };
+  int64_t row = static_cast<int64_t>(blockIdx.x) * GR + grp;
+  load(row);
+  for (int turn = 0; row < a.rows; row += step, turn ^= 1) {
+    float2 v[kCh][4];
+    float2 sq = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int t = 0; t < kCh; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[t][i] = res ? __fadd2_rn(rx[t].pair(i), rr[t].pair(i)) : rx[t].pair(i);
+        sq = __ffma2_rn(v[t][i], v[t][i], sq);
+      }
+    load(row + step);   // the next row's loads are in flight while this one is reduced and written
+    const float sum = row_sum<WPR>(__fadd_rn(sq.x, sq.y), red[grp], turn, grp, wr, lane);
+    const float rs = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(sum, static_cast<float>(C)), a.eps)));
+    if (a.rsigma && wr == 0 && lane == 0) a.rsigma[row] = rs;
+    const float2 rs2 = make_float2(rs, rs);
+#pragma unroll
+    for (int t = 0; t < kCh; ++t) {
+      const int col = col0 + 256 * t;
+      const bool live = col < C;
+      const int64_t at = row * C + col;
+      float2 g[4] = {}, y[4];
+      if (live) ldg8(a.gamma + col, g);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[i] = __fmul2_rn(__fmul2_rn(v[t][i], rs2), g[i]);
+      if (live && a.res_out) store8(static_cast<T*>(a.res_out) + at, v[t]);
+      if (live && a.y) store8(a.y + at, y);
+      unsigned int m = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        m = max(m, max(__float_as_uint(y[i].x) & 0x7FFFFFFFu, __float_as_uint(y[i].y) & 0x7FFFFFFFu));
+      float mul = sc;
+      if (MX) {
+        // a block of 32 columns is four neighbouring lanes' chunks (cols % 32 == 0: all live or none)
+        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+        const int e = mx_exponent(__uint_as_float(m));
+        mul = mx_mult(e);
+        if (live && (lane & 3) == 0)
+          a.s_row[scale_offset(static_cast<uint64_t>(row), static_cast<uint64_t>(col >> 5), static_cast<uint64_t>(a.kpad))] =
+              static_cast<uint8_t>(e + 127);
+      } else if (live) {
+        lmax = max(lmax, m);
+      }
+      if (live && a.q) {
+        const float2 m2 = make_float2(mul, mul);
+        uint32_t w[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float2 p = __fmul2_rn(y[2 * h], m2), r = __fmul2_rn(y[2 * h + 1], m2);
+          w[h] = (!MX && a.e5m2) ? (cvt_e5m2x2(p.x, p.y) | (cvt_e5m2x2(r.x, r.y) << 16))
+                                 : (cvt_e4m3x2(p.x, p.y) | (cvt_e4m3x2(r.x, r.y) << 16));
+        }
+        *reinterpret_cast<uint2*>(a.q + at) = make_uint2(w[0], w[1]);
+      }
+    }
+    if (MX && wr == 0 && lane == 0)   // padding columns of this row's scales
+      for (int64_t j = C / 32; j < a.kpad; ++j)
+        a.s_row[scale_offset(static_cast<uint64_t>(row), static_cast<uint64_t>(j), static_cast<uint64_t>(a.kpad))] = 0;
+  }
+  if (MX) {
+    // padding rows, four scale columns a word
+    const int64_t words = (a.rpad - a.rows) * (a.kpad / 4);
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < words;
+         i += static_cast<int64_t>(gridDim.x) * blockDim.x)
+      *reinterpret_cast<uint32_t*>(a.s_row + scale_offset(static_cast<uint64_t>(a.rows + i / (a.kpad / 4)),
+                                                          static_cast<uint64_t>(i % (a.kpad / 4) * 4),
+                                                          static_cast<uint64_t>(a.kpad))) = 0u;
+    return;
+  }
+  if (a.scale_inv && blockIdx.x == 0 && threadIdx.x == 0) *a.scale_inv = __fdiv_rn(1.0f, sc);
+  if (a.amax) {
+    lmax = __reduce_max_sync(0xFFFFFFFFu, lmax);
+    if (lane == 0) top[warp] = lmax;
+    __syncthreads();
+    if (warp == 0) {
+      lmax = __reduce_max_sync(0xFFFFFFFFu, lane < cta_warps(WPR) ? top[lane] : 0u);
+      if (lane == 0) {
+        if (a.amax_whole) *a.amax = lmax;
+        else atomicMax(a.amax, lmax);
+      }
+    }
+  }
+}
+
+struct NormBwdArgs {
+  const __nv_bfloat16* dy;
+  const void* s;
+  const void* dres;
+  const float* gamma;
+  const float* rsigma;
+  int64_t rows, cols;
+  void* dx;
+  float* partial;   // [gridDim.x, cols]
+};
+
+template <typename T, int WPR>
+__global__ void __launch_bounds__(32 * cta_warps(WPR), WPR <= 8 ? 2 : 1) rmsnorm_bwd_kernel(const NormBwdArgs a) {
+  constexpr int GR = cta_rows(WPR);
+  __shared__ float red[GR][2][WPR];
+  extern __shared__ __align__(16) float cols_sum[];   // [GR - 1][cols]
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int grp = warp / WPR, wr = warp % WPR;
+  const int64_t C = a.cols;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * GR;
+  const T* s = static_cast<const T*>(a.s);
+  const T* dres = static_cast<const T*>(a.dres);
+  const int col0 = (wr * kCh * 32 + lane) * 8;
+  float2 dg[kCh][4];
+#pragma unroll
+  for (int t = 0; t < kCh; ++t)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dg[t][i] = make_float2(0.f, 0.f);
+
+  int turn = 0;
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * GR + grp; row < a.rows; row += step, turn ^= 1) {
+    Raw8<__nv_bfloat16> rd[kCh];
+    Raw8<T> rx[kCh], rr[kCh];
+#pragma unroll
+    for (int t = 0; t < kCh; ++t) {
+      const int col = col0 + 256 * t;
+      rd[t].zero();
+      rx[t].zero();
+      rr[t].zero();
+      if (col < C) {
+        rd[t].load(a.dy + row * C + col);
+        rx[t].load(s + row * C + col);
+        if (dres) rr[t].load(dres + row * C + col);
+      }
+    }
+    const float rs = a.rsigma[row];
+    const float2 rs2 = make_float2(rs, rs);
+    float2 dot = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int t = 0; t < kCh; ++t) {
+      const int col = col0 + 256 * t;
+      float2 g[4] = {};
+      if (col < C) ldg8(a.gamma + col, g);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 w = __fmul2_rn(rd[t].pair(i), __fmul2_rn(rx[t].pair(i), rs2));   // dy * xhat
+        dg[t][i] = __fadd2_rn(dg[t][i], w);
+        dot = __ffma2_rn(w, g[i], dot);
+      }
+    }
+    const float sum = row_sum<WPR>(__fadd_rn(dot.x, dot.y), red[grp], turn, grp, wr, lane);
+    const float c = -__fdiv_rn(sum, static_cast<float>(C));
+    const float2 c2 = make_float2(c, c);
+#pragma unroll
+    for (int t = 0; t < kCh; ++t) {
+      const int col = col0 + 256 * t;
+      if (col >= C) break;
+      float2 g[4], o[4];
+      ldg8(a.gamma + col, g);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 p = __fmul2_rn(rd[t].pair(i), g[i]);
+        const float2 d = __ffma2_rn(__fmul2_rn(rx[t].pair(i), rs2), c2, p);
+        o[i] = __ffma2_rn(d, rs2, rr[t].pair(i));
+      }
+      store8(static_cast<T*>(a.dx) + row * C + col, o);
+    }
+  }
+  // the CTA's column sums: the row groups in order
+  if (GR > 1) {
+    if (grp > 0) {
+#pragma unroll
+      for (int t = 0; t < kCh; ++t)
+        if (col0 + 256 * t < C) store8(cols_sum + (grp - 1) * C + col0 + 256 * t, dg[t]);
+    }
+    __syncthreads();
+    if (grp > 0) return;
+    for (int k = 0; k < GR - 1; ++k)
+#pragma unroll
+      for (int t = 0; t < kCh; ++t) {
+        const int col = col0 + 256 * t;
+        if (col >= C) break;
+        const float4 u = *reinterpret_cast<const float4*>(cols_sum + k * C + col);
+        const float4 w = *reinterpret_cast<const float4*>(cols_sum + k * C + col + 4);
+        dg[t][0] = __fadd2_rn(dg[t][0], make_float2(u.x, u.y));
+        dg[t][1] = __fadd2_rn(dg[t][1], make_float2(u.z, u.w));
+        dg[t][2] = __fadd2_rn(dg[t][2], make_float2(w.x, w.y));
+        dg[t][3] = __fadd2_rn(dg[t][3], make_float2(w.z, w.w));
+      }
+  }
+#pragma unroll
+  for (int t = 0; t < kCh; ++t)
+    if (col0 + 256 * t < C) store8(a.partial + static_cast<int64_t>(blockIdx.x) * C + col0 + 256 * t, dg[t]);
+}
+
+// dgamma[c] = the sum of the partial rows in a fixed order: 32 columns x 8 row lanes a CTA.
+__global__ void __launch_bounds__(256) dgamma_kernel(const float* __restrict__ partial, int n, int64_t C,
+                                                     float* __restrict__ dgamma) {
+  __shared__ float part[8][32];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+  float t = 0.0f;
+  if (c < C) {
+#pragma unroll 8
+    for (int r = w; r < n; r += 8) t = __fadd_rn(t, partial[static_cast<int64_t>(r) * C + c]);
+  }
+  part[w][lane] = t;
+  __syncthreads();
+  if (w == 0 && c < C) {
+#pragma unroll
+    for (int k = 1; k < 8; ++k) t = __fadd_rn(t, part[k][lane]);
+    dgamma[c] = t;
+  }
+}
+
+// Warps per row: the fewest whose lanes hold `cols` columns.
+int warps_per_row(int64_t cols) {
+  int w = 1;
+  while (w * kWarpCols < cols) w *= 2;
+  return w;
+}
+
+// CTAs of the persistent walk over `rows`.
+int walk_grid(int64_t rows, int wpr) {
+  const int64_t want = (rows + cta_rows(wpr) - 1) / cta_rows(wpr);
+  const int64_t fit = static_cast<int64_t>(wpr <= 8 ? 2 : 1) * num_sms();
+  const int64_t most = fit < kMaxPartials ? fit : kMaxPartials;
+  return static_cast<int>(want < most ? (want > 0 ? want : 1) : most);
+}
+
+template <typename T, bool MX>
+te_status launch_norm(NormArgs& a, cudaStream_t st) {
+  const int wpr = warps_per_row(a.cols);
+  const int grid = walk_grid(a.rows, wpr);
+  if (a.amax) {
+    a.amax_whole = grid == 1;
+    if (grid > 1 && cudaMemsetAsync(a.amax, 0, sizeof(float), st) != cudaSuccess) return record_cuda(cudaGetLastError());
+  }
+  switch (wpr) {
+    case 1: rmsnorm_kernel<T, 1, MX><<<grid, 256, 0, st>>>(a); break;
+    case 2: rmsnorm_kernel<T, 2, MX><<<grid, 256, 0, st>>>(a); break;
+    case 4: rmsnorm_kernel<T, 4, MX><<<grid, 256, 0, st>>>(a); break;
+    case 8: rmsnorm_kernel<T, 8, MX><<<grid, 256, 0, st>>>(a); break;
+    default: rmsnorm_kernel<T, 16, MX><<<grid, 512, 0, st>>>(a); break;
+  }
+  count_launch();
+  return launch_status();
+}
+
+template <typename T>
+void launch_norm_bwd(const NormBwdArgs& a, int wpr, int grid, cudaStream_t st) {
+  const size_t smem = static_cast<size_t>(cta_rows(wpr) - 1) * static_cast<size_t>(a.cols) * sizeof(float);
+  switch (wpr) {
+    case 1: rmsnorm_bwd_kernel<T, 1><<<grid, 256, smem, st>>>(a); break;
+    case 2: rmsnorm_bwd_kernel<T, 2><<<grid, 256, smem, st>>>(a); break;
+    case 4: rmsnorm_bwd_kernel<T, 4><<<grid, 256, smem, st>>>(a); break;
+    case 8: rmsnorm_bwd_kernel<T, 8><<<grid, 256, smem, st>>>(a); break;
+    default: rmsnorm_bwd_kernel<T, 16><<<grid, 512, smem, st>>>(a); break;
+  }
+}
+
+te_status check_norm(const void* x, te_dtype in, int64_t rows, int64_t cols, const float* gamma, float eps,
+                     const void* residual, const void* res_out, const void* y) {
+  if (in != TE_BF16 && in != TE_F32) return TE_ERR_DTYPE;
+  if (rows < 0 || cols <= 0 || cols % 16 || cols > kMaxCols || rows > (int64_t(1) << 31)) return TE_ERR_SHAPE;
+  if (!(eps >= 0.0f) || !isfinite(eps)) return TE_ERR_ARG;
+  if (gamma == nullptr || (rows > 0 && x == nullptr)) return TE_ERR_NULL;
+  if (!aligned16(x) || !aligned16(gamma) || !aligned16(residual) || !aligned16(res_out) || !aligned16(y))
+    return TE_ERR_ALIGN;
+  return TE_OK;
+}
+
+NormArgs norm_args(const void* x, int64_t rows, int64_t cols, const void* residual, const float* gamma, float eps,
+                   void* y, void* res_out, float* rsigma) {
+  NormArgs a = {};
+  a.x = x;
+  a.res = residual;
+  a.gamma = gamma;
+  a.eps = eps;
+  a.rows = rows;
+  a.cols = cols;
+  a.y = static_cast<__nv_bfloat16*>(y);
+  a.res_out = res_out;
+  a.rsigma = rsigma;
+  return a;
+}
+
+}  // namespace
+}  // namespace te
+
+using namespace te;
+
+extern "C" {
+
+te_status te_rmsnorm_fp8(const void* x, te_dtype in_dtype, int64_t rows, int64_t cols, const void* residual,
+                         const float* gamma, float eps, te_dtype fmt, const float* scale, uint8_t* q_row, void* y,
+                         void* res_out, float* rsigma, float* amax_out, float* scale_inv_out, void* stream) {
+  te_status s = check_norm(x, in_dtype, rows, cols, gamma, eps, residual, res_out, y);
+  if (s != TE_OK) return s;
+  if (fmt != TE_E4M3 && fmt != TE_E5M2) return TE_ERR_DTYPE;
+  if ((q_row || scale_inv_out) && scale == nullptr) return TE_ERR_NULL;
+  if (!aligned16(q_row)) return TE_ERR_ALIGN;
+  NormArgs a = norm_args(x, rows, cols, residual, gamma, eps, y, res_out, rsigma);
+  a.q = q_row;
+  a.scale = scale;
+  a.e5m2 = fmt == TE_E5M2;
+  a.amax = reinterpret_cast<unsigned int*>(amax_out);
+  a.scale_inv = scale_inv_out;
+  if (rows == 0 && !amax_out && !scale_inv_out) return TE_OK;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return in_dtype == TE_BF16 ? launch_norm<__nv_bfloat16, false>(a, st) : launch_norm<float, false>(a, st);
+}
+
+te_status te_rmsnorm_mxfp8(const void* x, te_dtype in_dtype, int64_t rows, int64_t cols, const void* residual,
+                           const float* gamma, float eps, uint8_t* q_row, uint8_t* s_row, void* y, void* res_out,
+                           float* rsigma, void* stream) {
+  te_status s = check_norm(x, in_dtype, rows, cols, gamma, eps, residual, res_out, y);
+  if (s != TE_OK) return s;
+  if (cols % 32) return TE_ERR_SHAPE;
+  if (rows == 0) return TE_OK;
+  if (q_row == nullptr || s_row == nullptr) return TE_ERR_NULL;
+  if (!aligned16(q_row) || !aligned16(s_row)) return TE_ERR_ALIGN;
+  NormArgs a = norm_args(x, rows, cols, residual, gamma, eps, y, res_out, rsigma);
+  a.q = q_row;
+  a.s_row = s_row;
+  a.kpad = (cols / 32 + 3) / 4 * 4;
+  a.rpad = (rows + 127) / 128 * 128;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return in_dtype == TE_BF16 ? launch_norm<__nv_bfloat16, true>(a, st) : launch_norm<float, true>(a, st);
+}
+
+size_t te_rmsnorm_bwd_workspace_bytes(int64_t rows, int64_t cols) {
+  if (rows <= 0 || cols <= 0) return 0;
+  return static_cast<size_t>(rows < kMaxPartials ? rows : kMaxPartials) * static_cast<size_t>(cols) * sizeof(float);
+}
+
+te_status te_rmsnorm_bwd(const void* dy, const void* s, te_dtype in_dtype, int64_t rows, int64_t cols,
+                         const float* gamma, const float* rsigma, const void* dres, void* dx, float* dgamma,
+                         float* workspace, size_t workspace_bytes, void* stream) {
+  if (in_dtype != TE_BF16 && in_dtype != TE_F32) return TE_ERR_DTYPE;
+  if (rows < 0 || cols <= 0 || cols % 16 || cols > kMaxCols || rows > (int64_t(1) << 31)) return TE_ERR_SHAPE;
+  if (gamma == nullptr || dgamma == nullptr) return TE_ERR_NULL;
+  if (rows > 0 && (!dy || !s || !rsigma || !dx || !workspace)) return TE_ERR_NULL;
+  if (workspace_bytes < te_rmsnorm_bwd_workspace_bytes(rows, cols)) return TE_ERR_SHAPE;
+  if (!aligned16(dy) || !aligned16(s) || !aligned16(gamma) || !aligned16(dres) || !aligned16(dx) ||
+      !aligned16(workspace))
+    return TE_ERR_ALIGN;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (rows == 0) {
+    if (cudaMemsetAsync(dgamma, 0, static_cast<size_t>(cols) * sizeof(float), st) != cudaSuccess)
+      return record_cuda(cudaGetLastError());
+    return TE_OK;
+  }
+  NormBwdArgs a = {static_cast<const __nv_bfloat16*>(dy), s, dres, gamma, rsigma, rows, cols, dx, workspace};
+  const int wpr = warps_per_row(cols);
+  const int grid = walk_grid(rows, wpr);
+  if (in_dtype == TE_BF16) launch_norm_bwd<__nv_bfloat16>(a, wpr, grid, st);
+  else launch_norm_bwd<float>(a, wpr, grid, st);
+  count_launch();
+  te_status st1 = launch_status();
+  if (st1 != TE_OK) return st1;
+  dgamma_kernel<<<static_cast<unsigned>((cols + 31) / 32), 256, 0, st>>>(workspace, grid, cols, dgamma);
+  count_launch();
+  return launch_status();
+}
+
+}  // extern "C"

@@ -17,6 +17,7 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "convert.cuh"
 
 namespace te {
 namespace {
@@ -25,16 +26,6 @@ constexpr int kThreads = 256;
 
 // ---- format conversions (hardware cvt, round-to-nearest-even, satfinite) --------------
 
-__device__ __forceinline__ uint32_t cvt_e4m3x2(float lo, float hi) {
-  uint16_t d;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
-  return d;
-}
-__device__ __forceinline__ uint32_t cvt_e5m2x2(float lo, float hi) {
-  uint16_t d;
-  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
-  return d;
-}
 // Two E2M1 codes: `lo` in bits 0-3, `hi` in bits 4-7.
 __device__ __forceinline__ uint32_t cvt_e2m1x2(float lo, float hi) {
   uint32_t d;
@@ -679,17 +670,6 @@ __device__ __forceinline__ float current_scale(float a, float fmax) {
   const float s = __fdiv_rn(fmax, a);
   return isfinite(s) ? s : 1.0f;
 }
-
-// Shared exponent of an MXFP8 block: clamp(floor(log2 amax) - 8, -127, 127); -127 for a zero block.
-__device__ __forceinline__ int mx_exponent(float amax) {
-  const uint32_t b = __float_as_uint(amax);
-  if (b == 0) return -127;
-  const uint32_t ef = b >> 23;
-  int e = (ef == 0) ? (31 - __clz(static_cast<int>(b))) - 149 : static_cast<int>(ef) - 127;
-  e -= 8;
-  return max(-127, min(127, e));
-}
-__device__ __forceinline__ float mx_mult(int E) { return __uint_as_float(static_cast<uint32_t>(127 - E) << 23); }
 
 __device__ __forceinline__ float nv_senc(float A) {
   if (!(A > 0.0f)) return 1.0f;

@@ -18,10 +18,11 @@ Modules
   quantize  -- per-tensor FP8, MXFP8 and NVFP4 quantizers (RHT, SR, 2D)
   gemm      -- fp64 GEMM over dequantized operands, epilogue, Wgrad accumulation
   layernorm -- LayerNorm of the rows (the step before the QKV / MLP-up Fprop)
+  rmsnorm   -- root-mean-square norm with the residual's addition, and its gradient
 
 Every function is pinned by a ``-m "not gpu"`` test in ``tests/test_oracle_*``
 to a closed form, a brute-force check, a hand-worked table or an independent
 second implementation.  Parity status per function is listed in each module's
 docstring; none is unpinned.
 """
-from . import formats, philox, recipes, quantize, gemm, layernorm  # noqa: F401
+from . import formats, philox, recipes, quantize, gemm, layernorm, rmsnorm  # noqa: F401
