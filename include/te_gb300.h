@@ -327,6 +327,66 @@ te_status te_gemm_nvfp4(const uint8_t* A, const uint8_t* sA, const float* gA, co
                         const uint8_t* sB, const float* gB, const float* bias, void* D,
                         te_dtype out_dtype, int accumulate, int64_t M, int64_t N, int64_t K, void* stream);
 
+/* ---- gated feed-forward projections ---------------------------------------------
+ * The first half of a gated feed-forward block (SwiGLU / GEGLU), both projections, the
+ * activation and the product in one kernel:
+ *   g = x Wg^T, u = x Wu^T, h = act(g) * u
+ * x [T, K] (T tokens, any number); w [2 F, K]: the gate's F rows, then the up projection's;
+ * both contraction-major.  act: TE_ACT_SILU, g sigmoid(g); TE_ACT_GELU, the tanh form
+ * g/2 (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))).  fp32 accumulation; g, u and h stay fp32
+ * until each output is rounded once.  Outputs, each nullable, one at least:
+ *   h  bf16 [T, F];   gu bf16 [T, 2 F]: g, then u -- what the backward pass keeps.
+ * K % 16 == 0 and F % 16 == 0 (BF16, FP8); K % 32 == 0 and F % 128 == 0 (MXFP8, NVFP4: the
+ * two halves of w start at whole 128-row groups of the scale layout).  T = 0 is a no-op but
+ * for the amax and 1 / scale. */
+enum { TE_ACT_SILU = 0, TE_ACT_GELU = 1 };
+
+te_status te_gated_gemm_bf16(const void* x, const void* w, int act, void* h, void* gu, int64_t T, int64_t K, int64_t F,
+                             void* stream);
+
+/* x, w per-tensor scaled FP8, as te_gemm_fp8.  q_h (nullable) [T, F] = h_fmt(fl32(h * *h_scale)),
+ * saturating, the down projection's operand under DelayedScaling; with it h_amax (nullable) =
+ * max |h| in fp32 (NaN if an h is NaN) and h_scale_inv (nullable) = fl32(1 / *h_scale). */
+te_status te_gated_gemm_fp8(const uint8_t* x, te_dtype fx, const uint8_t* w, te_dtype fw, const float* x_scale_inv,
+                            const float* w_scale_inv, int act, void* h, void* gu, uint8_t* q_h, te_dtype h_fmt,
+                            const float* h_scale, float* h_amax, float* h_scale_inv, int64_t T, int64_t K, int64_t F,
+                            void* stream);
+
+/* MXFP8 operands, as te_gemm_mxfp8 (sw: scales of [2 F, K/32]).  q_h [T, F], s_h (nullable as a
+ * pair): h as te_quantize_mxfp8 writes a row copy, padding zero. */
+te_status te_gated_gemm_mxfp8(const uint8_t* x, te_dtype fx, const uint8_t* sx, const uint8_t* w, te_dtype fw,
+                              const uint8_t* sw, int act, void* h, void* gu, uint8_t* q_h, uint8_t* s_h, int64_t T,
+                              int64_t K, int64_t F, void* stream);
+
+/* NVFP4 operands, as te_gemm_nvfp4 (h in NVFP4 needs h's amax first: te_quantize_nvfp4). */
+te_status te_gated_gemm_nvfp4(const uint8_t* x, const uint8_t* sx, const float* gx, const uint8_t* w, const uint8_t* sw,
+                              const float* gw, int act, void* h, void* gu, int64_t T, int64_t K, int64_t F,
+                              void* stream);
+
+/* Backward: from dy [T, N], the gradient of y = h W2^T (W2 [N, F], the down projection), and the
+ * forward pass's gu, in one kernel:
+ *   dh = dy W2;  dg = dh u act'(g);  du = dh act(g);   dgu bf16 [T, 2 F]: dg, then du
+ * dh stays fp32.  dgu may be gu itself.  The 8- and 4-bit forms take dy's row copy [T, N] and W2's
+ * col copy [F, N] with their scales (N % 16 == 0 for FP8, % 32 for MXFP8 and NVFP4; F % 16 == 0);
+ * dx and dw follow by te_gemm_* on dgu's quantized copies. */
+te_status te_gated_dgrad_fp8(const uint8_t* dy, te_dtype fd, const uint8_t* w2, te_dtype fw, const float* dy_scale_inv,
+                             const float* w2_scale_inv, const void* gu, int act, void* dgu, int64_t T, int64_t F,
+                             int64_t N, void* stream);
+te_status te_gated_dgrad_mxfp8(const uint8_t* dy, te_dtype fd, const uint8_t* sd, const uint8_t* w2, te_dtype fw,
+                               const uint8_t* sw, const void* gu, int act, void* dgu, int64_t T, int64_t F, int64_t N,
+                               void* stream);
+te_status te_gated_dgrad_nvfp4(const uint8_t* dy, const uint8_t* sd, const float* gd, const uint8_t* w2,
+                               const uint8_t* sw, const float* gw, const void* gu, int act, void* dgu, int64_t T,
+                               int64_t F, int64_t N, void* stream);
+
+/* The whole backward pass in BF16, for any number of tokens: dgu as above from dy [T, N] and
+ * w2 [N, F], then (each nullable) dx bf16 [T, K] = dgu w and dw [2 F, K] = dgu^T x (dw_dtype
+ * TE_BF16 or TE_F32; accumulate = 1 with TE_F32: dw += dgu^T x).  w is read for dx, x for dw.
+ * K, F, N multiples of 16.  T = 0: dw = 0 (kept with accumulate). */
+te_status te_gated_bwd_bf16(const void* x, const void* w, const void* w2, const void* dy, const void* gu, int act,
+                            void* dgu, void* dx, void* dw, te_dtype dw_dtype, int accumulate, int64_t T, int64_t K,
+                            int64_t F, int64_t N, void* stream);
+
 /* ---- host helpers ------------------------------------------------------------------ */
 
 /* Bytes of the block-scale tensor of a quantized copy with `rows` rows of `cols`

@@ -21,6 +21,8 @@ F32, BF16, E4M3, E5M2, E2M1, E8M0, UE4M3 = range(7)
 # NVFP4 flags
 NVFP4_2D, NVFP4_RHT_COL, NVFP4_SR = 1, 2, 4
 ALGO_MAX, ALGO_MOST_RECENT = 0, 1
+# gated activations
+ACT_SILU, ACT_GELU = 0, 1
 # te_layout
 K_MAJOR, MN_MAJOR = 0, 1
 
@@ -59,6 +61,16 @@ SIGNATURES = {
     "te_gemm_fp8": (_st, [_vp, _int, _vp, _int, _vp, _vp, _vp, _vp, _int, _int, _i64, _i64, _i64, _vp]),
     "te_gemm_mxfp8": (_st, [_vp, _int, _vp, _vp, _int, _vp, _vp, _vp, _int, _int, _i64, _i64, _i64, _vp]),
     "te_gemm_nvfp4": (_st, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _int, _int, _i64, _i64, _i64, _vp]),
+    "te_gated_gemm_bf16": (_st, [_vp, _vp, _int, _vp, _vp, _i64, _i64, _i64, _vp]),
+    "te_gated_gemm_fp8": (_st, [_vp, _int, _vp, _int, _vp, _vp, _int, _vp, _vp, _vp, _int, _vp, _vp, _vp, _i64, _i64,
+                                _i64, _vp]),
+    "te_gated_gemm_mxfp8": (_st, [_vp, _int, _vp, _vp, _int, _vp, _int, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp]),
+    "te_gated_gemm_nvfp4": (_st, [_vp, _vp, _vp, _vp, _vp, _vp, _int, _vp, _vp, _i64, _i64, _i64, _vp]),
+    "te_gated_dgrad_fp8": (_st, [_vp, _int, _vp, _int, _vp, _vp, _vp, _int, _vp, _i64, _i64, _i64, _vp]),
+    "te_gated_dgrad_mxfp8": (_st, [_vp, _int, _vp, _vp, _int, _vp, _vp, _int, _vp, _i64, _i64, _i64, _vp]),
+    "te_gated_dgrad_nvfp4": (_st, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _int, _vp, _i64, _i64, _i64, _vp]),
+    "te_gated_bwd_bf16": (_st, [_vp, _vp, _vp, _vp, _vp, _int, _vp, _vp, _vp, _int, _int, _i64, _i64, _i64, _i64,
+                                _vp]),
     "te_scale_bytes": (ctypes.c_size_t, [_int, _i64, _i64]),
     "te_scale_unswizzle": (_st, [_int, _i64, _i64, _vp, _vp]),
     "te_status_str": (ctypes.c_char_p, [_int]),
@@ -314,6 +326,126 @@ def te_gemm_nvfp4(A, sA, gA, B, sB, gB, D, bias=None, accumulate: int = 0, strea
     _check("te_gemm_nvfp4", lib().te_gemm_nvfp4(_ptr(A), _ptr(sA), _ptr(gA), _ptr(B), _ptr(sB), _ptr(gB),
                                                 _ptr(bias), _ptr(D), _out_dtype(D), int(accumulate), M, N, 2 * Kh,
                                                 _stream(stream)))
+
+
+# ---- gated feed-forward projections: w [2 F, K] holds the gate's rows, then the up projection's --------
+
+def _gated_shape(fn, x, w, packed: int = 1):
+    """(T, K, F) of x [T, K / packed] and w [2 F, K / packed]."""
+    if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1] or w.shape[0] % 2:
+        raise ValueError(f"{fn}: x {tuple(x.shape)} and w {tuple(w.shape)} are not [T, K] and [2 F, K]")
+    return x.shape[0], x.shape[1] * packed, w.shape[0] // 2
+
+
+def te_gated_gemm_bf16(x, w, act: int, h=None, gu=None, stream=None):
+    """h = act(x Wg^T) * (x Wu^T) in bf16 and / or the pre-activations gu = [g, u]."""
+    import torch
+    fn, bf = "te_gated_gemm_bf16", torch.bfloat16
+    T, K, F = _gated_shape(fn, x, w)
+    _check(fn, lib().te_gated_gemm_bf16(
+        _need(fn, "x", x, bf, (T, K)), _need(fn, "w", w, bf, (2 * F, K)), act, _need(fn, "h", h, bf, (T, F), True),
+        _need(fn, "gu", gu, bf, (T, 2 * F), True), T, K, F, _stream(stream)))
+
+
+def te_gated_gemm_fp8(x, fx: int, w, fw: int, x_scale_inv, w_scale_inv, act: int, h=None, gu=None, q_h=None,
+                      h_fmt: int = E4M3, h_scale=None, h_amax=None, h_scale_inv=None, stream=None):
+    """te_gated_gemm_bf16 on per-tensor scaled FP8 operands; q_h is h in FP8 for the down projection."""
+    import torch
+    fn, bf, u8, f32 = "te_gated_gemm_fp8", torch.bfloat16, torch.uint8, torch.float32
+    T, K, F = _gated_shape(fn, x, w)
+    _check(fn, lib().te_gated_gemm_fp8(
+        _need(fn, "x", x, u8, (T, K)), fx, _need(fn, "w", w, u8, (2 * F, K)), fw,
+        _need(fn, "x_scale_inv", x_scale_inv, f32, 1), _need(fn, "w_scale_inv", w_scale_inv, f32, 1), act,
+        _need(fn, "h", h, bf, (T, F), True), _need(fn, "gu", gu, bf, (T, 2 * F), True),
+        _need(fn, "q_h", q_h, u8, (T, F), True), h_fmt, _need(fn, "h_scale", h_scale, f32, 1, True),
+        _need(fn, "h_amax", h_amax, f32, 1, True), _need(fn, "h_scale_inv", h_scale_inv, f32, 1, True), T, K, F,
+        _stream(stream)))
+
+
+def te_gated_gemm_mxfp8(x, sx, w, sw, act: int, h=None, gu=None, q_h=None, s_h=None, fx: int = E4M3, fw: int = E4M3,
+                        stream=None):
+    """te_gated_gemm_bf16 on MXFP8 operands; q_h, s_h are h in MXFP8 for the down projection."""
+    import torch
+    fn, bf, u8 = "te_gated_gemm_mxfp8", torch.bfloat16, torch.uint8
+    T, K, F = _gated_shape(fn, x, w)
+    _check(fn, lib().te_gated_gemm_mxfp8(
+        _need(fn, "x", x, u8, (T, K)), fx, _need(fn, "sx", sx, u8, te_scale_bytes(E8M0, T, K)),
+        _need(fn, "w", w, u8, (2 * F, K)), fw, _need(fn, "sw", sw, u8, te_scale_bytes(E8M0, 2 * F, K)), act,
+        _need(fn, "h", h, bf, (T, F), True), _need(fn, "gu", gu, bf, (T, 2 * F), True),
+        _need(fn, "q_h", q_h, u8, (T, F), True), _need(fn, "s_h", s_h, u8, te_scale_bytes(E8M0, T, F), True), T, K, F,
+        _stream(stream)))
+
+
+def te_gated_gemm_nvfp4(x, sx, gx, w, sw, gw, act: int, h=None, gu=None, stream=None):
+    """te_gated_gemm_bf16 on NVFP4 operands (packed codes, block scales, tensor scales)."""
+    import torch
+    fn, bf, u8, f32 = "te_gated_gemm_nvfp4", torch.bfloat16, torch.uint8, torch.float32
+    T, K, F = _gated_shape(fn, x, w, 2)
+    _check(fn, lib().te_gated_gemm_nvfp4(
+        _need(fn, "x", x, u8, (T, K // 2)), _need(fn, "sx", sx, u8, te_scale_bytes(UE4M3, T, K)),
+        _need(fn, "gx", gx, f32, 1), _need(fn, "w", w, u8, (2 * F, K // 2)),
+        _need(fn, "sw", sw, u8, te_scale_bytes(UE4M3, 2 * F, K)), _need(fn, "gw", gw, f32, 1), act,
+        _need(fn, "h", h, bf, (T, F), True), _need(fn, "gu", gu, bf, (T, 2 * F), True), T, K, F, _stream(stream)))
+
+
+def _dgrad_shape(fn, dy, w2, gu, dgu, packed: int = 1):
+    """(T, F, N) of dy [T, N / packed] and W2's col copy [F, N / packed], and the pointers of gu and dgu."""
+    import torch
+    if dy.dim() != 2 or w2.dim() != 2 or dy.shape[1] != w2.shape[1]:
+        raise ValueError(f"{fn}: dy {tuple(dy.shape)} and w2 {tuple(w2.shape)} are not [T, N] and [F, N]")
+    T, F = dy.shape[0], w2.shape[0]
+    return (T, F, dy.shape[1] * packed, _need(fn, "gu", gu, torch.bfloat16, (T, 2 * F)),
+            _need(fn, "dgu", dgu, torch.bfloat16, (T, 2 * F)))
+
+
+def te_gated_dgrad_fp8(dy, fd: int, w2, fw: int, dy_scale_inv, w2_scale_inv, gu, act: int, dgu, stream=None):
+    """Gradients of the pre-activations from dy's row copy [T, N] and W2's col copy [F, N] in FP8."""
+    import torch
+    fn, u8, f32 = "te_gated_dgrad_fp8", torch.uint8, torch.float32
+    T, F, N, pgu, pdgu = _dgrad_shape(fn, dy, w2, gu, dgu)
+    _check(fn, lib().te_gated_dgrad_fp8(
+        _need(fn, "dy", dy, u8, (T, N)), fd, _need(fn, "w2", w2, u8, (F, N)), fw,
+        _need(fn, "dy_scale_inv", dy_scale_inv, f32, 1), _need(fn, "w2_scale_inv", w2_scale_inv, f32, 1), pgu, act, pdgu,
+        T, F, N, _stream(stream)))
+
+
+def te_gated_dgrad_mxfp8(dy, sd, w2, sw, gu, act: int, dgu, fd: int = E4M3, fw: int = E4M3, stream=None):
+    """te_gated_dgrad_fp8 on MXFP8 copies."""
+    import torch
+    fn, u8 = "te_gated_dgrad_mxfp8", torch.uint8
+    T, F, N, pgu, pdgu = _dgrad_shape(fn, dy, w2, gu, dgu)
+    _check(fn, lib().te_gated_dgrad_mxfp8(
+        _need(fn, "dy", dy, u8, (T, N)), fd, _need(fn, "sd", sd, u8, te_scale_bytes(E8M0, T, N)),
+        _need(fn, "w2", w2, u8, (F, N)), fw, _need(fn, "sw", sw, u8, te_scale_bytes(E8M0, F, N)), pgu, act, pdgu, T, F, N,
+        _stream(stream)))
+
+
+def te_gated_dgrad_nvfp4(dy, sd, gd, w2, sw, gw, gu, act: int, dgu, stream=None):
+    """te_gated_dgrad_fp8 on NVFP4 copies."""
+    import torch
+    fn, u8, f32 = "te_gated_dgrad_nvfp4", torch.uint8, torch.float32
+    T, F, N, pgu, pdgu = _dgrad_shape(fn, dy, w2, gu, dgu, 2)
+    _check(fn, lib().te_gated_dgrad_nvfp4(
+        _need(fn, "dy", dy, u8, (T, N // 2)), _need(fn, "sd", sd, u8, te_scale_bytes(UE4M3, T, N)),
+        _need(fn, "gd", gd, f32, 1), _need(fn, "w2", w2, u8, (F, N // 2)),
+        _need(fn, "sw", sw, u8, te_scale_bytes(UE4M3, F, N)), _need(fn, "gw", gw, f32, 1), pgu, act, pdgu, T, F, N,
+        _stream(stream)))
+
+
+def te_gated_bwd_bf16(x, w, w2, dy, gu, act: int, dgu, dx=None, dw=None, accumulate: int = 0, stream=None):
+    """The BF16 backward pass: dgu from dy [T, N] and w2 [N, F], then dx = dgu w and dw (+)= dgu^T x."""
+    import torch
+    fn, bf = "te_gated_bwd_bf16", torch.bfloat16
+    T, K, F = _gated_shape(fn, x, w)
+    if dy.dim() != 2:
+        raise ValueError(f"{fn}: dy has shape {tuple(dy.shape)}, expected [T, N]")
+    N = dy.shape[1]
+    _check(fn, lib().te_gated_bwd_bf16(
+        _need(fn, "x", x, bf, (T, K)), _need(fn, "w", w, bf, (2 * F, K)), _need(fn, "w2", w2, bf, (N, F)),
+        _need(fn, "dy", dy, bf, (T, N)), _need(fn, "gu", gu, bf, (T, 2 * F)), act,
+        _need(fn, "dgu", dgu, bf, (T, 2 * F)), _need(fn, "dx", dx, bf, (T, K), True),
+        _need(fn, "dw", dw, (bf, torch.float32), (2 * F, K), True), BF16 if dw is None else _out_dtype(dw),
+        int(accumulate), T, K, F, N, _stream(stream)))
 
 
 def te_scale_bytes(scale_fmt: int, rows: int, cols: int) -> int:

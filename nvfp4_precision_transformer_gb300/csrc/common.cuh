@@ -46,6 +46,16 @@ te_status make_tmap_2d_f32(CUtensorMap* map, const float* base, uint64_t cols, u
 te_status make_tmap_2d_boxswz(CUtensorMap* map, const void* base, uint64_t row_bytes, uint64_t rows,
                               uint32_t box_inner_bytes, uint32_t box_rows);
 
+// Byte matrix [rows, width_bytes] with rows `stride_bytes` apart, boxes of 32 rows x 64 bytes under
+// the 64-byte swizzle (the gated epilogues' boxes).
+te_status make_tmap_2d_view64(CUtensorMap* map, const void* base, uint64_t width_bytes, uint64_t stride_bytes,
+                              uint64_t rows);
+
+// D [M, N] = A B^T in BF16, as te_gemm_bf16 but with any M where it is not contiguous in an operand,
+// and any K where both operands are stored MN-major (no checks: the caller's).
+te_status gemm_bf16_tokens(const void* A, int a_mn, const void* B, int b_mn, void* D, te_dtype out, int accumulate,
+                           int64_t M, int64_t N, int64_t K, cudaStream_t st);
+
 // Byte offset of logical scale (r, j) in the tensor-core block-scale layout;
 // kpad = number of scale columns after padding (multiple of 4).
 __host__ __device__ inline uint64_t scale_offset(uint64_t r, uint64_t j, uint64_t kpad) {
@@ -199,7 +209,8 @@ __device__ __forceinline__ void tma_reduce_add_2d(const CUtensorMap* map, const 
                : "memory");
 }
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-// Wait until the shared-memory source of every committed bulk store has been read.
+// Wait until the shared-memory source of every committed bulk store (every one but the latest) has been read.
+__device__ __forceinline__ void bulk_wait_read1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_read0() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 // Wait until every committed bulk store has completed.
 __device__ __forceinline__ void bulk_wait0() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }

@@ -79,7 +79,7 @@ int num_sms() {
 
 static te_status encode_2d_typed(CUtensorMap* map, const void* base, CUtensorMapDataType dtype, uint64_t elem_bytes,
                                  uint64_t cols, uint64_t rows, uint32_t box_inner, uint32_t box_rows,
-                                 CUtensorMapSwizzle swz) {
+                                 CUtensorMapSwizzle swz, uint64_t stride_bytes = 0) {
   {
     std::lock_guard<std::mutex> lk(g_mu);
     if (g_encode == nullptr) {
@@ -93,7 +93,7 @@ static te_status encode_2d_typed(CUtensorMap* map, const void* base, CUtensorMap
     }
   }
   cuuint64_t dims[2] = {cols, rows};
-  cuuint64_t strides[1] = {cols * elem_bytes};
+  cuuint64_t strides[1] = {stride_bytes ? stride_bytes : cols * elem_bytes};
   cuuint32_t box[2] = {box_inner, box_rows};
   cuuint32_t estr[2] = {1u, 1u};
   CUresult r = g_encode(map, dtype, 2, const_cast<void*>(base), dims, strides, box, estr,
@@ -129,6 +129,12 @@ te_status make_tmap_2d_boxswz(CUtensorMap* map, const void* base, uint64_t row_b
                                  : box_inner_bytes == 32 ? CU_TENSOR_MAP_SWIZZLE_32B
                                                          : CU_TENSOR_MAP_SWIZZLE_NONE;
   return encode_2d(map, base, row_bytes, rows, box_inner_bytes, box_rows, swz);
+}
+
+te_status make_tmap_2d_view64(CUtensorMap* map, const void* base, uint64_t width_bytes, uint64_t stride_bytes,
+                              uint64_t rows) {
+  return encode_2d_typed(map, base, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, width_bytes, rows, 64u, 32u,
+                         CU_TENSOR_MAP_SWIZZLE_64B, stride_bytes);
 }
 
 }  // namespace te

@@ -19,10 +19,11 @@ Modules
   gemm      -- fp64 GEMM over dequantized operands, epilogue, Wgrad accumulation
   layernorm -- LayerNorm of the rows (the step before the QKV / MLP-up Fprop)
   rmsnorm   -- root-mean-square norm with the residual's addition, and its gradient
+  gated     -- gated feed-forward projections (SwiGLU / GEGLU) and their gradient
 
 Every function is pinned by a ``-m "not gpu"`` test in ``tests/test_oracle_*``
 to a closed form, a brute-force check, a hand-worked table or an independent
 second implementation.  Parity status per function is listed in each module's
 docstring; none is unpinned.
 """
-from . import formats, philox, recipes, quantize, gemm, layernorm, rmsnorm  # noqa: F401
+from . import formats, philox, recipes, quantize, gemm, layernorm, rmsnorm, gated  # noqa: F401
