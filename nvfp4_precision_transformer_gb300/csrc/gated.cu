@@ -1,6 +1,6 @@
 // Entry points of the gated feed-forward projections: h = act(x Wg^T) * (x Wu^T) in one kernel, and
 // its backward pass.  The kernels are gemm_kernel with the gated epilogues (gemm.cuh).
-#include "gemm.cuh"
+#include "gated_decode.cuh"
 
 namespace te {
 namespace {
@@ -30,9 +30,8 @@ te_status halves(CUtensorMap* lo, CUtensorMap* hi, const void* p, int64_t T, int
                              static_cast<uint64_t>(F) * 4, static_cast<uint64_t>(T));
 }
 
-// Checks the bf16 outputs and describes them.
+// Describes the bf16 outputs.
 te_status bf16_outputs(GatedArgs* ep, void* h, void* gu, int64_t T, int64_t F, int act) {
-  if (!aligned16(h) || !aligned16(gu)) return TE_ERR_ALIGN;
   ep->F = static_cast<int>(F);
   ep->act = act;
   ep->has_h = h != nullptr;
@@ -72,6 +71,14 @@ te_status te_gated_gemm_bf16(const void* x, const void* w, int act, void* h, voi
   if (s != TE_OK || T == 0) return s;
   if (!h && !gu) return TE_ERR_NULL;
   if ((s = check_operands(x, w)) != TE_OK) return s;
+  if (!aligned16(h) || !aligned16(gu)) return TE_ERR_ALIGN;
+  if (decodes(T, K, 2)) {
+    const DecodeArgs a = {static_cast<const uint8_t*>(x), static_cast<const uint8_t*>(w), static_cast<int>(T),
+                          static_cast<int>(K), static_cast<int>(F), act, nullptr, nullptr,
+                          static_cast<__nv_bfloat16*>(h), static_cast<__nv_bfloat16*>(gu), nullptr, nullptr, 0, nullptr,
+                          nullptr};
+    return launch_decode<kDecBF16, kDecBF16>(a, static_cast<cudaStream_t>(stream));
+  }
   GatedArgs ep = {};
   if ((s = bf16_outputs(&ep, h, gu, T, F, act)) != TE_OK) return s;
   return launch_gemm<kBF16, 2, kGated>(x, w, K * 2, nullptr, nullptr, 0, nullptr, nullptr, nullptr, nullptr, TE_BF16, 0,
@@ -97,7 +104,16 @@ te_status te_gated_gemm_fp8(const uint8_t* x, te_dtype fx, const uint8_t* w, te_
   if (q_h ? !h_scale : (h_amax || h_scale_inv)) return TE_ERR_NULL;   // the amax and 1 / scale go with q_h
   if (!x_scale_inv || !w_scale_inv) return TE_ERR_NULL;
   if ((s = check_operands(x, w)) != TE_OK) return s;
-  if (!aligned16(q_h)) return TE_ERR_ALIGN;
+  if (!aligned16(h) || !aligned16(gu) || !aligned16(q_h)) return TE_ERR_ALIGN;
+  if (h_amax && cudaMemsetAsync(h_amax, 0, sizeof(float), st) != cudaSuccess) return record_cuda(cudaGetLastError());
+  if (decodes(T, K, 1)) {
+    const DecodeArgs a = {x, w, static_cast<int>(T), static_cast<int>(K), static_cast<int>(F), act,
+                          x_scale_inv, w_scale_inv, static_cast<__nv_bfloat16*>(h), static_cast<__nv_bfloat16*>(gu), q_h,
+                          h_scale, h_fmt == TE_E5M2, reinterpret_cast<unsigned int*>(h_amax), h_scale_inv};
+    if (fw == TE_E4M3)
+      return fx == TE_E4M3 ? launch_decode<kDecE4M3, kDecE4M3>(a, st) : launch_decode<kDecE4M3, kDecE5M2>(a, st);
+    return fx == TE_E4M3 ? launch_decode<kDecE5M2, kDecE4M3>(a, st) : launch_decode<kDecE5M2, kDecE5M2>(a, st);
+  }
   GatedArgs ep = {};
   if ((s = bf16_outputs(&ep, h, gu, T, F, act)) != TE_OK) return s;
   if (q_h) {
@@ -108,7 +124,6 @@ te_status te_gated_gemm_fp8(const uint8_t* x, te_dtype fx, const uint8_t* w, te_
     ep.scale_inv = h_scale_inv;
     s = make_tmap_2d_view64(&ep.q, q_h, static_cast<uint64_t>(F), static_cast<uint64_t>(F), static_cast<uint64_t>(T));
     if (s != TE_OK) return s;
-    if (h_amax && cudaMemsetAsync(h_amax, 0, sizeof(float), st) != cudaSuccess) return record_cuda(cudaGetLastError());
   }
   return launch_gemm<kFP8, 2, kGated>(x, w, K, nullptr, nullptr, 0, x_scale_inv, w_scale_inv, nullptr, nullptr, TE_BF16,
                                       0, T, 2 * F, K, fp8_code(fx), fp8_code(fw), st, 0, 0, ep);
@@ -123,7 +138,7 @@ te_status te_gated_gemm_mxfp8(const uint8_t* x, te_dtype fx, const uint8_t* sx, 
   if ((!h && !gu && !q_h) || (q_h == nullptr) != (s_h == nullptr)) return TE_ERR_NULL;
   if ((s = check_operands(x, w)) != TE_OK) return s;
   if ((s = check_operands(sx, sw)) != TE_OK) return s;
-  if (!aligned16(q_h) || !aligned16(s_h)) return TE_ERR_ALIGN;
+  if (!aligned16(h) || !aligned16(gu) || !aligned16(q_h) || !aligned16(s_h)) return TE_ERR_ALIGN;
   GatedArgs ep = {};
   if ((s = bf16_outputs(&ep, h, gu, T, F, act)) != TE_OK) return s;
   if (q_h) {
@@ -147,6 +162,7 @@ te_status te_gated_gemm_nvfp4(const uint8_t* x, const uint8_t* sx, const float* 
   if ((!h && !gu) || !gx || !gw) return TE_ERR_NULL;
   if ((s = check_operands(x, w)) != TE_OK) return s;
   if ((s = check_operands(sx, sw)) != TE_OK) return s;
+  if (!aligned16(h) || !aligned16(gu)) return TE_ERR_ALIGN;
   GatedArgs ep = {};
   if ((s = bf16_outputs(&ep, h, gu, T, F, act)) != TE_OK) return s;
   return launch_gemm<kNVFP4, 2, kGated>(x, w, K / 2, sx, sw, (K / 16 + 15) / 16 * 4, gx, gw, nullptr, nullptr, TE_BF16,

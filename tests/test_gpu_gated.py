@@ -191,6 +191,32 @@ def test_several_tiles_per_cta(kind, outs):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,K,Fc", [(1, 4096, 2480), (8, 2064, 80), (9, 1040, 1232), (16, 4112, 32), (24, 4096, 48),
+                                    (32, 2096, 1248), (25, 4096, 32)])
+@pytest.mark.parametrize("kind,outs,fmt", [("bf16", ("h", "gu"), "e4m3"), ("fp8", ("h", "gu", "q"), "e4m3"),
+                                           ("fp8", ("q",), "e5m2")])
+def test_few_tokens(T, K, Fc, kind, outs, fmt):
+    """Long rows and more units of columns than SMs: the streaming kernel's steps and its prefetch
+    across units."""
+    _check_forward(kind, T, K, Fc, "gelu", outs, fmt)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [5, 200])
+@pytest.mark.parametrize("fx,fw", [("e4m3", "e5m2"), ("e5m2", "e4m3"), ("e5m2", "e5m2")])
+def test_fp8_operand_formats(T, fx, fw):
+    a, b = _inputs(T, 208, 144, 5)
+    x, w = Operand(a, "fp8", fx), Operand(b, "fp8", fw)
+    h = Out(T, 144)
+    te.te_gated_gemm_fp8(x.q, FMT[fx], w.q, FMT[fw], x.inv, w.inv, te.ACT_SILU, h=h.t)
+    torch.cuda.synchronize()
+    h64, g64, u64 = gated(x.v, w.v, "silu")
+    S = np.abs(x.v) @ np.abs(w.v).T * (212 * E23)
+    err = _sizes(g64, u64, S[:, :144], S[:, 144:], "silu")
+    assert np.all(np.abs(h.np() - h64) <= BF * (np.abs(h64) + err) + err)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T", [1, 40, 300])
 def test_special_values_stay_in_their_row(T):
     a, b = _inputs(T, 64, 160, 1)
