@@ -54,7 +54,7 @@ te_status make_tmap_2d_view64(CUtensorMap* map, const void* base, uint64_t width
 // D [M, N] = A B^T in BF16, as te_gemm_bf16 but with any M where it is not contiguous in an operand,
 // and any K where both operands are stored MN-major (no checks: the caller's).
 te_status gemm_bf16_tokens(const void* A, int a_mn, const void* B, int b_mn, void* D, te_dtype out, int accumulate,
-                           int64_t M, int64_t N, int64_t K, cudaStream_t st);
+                           int64_t M, int64_t N, int64_t K, cudaStream_t st, int pdl = 0);
 
 // Byte offset of logical scale (r, j) in the tensor-core block-scale layout;
 // kpad = number of scale columns after padding (multiple of 4).

@@ -234,12 +234,16 @@ te_status te_gated_bwd_bf16(const void* x, const void* w, const void* w2, const 
   if (dw && (s = check_operands(x, x)) != TE_OK) return s;
   GatedArgs ep = {};
   if ((s = dgrad_args(&ep, gu, dgu, T, F, act)) != TE_OK) return s;
-  // dh = dY W2 (W2 [N, F] read MN-major), dg and du in its epilogue
+  // dh = dY W2 (W2 [N, F] read MN-major), dg and du in its epilogue.  The next kernel is set up while
+  // this one drains, and dW, which reads the same dGU, runs beside dX wherever that leaves SMs idle
+  // (1001 tokens, K = N = 768, F = 2048: dX has 12 tiles for 76 pairs).
   s = launch_gemm<kBF16, 2, kDgrad>(dy, w2, N * 2, nullptr, nullptr, 0, nullptr, nullptr, nullptr, nullptr, TE_BF16, 0,
-                                    T, F, N, 1u, 1u, st, 0, 1, ep);
+                                    T, F, N, 1u, 1u, st, 0, 1, ep, (dx || dw) ? kPdlTrigger : 0);
   // dX = dGU W (W [2 F, K] MN-major);  dW = dGU^T X (both MN-major)
-  if (s == TE_OK && dx) s = gemm_bf16_tokens(dgu, 0, w, 1, dx, TE_BF16, 0, T, K, 2 * F, st);
-  if (s == TE_OK && dw) s = gemm_bf16_tokens(dgu, 1, x, 1, dw, dw_dtype, accumulate, 2 * F, K, T, st);
+  if (s == TE_OK && dx)
+    s = gemm_bf16_tokens(dgu, 0, w, 1, dx, TE_BF16, 0, T, K, 2 * F, st, kPdlWait | (dw ? kPdlTrigger : 0));
+  if (s == TE_OK && dw)
+    s = gemm_bf16_tokens(dgu, 1, x, 1, dw, dw_dtype, accumulate, 2 * F, K, T, st, dx ? kPdlWaitAtEnd : kPdlWait);
   return s;
 }
 

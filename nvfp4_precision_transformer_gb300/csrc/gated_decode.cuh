@@ -149,12 +149,13 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1) gated_decode_kernel(const D
         s.x += p.x, s.y += p.y, s.z += p.z, s.w += p.w;
       }
       const int f = unit * 8 + r;
+      const float2 g2 = __fmul2_rn(make_float2(s.x, s.y), both(alpha)), u2 = __fmul2_rn(make_float2(s.z, s.w), both(alpha));
+      const float2 h2 = __fmul2_rn(gate_act(g2, a.act), u2);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int64_t n = warp * 8 + 2 * t + j;
         if (n < a.T) {
-          const float g = (j ? s.y : s.x) * alpha, u = (j ? s.w : s.z) * alpha;
-          const float hv = gate_act(g, a.act) * u;
+          const float g = j ? g2.y : g2.x, u = j ? u2.y : u2.x, hv = j ? h2.y : h2.x;
           if (a.gu) {
             a.gu[n * 2 * a.F + f] = __float2bfloat16_rn(g);
             a.gu[n * 2 * a.F + a.F + f] = __float2bfloat16_rn(u);

@@ -126,6 +126,12 @@ struct Cfg {
   static_assert(kSmemTotal <= 232448, "shared memory budget");
 };
 
+// Programmatic dependent launch, for kernels that follow one another inside one call (bits of pdl):
+// the kernel waits for the one before it after its set-up; it lets the next one start once it has
+// itself begun (after that wait); it waits for the one before it only at its end, being independent
+// of its results, so that what follows in the stream finds both complete.
+constexpr int kPdlWait = 1, kPdlTrigger = 2, kPdlWaitAtEnd = 4;
+
 struct GemmArgs {
   int M, N, K;
   int k_tiles, m_tiles, n_tiles;
@@ -141,6 +147,7 @@ struct GemmArgs {
   int accumulate;       // 1: D (fp32) += result, by TMA reduce-add
   uint32_t idesc;
   int a_mn, b_mn;       // BF16 only: operand stored [K, M] / [K, N]
+  int pdl;              // programmatic dependent launch: see kPdl*
   int raster;           // 1: the smaller operand's tiles vary fastest (see tile_coords)
   int* err;
 };
@@ -267,6 +274,9 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, EPI>::kThreads, 1)
     }
   }
   __syncthreads();
+
+  if (args.pdl & kPdlWait) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (args.pdl & kPdlTrigger) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // Scale atoms j = j0, j0 + dj, ... of stage `st` (shared memory) -> its TMEM slot, one copy
   // per 512-byte atom, the A atom and the two B atoms of a k-step back to back (grouped by
@@ -629,6 +639,7 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, EPI>::kThreads, 1)
     if (lane == 0) dev::bulk_wait0();
   }
 
+  if (args.pdl & kPdlWaitAtEnd) asm volatile("griddepcontrol.wait;" ::: "memory");
   dev::tc_fence_before();
   __syncthreads();
   if (kPair) dev::cluster_sync();  // the leader's MMAs read the peer's shared memory until here
@@ -661,7 +672,7 @@ te_status launch_gemm(const void* A, const void* B, int64_t row_bytes, const uin
                       int64_t sf_katoms, const float* alpha_a, const float* alpha_b, const float* bias, void* D,
                       te_dtype out, int accumulate, int64_t M, int64_t N, int64_t K, uint32_t afmt, uint32_t bfmt,
                       cudaStream_t st, int a_mn = 0, int b_mn = 0,
-                      const typename EpiParam<EPI>::type& ep = typename EpiParam<EPI>::type()) {
+                      const typename EpiParam<EPI>::type& ep = typename EpiParam<EPI>::type(), int pdl = 0) {
   using C = Cfg<KIND, CG, EPI>;
   static bool attr_set[64] = {false};
   static int max_clusters[64] = {0};
@@ -669,7 +680,9 @@ te_status launch_gemm(const void* A, const void* B, int64_t row_bytes, const uin
   cudaGetDevice(&dev_id);
   if (dev_id < 0 || dev_id >= 64) return TE_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = CG;
   attr[0].val.clusterDim.y = 1;
@@ -745,6 +758,7 @@ te_status launch_gemm(const void* A, const void* B, int64_t row_bytes, const uin
   g.a_mn = a_mn;
   g.b_mn = b_mn;
   g.raster = (KIND != kBF16 && g.k_tiles >= 64 && g.m_tiles != g.n_tiles) ? 1 : 0;   // >= 8 KB of K per row
+  g.pdl = pdl;
   g.err = err;
   const int tiles = g.m_tiles * g.n_tiles;
   // The fewest CTA pairs that keep the number of waves: every pair runs the same number of
@@ -756,6 +770,7 @@ te_status launch_gemm(const void* A, const void* B, int64_t row_bytes, const uin
     units = (tiles + waves - 1) / waves;
   }
   cfg.gridDim = dim3(static_cast<unsigned>(CG * units), 1, 1);
+  cfg.numAttrs = (pdl & (kPdlWait | kPdlWaitAtEnd)) ? 2 : 1;
   if (cudaLaunchKernelEx(&cfg, gemm_kernel<KIND, CG, EPI>, ta, tb, td, tsa, tsb, g, ep) != cudaSuccess)
     return record_cuda(cudaGetLastError());
   count_launch();

@@ -6,8 +6,8 @@
 //             ds = rsigma * (p - xhat * mean(p * xhat)) (+ the residual stream's own gradient)
 //             dgamma = sum over the rows of dy * xhat
 //
-// Both are bound by HBM.  A row belongs to WPR warps (1 to 16: 1024 columns a warp), each lane
-// holding up to four chunks of eight columns in registers, so every tensor is read once; the
+// Both are bound by HBM.  A row belongs to WPR warps (1 to 16), each lane holding up to four (backward:
+// two) chunks of eight columns in registers, so every tensor is read once; the
 // row's sum is a butterfly over the lanes and one exchange through shared memory between the
 // row's warps.  Groups walk the rows with the grid's stride, and gamma comes from L1.  All sums
 // are fp32 in a fixed order, so results do not depend on timing.
@@ -239,9 +239,14 @@ struct NormBwdArgs {
   float* partial;   // [gridDim.x, cols]
 };
 
-template <typename T, int WPR>
+// Two chunks a lane and two CTAs per SM, with the next row in flight in bf16 (15872 x 4096: 87.7 us;
+// without it 105.1, four chunks 96.7, three CTAs 94.2 and, with it, spilled, 132.5).  In fp32 the
+// second row would take the registers of the second CTA's warps: 151 us without, 152 with it
+// (30000 x 768: 59.9 / 74.7), four chunks 217.
+template <typename T, int WPR, int CH>
 __global__ void __launch_bounds__(32 * cta_warps(WPR), WPR <= 8 ? 2 : 1) rmsnorm_bwd_kernel(const NormBwdArgs a) {
   constexpr int GR = cta_rows(WPR);
+  constexpr bool kAhead = sizeof(T) == 2 && CH == 2;   // the next row's loads before this row is reduced
   __shared__ float red[GR][2][WPR];
   extern __shared__ __align__(16) float cols_sum[];   // [GR - 1][cols]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -250,40 +255,50 @@ __global__ void __launch_bounds__(32 * cta_warps(WPR), WPR <= 8 ? 2 : 1) rmsnorm
   const int64_t step = static_cast<int64_t>(gridDim.x) * GR;
   const T* s = static_cast<const T*>(a.s);
   const T* dres = static_cast<const T*>(a.dres);
-  const int col0 = (wr * kCh * 32 + lane) * 8;
-  float2 dg[kCh][4];
+  const int col0 = (wr * CH * 32 + lane) * 8;
+  float2 dg[CH][4];
 #pragma unroll
-  for (int t = 0; t < kCh; ++t)
+  for (int t = 0; t < CH; ++t)
 #pragma unroll
     for (int i = 0; i < 4; ++i) dg[t][i] = make_float2(0.f, 0.f);
 
-  int turn = 0;
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * GR + grp; row < a.rows; row += step, turn ^= 1) {
-    Raw8<__nv_bfloat16> rd[kCh];
-    Raw8<T> rx[kCh], rr[kCh];
+  struct RowRegs {
+    Raw8<__nv_bfloat16> d[CH];
+    Raw8<T> x[CH], r[CH];
+    float rs;
+  };
+  auto load = [&](RowRegs& q, int64_t row) {
+    q.rs = row < a.rows ? a.rsigma[row] : 0.0f;
 #pragma unroll
-    for (int t = 0; t < kCh; ++t) {
+    for (int t = 0; t < CH; ++t) {
       const int col = col0 + 256 * t;
-      rd[t].zero();
-      rx[t].zero();
-      rr[t].zero();
-      if (col < C) {
-        rd[t].load(a.dy + row * C + col);
-        rx[t].load(s + row * C + col);
-        if (dres) rr[t].load(dres + row * C + col);
+      q.d[t].zero();
+      q.x[t].zero();
+      q.r[t].zero();
+      if (row < a.rows && col < C) {
+        q.d[t].load(a.dy + row * C + col);
+        q.x[t].load(s + row * C + col);
+        if (dres) q.r[t].load(dres + row * C + col);
       }
     }
-    const float rs = a.rsigma[row];
-    const float2 rs2 = make_float2(rs, rs);
+  };
+  RowRegs cur;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * GR + grp;
+  if (kAhead) load(cur, row);
+  for (int turn = 0; row < a.rows; row += step, turn ^= 1) {
+    RowRegs nxt;
+    if (kAhead) load(nxt, row + step);
+    else load(cur, row);
+    const float2 rs2 = make_float2(cur.rs, cur.rs);
     float2 dot = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int t = 0; t < kCh; ++t) {
+    for (int t = 0; t < CH; ++t) {
       const int col = col0 + 256 * t;
       float2 g[4] = {};
       if (col < C) ldg8(a.gamma + col, g);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float2 w = __fmul2_rn(rd[t].pair(i), __fmul2_rn(rx[t].pair(i), rs2));   // dy * xhat
+        const float2 w = __fmul2_rn(cur.d[t].pair(i), __fmul2_rn(cur.x[t].pair(i), rs2));   // dy * xhat
         dg[t][i] = __fadd2_rn(dg[t][i], w);
         dot = __ffma2_rn(w, g[i], dot);
       }
@@ -292,32 +307,34 @@ __global__ void __launch_bounds__(32 * cta_warps(WPR), WPR <= 8 ? 2 : 1) rmsnorm
     const float c = -__fdiv_rn(sum, static_cast<float>(C));
     const float2 c2 = make_float2(c, c);
 #pragma unroll
-    for (int t = 0; t < kCh; ++t) {
+    for (int t = 0; t < CH; ++t) {
       const int col = col0 + 256 * t;
       if (col >= C) break;
       float2 g[4], o[4];
       ldg8(a.gamma + col, g);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float2 p = __fmul2_rn(rd[t].pair(i), g[i]);
-        const float2 d = __ffma2_rn(__fmul2_rn(rx[t].pair(i), rs2), c2, p);
-        o[i] = __ffma2_rn(d, rs2, rr[t].pair(i));
+        const float2 p = __fmul2_rn(cur.d[t].pair(i), g[i]);
+        const float2 d = __ffma2_rn(__fmul2_rn(cur.x[t].pair(i), rs2), c2, p);
+        o[i] = __ffma2_rn(d, rs2, cur.r[t].pair(i));
       }
       store8(static_cast<T*>(a.dx) + row * C + col, o);
     }
+    if (kAhead) cur = nxt;
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // the CTA's column sums: the row groups in order
   if (GR > 1) {
     if (grp > 0) {
 #pragma unroll
-      for (int t = 0; t < kCh; ++t)
+      for (int t = 0; t < CH; ++t)
         if (col0 + 256 * t < C) store8(cols_sum + (grp - 1) * C + col0 + 256 * t, dg[t]);
     }
     __syncthreads();
     if (grp > 0) return;
     for (int k = 0; k < GR - 1; ++k)
 #pragma unroll
-      for (int t = 0; t < kCh; ++t) {
+      for (int t = 0; t < CH; ++t) {
         const int col = col0 + 256 * t;
         if (col >= C) break;
         const float4 u = *reinterpret_cast<const float4*>(cols_sum + k * C + col);
@@ -329,34 +346,39 @@ __global__ void __launch_bounds__(32 * cta_warps(WPR), WPR <= 8 ? 2 : 1) rmsnorm
       }
   }
 #pragma unroll
-  for (int t = 0; t < kCh; ++t)
+  for (int t = 0; t < CH; ++t)
     if (col0 + 256 * t < C) store8(a.partial + static_cast<int64_t>(blockIdx.x) * C + col0 + 256 * t, dg[t]);
 }
 
-// dgamma[c] = the sum of the partial rows in a fixed order: 32 columns x 8 row lanes a CTA.
-__global__ void __launch_bounds__(256) dgamma_kernel(const float* __restrict__ partial, int n, int64_t C,
-                                                     float* __restrict__ dgamma) {
-  __shared__ float part[8][32];
+// dgamma[c] = the sum of the partial rows in a fixed order: 32 columns x 32 row lanes a CTA, every
+// load of a lane in flight at once (304 rows x 4096: with 8 lanes 8 us, as much as it hid).
+__global__ void __launch_bounds__(1024) dgamma_kernel(const float* __restrict__ partial, int n, int64_t C,
+                                                      float* __restrict__ dgamma) {
+  __shared__ float part[32][33];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the partial sums are complete
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   float t = 0.0f;
   if (c < C) {
-#pragma unroll 8
-    for (int r = w; r < n; r += 8) t = __fadd_rn(t, partial[static_cast<int64_t>(r) * C + c]);
+    float v[16];   // n <= 512
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const int r = w + 32 * k;
+      v[k] = r < n ? partial[static_cast<int64_t>(r) * C + c] : 0.0f;
+    }
+#pragma unroll
+    for (int k = 0; k < 16; ++k) t = __fadd_rn(t, v[k]);
   }
   part[w][lane] = t;
   __syncthreads();
-  if (w == 0 && c < C) {
-#pragma unroll
-    for (int k = 1; k < 8; ++k) t = __fadd_rn(t, part[k][lane]);
-    dgamma[c] = t;
-  }
+  t = warp_sum(part[lane][w]);   // warp w: column w
+  if (lane == 0 && static_cast<int64_t>(blockIdx.x) * 32 + w < C) dgamma[static_cast<int64_t>(blockIdx.x) * 32 + w] = t;
 }
 
-// Warps per row: the fewest whose lanes hold `cols` columns.
-int warps_per_row(int64_t cols) {
+// Warps per row (at most 16): the fewest whose lanes hold `cols` columns in `ch` chunks each.
+int warps_per_row(int64_t cols, int ch) {
   int w = 1;
-  while (w * kWarpCols < cols) w *= 2;
+  while (w < 16 && w * 32 * 8 * ch < cols) w *= 2;
   return w;
 }
 
@@ -370,7 +392,7 @@ int walk_grid(int64_t rows, int wpr) {
 
 template <typename T, bool MX>
 te_status launch_norm(NormArgs& a, cudaStream_t st) {
-  const int wpr = warps_per_row(a.cols);
+  const int wpr = warps_per_row(a.cols, kCh);
   const int grid = walk_grid(a.rows, wpr);
   if (a.amax) {
     a.amax_whole = grid == 1;
@@ -391,11 +413,13 @@ template <typename T>
 void launch_norm_bwd(const NormBwdArgs& a, int wpr, int grid, cudaStream_t st) {
   const size_t smem = static_cast<size_t>(cta_rows(wpr) - 1) * static_cast<size_t>(a.cols) * sizeof(float);
   switch (wpr) {
-    case 1: rmsnorm_bwd_kernel<T, 1><<<grid, 256, smem, st>>>(a); break;
-    case 2: rmsnorm_bwd_kernel<T, 2><<<grid, 256, smem, st>>>(a); break;
-    case 4: rmsnorm_bwd_kernel<T, 4><<<grid, 256, smem, st>>>(a); break;
-    case 8: rmsnorm_bwd_kernel<T, 8><<<grid, 256, smem, st>>>(a); break;
-    default: rmsnorm_bwd_kernel<T, 16><<<grid, 512, smem, st>>>(a); break;
+    case 1: rmsnorm_bwd_kernel<T, 1, 2><<<grid, 256, smem, st>>>(a); break;
+    case 2: rmsnorm_bwd_kernel<T, 2, 2><<<grid, 256, smem, st>>>(a); break;
+    case 4: rmsnorm_bwd_kernel<T, 4, 2><<<grid, 256, smem, st>>>(a); break;
+    case 8: rmsnorm_bwd_kernel<T, 8, 2><<<grid, 256, smem, st>>>(a); break;
+    default:
+      if (a.cols <= 16 * 32 * 8 * 2) rmsnorm_bwd_kernel<T, 16, 2><<<grid, 512, smem, st>>>(a);
+      else rmsnorm_bwd_kernel<T, 16, 4><<<grid, 512, smem, st>>>(a);
   }
 }
 
@@ -492,14 +516,25 @@ te_status te_rmsnorm_bwd(const void* dy, const void* s, te_dtype in_dtype, int64
     return TE_OK;
   }
   NormBwdArgs a = {static_cast<const __nv_bfloat16*>(dy), s, dres, gamma, rsigma, rows, cols, dx, workspace};
-  const int wpr = warps_per_row(cols);
+  const int wpr = warps_per_row(cols, 2);
   const int grid = walk_grid(rows, wpr);
   if (in_dtype == TE_BF16) launch_norm_bwd<__nv_bfloat16>(a, wpr, grid, st);
   else launch_norm_bwd<float>(a, wpr, grid, st);
   count_launch();
   te_status st1 = launch_status();
   if (st1 != TE_OK) return st1;
-  dgamma_kernel<<<static_cast<unsigned>((cols + 31) / 32), 256, 0, st>>>(workspace, grid, cols, dgamma);
+  // The sums' launch overlaps the end of the first kernel (programmatic dependent launch).
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((cols + 31) / 32), 1, 1);
+  cfg.blockDim = dim3(1024, 1, 1);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, dgamma_kernel, static_cast<const float*>(workspace), grid, cols, dgamma) != cudaSuccess)
+    return record_cuda(cudaGetLastError());
   count_launch();
   return launch_status();
 }

@@ -370,6 +370,45 @@ def test_streams_graphs_and_repeats():
         assert torch.equal(h, o["h"].t)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,K,Fc,N", [(1001, 768, 2048, 768), (60, 64, 1040, 2048), (3000, 1024, 1024, 256)])
+def test_bwd_overlap_and_graph(T, K, Fc, N):
+    """dX and dW overlap and start while dGU's kernel drains: twenty calls in a row, eager and in a
+    graph, give the bits that calls on their own give, and what follows in the stream sees both."""
+    dy, w2, gu = _bwd_inputs(T, Fc, N, 6)
+    a, b = _inputs(T, K, Fc, 6)
+    x, w, d, w2 = (torch.from_numpy(v).bfloat16().to(G.DEV) for v in (a, b, dy, w2))
+    bufs = [(torch.empty(T, 2 * Fc, dtype=torch.bfloat16, device=G.DEV), torch.empty_like(x), torch.empty_like(w))
+            for _ in range(2)]
+
+    def call(scale, i):
+        g, dx, dw = bufs[i]
+        te.te_gated_bwd_bf16(x, w, w2, d * scale, gu, te.ACT_SILU, g, dx=dx, dw=dw)
+        return g.clone(), dx.clone(), dw.clone()
+
+    want = []
+    for i in range(20):
+        want.append(call(2.0 ** (i % 3), 0))
+        torch.cuda.synchronize()
+    got = [call(2.0 ** (i % 3), i % 2) for i in range(20)]
+    torch.cuda.synchronize()
+    for p, q in zip(want, got):
+        assert all(torch.equal(m, n) for m, n in zip(p, q))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        g, dx, dw = bufs[1]
+        for i in range(5):
+            te.te_gated_bwd_bf16(x, w, w2, d, gu, te.ACT_SILU, g, dx=dx, dw=dw)
+        copies = [t.clone() for t in bufs[1]]
+    for _ in range(3):
+        for t in bufs[1]:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(m, n) for m, n in zip(want[0], copies))
+    G.check_no_device_error()
+
+
 # ---- refusals: nothing reaches the GPU -------------------------------------------------------------
 
 def test_wrapper_refusals():

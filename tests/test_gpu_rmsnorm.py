@@ -229,6 +229,29 @@ def test_other_stream_and_graph():
     assert torch.equal(q, q2) and torch.equal(amax, amax2)
 
 
+@pytest.mark.gpu
+def test_backward_in_a_graph():
+    """The sums of dgamma start while the rows' kernel drains, eagerly and in a graph: the same bits."""
+    dy, x, gamma, rs, dres, dx, dgamma = _bwd_check(2000, 768, "bf16", True)
+    ws = torch.full((te.te_rmsnorm_bwd_workspace_bytes(2000, 768) // 4,), float("nan"), device=G.DEV)
+    dx2, dg2 = torch.empty_like(dx), torch.empty_like(dgamma)
+    for _ in range(20):
+        te.te_rmsnorm_bwd(dy, x, gamma, rs, dx2, dg2, ws, dres=dres)
+    torch.cuda.synchronize()
+    assert torch.equal(dx, dx2) and torch.equal(dgamma, dg2)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(4):
+            te.te_rmsnorm_bwd(dy, x, gamma, rs, dx2, dg2, ws, dres=dres)
+        dg3 = dg2.clone()
+    for _ in range(3):
+        dg2.zero_()
+        ws.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(dgamma, dg3) and torch.equal(dx, dx2)
+
+
 # ---- refusals: nothing reaches the GPU --------------------------------------------------------
 
 def test_wrapper_refusals():
