@@ -1,6 +1,6 @@
 // Entry points of the gated feed-forward projections: h = act(x Wg^T) * (x Wu^T) in one kernel, and
 // its backward pass.  The kernels are gemm_kernel with the gated epilogues (gemm.cuh).
-#include "gated_decode.cuh"
+#include "gated_stream.cuh"
 
 namespace te {
 namespace {
@@ -72,12 +72,13 @@ te_status te_gated_gemm_bf16(const void* x, const void* w, int act, void* h, voi
   if (!h && !gu) return TE_ERR_NULL;
   if ((s = check_operands(x, w)) != TE_OK) return s;
   if (!aligned16(h) || !aligned16(gu)) return TE_ERR_ALIGN;
-  if (decodes(T, K, 2)) {
+  if (T <= kStrMaxTokens) {
     const DecodeArgs a = {static_cast<const uint8_t*>(x), static_cast<const uint8_t*>(w), static_cast<int>(T),
                           static_cast<int>(K), static_cast<int>(F), act, nullptr, nullptr,
                           static_cast<__nv_bfloat16*>(h), static_cast<__nv_bfloat16*>(gu), nullptr, nullptr, 0, nullptr,
                           nullptr};
-    return launch_decode<kDecBF16, kDecBF16>(a, static_cast<cudaStream_t>(stream));
+    if (decodes(T, K, F, 2)) return launch_decode<kDecBF16, kDecBF16>(a, static_cast<cudaStream_t>(stream));
+    return launch_stream<kBF16>(a, 1u, 1u, static_cast<cudaStream_t>(stream));
   }
   GatedArgs ep = {};
   if ((s = bf16_outputs(&ep, h, gu, T, F, act)) != TE_OK) return s;
@@ -106,10 +107,11 @@ te_status te_gated_gemm_fp8(const uint8_t* x, te_dtype fx, const uint8_t* w, te_
   if ((s = check_operands(x, w)) != TE_OK) return s;
   if (!aligned16(h) || !aligned16(gu) || !aligned16(q_h)) return TE_ERR_ALIGN;
   if (h_amax && cudaMemsetAsync(h_amax, 0, sizeof(float), st) != cudaSuccess) return record_cuda(cudaGetLastError());
-  if (decodes(T, K, 1)) {
+  if (T <= kStrMaxTokens) {
     const DecodeArgs a = {x, w, static_cast<int>(T), static_cast<int>(K), static_cast<int>(F), act,
                           x_scale_inv, w_scale_inv, static_cast<__nv_bfloat16*>(h), static_cast<__nv_bfloat16*>(gu), q_h,
                           h_scale, h_fmt == TE_E5M2, reinterpret_cast<unsigned int*>(h_amax), h_scale_inv};
+    if (!decodes(T, K, F, 1)) return launch_stream<kFP8>(a, fp8_code(fx), fp8_code(fw), st);
     if (fw == TE_E4M3)
       return fx == TE_E4M3 ? launch_decode<kDecE4M3, kDecE4M3>(a, st) : launch_decode<kDecE4M3, kDecE5M2>(a, st);
     return fx == TE_E4M3 ? launch_decode<kDecE5M2, kDecE4M3>(a, st) : launch_decode<kDecE5M2, kDecE5M2>(a, st);

@@ -8,8 +8,8 @@
 // the registers the instruction reads it from (the order of k inside a block is free, as long as x
 // follows it), four blocks ahead and across units, so the loads never wait for the arithmetic.
 // Each unit ends with the warps' partial sums added in warp
-// order through shared memory.  tcgen05 has no smaller tile than 128 rows, whose share of F leaves
-// SMs idle, and nothing to win where the tensor work is this small.
+// order through shared memory.  One token, K = 4096, F = 16384: BF16 42.7 us (6.28 TB/s; gemm_kernel,
+// whose SMs all read the one line of x at the same time, 84.0), FP8 23.9 us (5.61 TB/s; 43.4).
 #pragma once
 
 #include "gemm.cuh"
@@ -206,16 +206,18 @@ te_status launch_decode(const DecodeArgs& a, cudaStream_t st) {
   }
 }
 
-// Whether the decode kernel takes this call.  Up to 16 tokens it is the faster one wherever x fits
-// (K = 4096, F = 16384, us against the tcgen05 kernel: BF16 T = 1 42.7 / 84.0, 8 44.0 / 63.5, 16
-// 51.1 / 51.6; FP8 23.9 / 43.4, 24.7 / 34.7, 30.5 / 34.1).  From 17 to 32 its matrix rate (512
-// multiply-adds a clock and SM) and its shared memory, taken from the L1 that the loads in flight
-// pass through, cost more than the stream: BF16 T = 24 86.6 / 51.5, FP8 39.6 / 33.2, but K = 2048,
-// F = 5632 11.3 / 13.5 in FP8 and K = 768, F = 2048 T = 32 5.9 / 10.1 in BF16, so it keeps the
-// calls whose x and partial sums stay under 96 KB.
-inline bool decodes(int64_t T, int64_t K, int elem) {
+// Whether this kernel takes the call, or the one of gated_stream.cuh (us, this / that):
+//   K = 4096, F = 16384 (BF16 268 MB of weights, FP8 134): T = 1 42.7 / 47.7 and 23.9 / 25.2, T = 8
+//   43.5 / 44.6 and 24.7 / 25.7, T = 16 51.3 / 45.2 and 29.9 / 25.7, T = 24 86.6 / 45.3;
+//   K = 2048, F = 5632 (46 and 23 MB): T = 8 10.8 / 12.4 and 8.2 / 8.7, T = 16 12.3 / 12.4 and 9.4 / 8.6;
+//   K = 768, F = 2048 (6.3 and 3.1 MB): T = 16 4.7 / 7.2 and 4.0 / 5.7, T = 32 5.9 / 7.2 and 5.3 / 5.7.
+// Up to eight tokens it is the faster one at every size: no tensor memory to set up, and the loads go
+// out at once.  Beyond, its matrix rate (512 multiply-adds a clock and SM) and its shared memory, taken
+// from the L1 that the loads in flight pass through, cost more than that saves unless w is small.
+inline bool decodes(int64_t T, int64_t K, int64_t F, int elem) {
   if (T > 8 * kDecMaxTiles || K > (1 << 17)) return false;
-  return decode_smem(static_cast<int>(T), static_cast<int>(K), elem) <= (T <= 16 ? 232448u : 98304u);
+  if (T > 8 && 2 * F * K * elem > (int64_t(16) << 20)) return false;
+  return decode_smem(static_cast<int>(T), static_cast<int>(K), elem) <= 232448;
 }
 
 }  // namespace

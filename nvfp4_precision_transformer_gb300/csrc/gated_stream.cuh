@@ -1,0 +1,263 @@
+// The gated projections of up to 64 tokens that the kernel of gated_decode.cuh does not take: still a stream over the weights, but with too much matrix
+// work for mma.sync.  The operands change places against gemm_kernel: the weights are the 128-row
+// operand of the MMA (64 gate rows and the 64 up rows beside them) and the tokens its N (32 or 64), so
+// a stage is 16 KB of weights and 4 or 8 KB of x, and ten (eight) of them fit where gemm_kernel has
+// six with as much x as weights: 160 KB of weights in flight per SM.  One CTA per SM, no pairs: tiles
+// of 64 columns of h, and a CTA with one tile more than another has that much more of the bandwidth
+// at the end.
+//
+// warp 0 TMA producer, warp 1 MMA issuer, warps 2-5 epilogue.  Accumulator lanes 0-63 hold g and 64-127
+// u of the tile's columns, tokens along the TMEM columns: the g warps hand the second half of the
+// tokens to the u warps through shared memory and get the first half's u back, and each thread then
+// has one column of h for half of the tokens; neighbouring lanes write neighbouring columns.
+//
+// 24 tokens, K = 4096, F = 16384: BF16 45.3 us (5.92 TB/s; gemm_kernel 51.5), FP8 25.6 us (5.24 TB/s;
+// 33.2); 64 tokens 47.9 / 52.5 and 27.9 / 30.1.  gemm_kernel's six stages turn round in about 1.7 us
+// (load, MMA, commit), which bounds what an SM can have in flight; these turn round in less and are more.
+#pragma once
+
+#include "gated_decode.cuh"
+
+namespace te {
+namespace {
+
+constexpr int kStrThreads = 32 * 6;
+constexpr int64_t kStrMaxTokens = 64;
+constexpr int kStrMaxStages = 12;
+
+template <int NP>   // tokens, padded
+struct StrCfg {
+  static constexpr int kA = 128 * 128, kB = NP * 128;
+  static constexpr int kExchange = NP * 64 * 4;
+  static constexpr int kFit = (232448 - 1024 - 512 - kExchange) / (kA + kB);
+  static constexpr int kStages = kFit < kStrMaxStages ? kFit : kStrMaxStages;
+  static constexpr int kSmemB = kStages * kA;
+  static constexpr int kSmemX = kSmemB + kStages * kB;
+  static constexpr int kSmemBar = kSmemX + kExchange;
+  static constexpr int kSmemTotal = kSmemBar + 512 + 1024;
+  static constexpr int kCols = 2 * NP;   // two accumulators
+  static_assert(kSmemTotal <= 232448 && (2 * kStages + 5) * 8 + 16 <= 512, "shared memory");
+  static_assert(NP == 32 || NP == 64, "whole tcgen05.ld chunks, power-of-two TMEM columns");
+};
+
+template <int KIND, int NP>
+__global__ void __launch_bounds__(kStrThreads, 1)
+    gated_stream_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                        const __grid_constant__ DecodeArgs a, uint32_t idesc, int k_tiles, int* err) {
+  using C = StrCfg<NP>;
+  constexpr int S = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = dev::smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+  uint8_t* sA = smem;
+  uint8_t* sB = smem + C::kSmemB;
+  float* ex = reinterpret_cast<float*>(smem + C::kSmemX);   // [token][64 columns]
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kSmemBar);
+  uint64_t* empty = full + S;
+  uint64_t* acc_full = empty + S;
+  uint64_t* acc_empty = acc_full + 2;
+  uint64_t* drain = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tiles = (a.F + 63) / 64;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      dev::mbar_init(&full[s], 1);
+      dev::mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      dev::mbar_init(&acc_full[s], 1);
+      dev::mbar_init(&acc_empty[s], 4);
+    }
+    dev::mbar_init(drain, 1);
+    *abort_flag = 0;
+    dev::fence_barrier_init();
+    dev::prefetch_tmap(&tmW);
+    dev::prefetch_tmap(&tmX);
+  }
+  if (warp == 1) dev::tmem_alloc(tmem_slot, C::kCols);
+  dev::tc_fence_before();
+  __syncthreads();
+  dev::tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      int issued = 0;
+      bool ok = true;
+      for (int tile = static_cast<int>(blockIdx.x); tile < tiles && ok; tile += static_cast<int>(gridDim.x)) {
+        for (int kt = 0; kt < k_tiles; ++kt) {
+          if (!dev::mbar_wait(&empty[stage], phase ^ 1u, abort_flag, err)) {
+            ok = false;
+            break;
+          }
+          dev::mbar_expect_tx(&full[stage], C::kA + C::kB);
+          dev::tma_load_2d(sA + stage * C::kA, &tmW, &full[stage], kt * 128, tile * 64);
+          dev::tma_load_2d(sA + stage * C::kA + 64 * 128, &tmW, &full[stage], kt * 128, a.F + tile * 64);
+          dev::tma_load_2d(sB + stage * C::kB, &tmX, &full[stage], kt * 128, 0);
+          ++issued;
+          if (++stage == S) stage = 0, phase ^= 1u;
+        }
+      }
+      if (!ok) {
+        // bounded wait for the copies in flight, the latest S at most
+        volatile int dummy = 0;
+        for (int i = issued > S ? issued - S : 0; i < issued; ++i)
+          dev::mbar_wait(&full[i % S], static_cast<uint32_t>(i / S) & 1u, &dummy, err);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      int stage = 0, it = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int tile = static_cast<int>(blockIdx.x); tile < tiles && ok; tile += static_cast<int>(gridDim.x), ++it) {
+        const int as = it & 1;
+        if (!dev::mbar_wait(&acc_empty[as], (static_cast<uint32_t>(it >> 1) & 1u) ^ 1u, abort_flag, err)) break;
+        dev::tc_fence_after();
+        const uint32_t d = tmem_base + static_cast<uint32_t>(as * NP);
+        for (int kt = 0; kt < k_tiles; ++kt) {
+          if (!dev::mbar_wait(&full[stage], phase, abort_flag, err)) {
+            ok = false;
+            break;
+          }
+          dev::tc_fence_after();
+          const uint32_t sa = dev::smem_u32(sA + stage * C::kA), sb = dev::smem_u32(sB + stage * C::kB);
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks) {
+            const uint64_t ad = dev::smem_desc(sa + 32 * ks, 0, 1024, 2), bd = dev::smem_desc(sb + 32 * ks, 0, 1024, 2);
+            if (KIND == kBF16) dev::mma_f16(d, ad, bd, idesc, (kt | ks) != 0);
+            else dev::mma_f8f6f4(d, ad, bd, idesc, (kt | ks) != 0);
+          }
+          dev::tc_commit(&empty[stage]);
+          if (++stage == S) stage = 0, phase ^= 1u;
+        }
+        if (!ok) break;
+        dev::tc_commit(&acc_full[as]);
+      }
+      dev::tc_commit(drain);
+      volatile int dummy = 0;
+      dev::mbar_wait(drain, 0, &dummy, err);
+    }
+  } else {
+    const int quarter = warp & 3;
+    const bool up = quarter >= 2;                 // lanes 64-127 of the accumulator: u
+    const int fl = (quarter & 1) * 32 + lane;     // column of the tile
+    const float alpha = (a.alpha_a ? __ldg(a.alpha_a) : 1.0f) * (a.alpha_b ? __ldg(a.alpha_b) : 1.0f);
+    const float qs = a.q ? __ldg(a.q_scale) : 1.0f;
+    unsigned int top = 0;
+    int it = 0;
+    bool ok = true;
+    for (int tile = static_cast<int>(blockIdx.x); tile < tiles; tile += static_cast<int>(gridDim.x), ++it) {
+      const int as = it & 1;
+      if (!dev::mbar_wait(&acc_full[as], static_cast<uint32_t>(it >> 1) & 1u, abort_flag, err)) ok = false;
+      // the four warps leave together: the exchange below has barriers of all of them
+      int all_ok;
+      asm volatile(
+          "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}\n"
+          : "=r"(all_ok)
+          : "r"(static_cast<int>(ok))
+          : "memory");
+      if (!all_ok) break;
+      dev::tc_fence_after();
+      uint32_t acc[NP / 32][32];
+      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(as * NP);
+#pragma unroll
+      for (int c = 0; c < NP / 32; ++c) dev::tmem_ld_32x32b_x32(taddr + 32 * c, acc[c]);
+      dev::tmem_ld_wait();
+#pragma unroll
+      for (int c = 0; c < NP / 32; ++c) dev::reg_fence(acc[c]);
+      dev::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) dev::mbar_arrive(&acc_empty[as]);
+      // g warps give away the second half of the tokens, u warps the first
+#pragma unroll
+      for (int n = 0; n < NP / 2; ++n) {
+        const int give = up ? n : n + NP / 2;
+        ex[give * 64 + fl] = __uint_as_float(up ? acc[n / 32][n % 32] : acc[(n + NP / 2) / 32][(n + NP / 2) % 32]);
+      }
+      asm volatile("bar.sync 2, 128;" ::: "memory");
+      const int f = tile * 64 + fl;
+#pragma unroll
+      for (int n = 0; n < NP / 2; n += 2) {
+        const int n0 = up ? n + NP / 2 : n;
+        const float2 mine = make_float2(
+            __uint_as_float(up ? acc[(n + NP / 2) / 32][(n + NP / 2) % 32] : acc[n / 32][n % 32]),
+            __uint_as_float(up ? acc[(n + NP / 2 + 1) / 32][(n + NP / 2 + 1) % 32] : acc[(n + 1) / 32][(n + 1) % 32]));
+        const float2 got = make_float2(ex[n0 * 64 + fl], ex[(n0 + 1) * 64 + fl]);
+        const float2 g = __fmul2_rn(up ? got : mine, both(alpha)), u = __fmul2_rn(up ? mine : got, both(alpha));
+        const float2 h = __fmul2_rn(gate_act(g, a.act), u);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int64_t t = n0 + j;
+          if (t < a.T && f < a.F) {
+            const float gv = j ? g.y : g.x, uv = j ? u.y : u.x, hv = j ? h.y : h.x;
+            if (a.gu) {
+              a.gu[t * 2 * a.F + f] = __float2bfloat16_rn(gv);
+              a.gu[t * 2 * a.F + a.F + f] = __float2bfloat16_rn(uv);
+            }
+            if (a.h) a.h[t * a.F + f] = __float2bfloat16_rn(hv);
+            if (a.q) {
+              top = max(top, __float_as_uint(hv) & 0x7FFFFFFFu);
+              a.q[t * a.F + f] = static_cast<uint8_t>(a.q_e5m2 ? cvt_e5m2x2(hv * qs, 0.0f) : cvt_e4m3x2(hv * qs, 0.0f));
+            }
+          }
+        }
+      }
+      // (the exchange is written again only after the next tile's first barrier)
+    }
+    if (a.amax) {
+      top = __reduce_max_sync(0xFFFFFFFFu, top);
+      if (lane == 0) atomicMax(a.amax, top);
+    }
+    if (a.scale_inv && blockIdx.x == 0 && threadIdx.x == 64) *a.scale_inv = __fdiv_rn(1.0f, qs);
+  }
+
+  dev::tc_fence_before();
+  __syncthreads();
+  dev::tc_fence_after();
+  if (warp == 1) dev::tmem_dealloc(tmem_base, C::kCols);
+}
+
+template <int KIND, int NP>
+te_status launch_stream(const DecodeArgs& a, uint32_t xfmt, uint32_t wfmt, cudaStream_t st) {
+  using C = StrCfg<NP>;
+  static bool attr_set[64] = {false};
+  int dev_id = 0;
+  cudaGetDevice(&dev_id);
+  if (dev_id < 0 || dev_id >= 64) return TE_ERR_CUDA;
+  if (!attr_set[dev_id]) {
+    if (cudaFuncSetAttribute(gated_stream_kernel<KIND, NP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             C::kSmemTotal) != cudaSuccess)
+      return record_cuda(cudaGetLastError());
+    attr_set[dev_id] = true;
+  }
+  const uint64_t row_bytes = static_cast<uint64_t>(a.K) * (KIND == kBF16 ? 2 : 1);
+  CUtensorMap tw, tx;
+  te_status s = make_tmap_2d(&tw, a.w, row_bytes, 2 * static_cast<uint64_t>(a.F), 64);
+  if (s != TE_OK) return s;
+  s = make_tmap_2d(&tx, a.x, row_bytes, static_cast<uint64_t>(a.T), NP);
+  if (s != TE_OK) return s;
+  int* err = device_error_word();
+  if (err == nullptr) return record_cuda(cudaErrorInvalidDevice);
+  // the weights are operand A: M = 128, N = NP
+  uint32_t idesc = make_idesc(KIND, wfmt, xfmt, 128);
+  idesc = (idesc & ~(0x3Fu << 17)) | (static_cast<uint32_t>(NP >> 3) << 17);
+  const int tiles = (a.F + 63) / 64;
+  gated_stream_kernel<KIND, NP><<<tiles < num_sms() ? tiles : num_sms(), kStrThreads, C::kSmemTotal, st>>>(
+      tw, tx, a, idesc, static_cast<int>((row_bytes + 127) / 128), err);
+  count_launch();
+  return launch_status();
+}
+
+template <int KIND>
+te_status launch_stream(const DecodeArgs& a, uint32_t xfmt, uint32_t wfmt, cudaStream_t st) {
+  return a.T <= 32 ? launch_stream<KIND, 32>(a, xfmt, wfmt, st) : launch_stream<KIND, 64>(a, xfmt, wfmt, st);
+}
+
+}  // namespace
+}  // namespace te

@@ -192,12 +192,13 @@ def test_several_tiles_per_cta(kind, outs):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("T,K,Fc", [(1, 4096, 2480), (8, 2064, 80), (9, 1040, 1232), (16, 4112, 32), (24, 4096, 48),
-                                    (32, 2096, 1248), (25, 4096, 32)])
+                                    (32, 2096, 1248), (25, 4096, 32), (20, 4096, 80), (40, 128, 10000), (64, 2064, 272),
+                                    (31, 6000, 16), (3, 16400, 32)])
 @pytest.mark.parametrize("kind,outs,fmt", [("bf16", ("h", "gu"), "e4m3"), ("fp8", ("h", "gu", "q"), "e4m3"),
                                            ("fp8", ("q",), "e5m2")])
 def test_few_tokens(T, K, Fc, kind, outs, fmt):
-    """Long rows and more units of columns than SMs: the streaming kernel's steps and its prefetch
-    across units."""
+    """Long rows and more units of columns than SMs: the streaming kernels' steps, their prefetch
+    across units and the reuse of their rings and exchange buffers."""
     _check_forward(kind, T, K, Fc, "gelu", outs, fmt)
 
 
