@@ -200,7 +200,7 @@ def te_layernorm_fp8(x, gamma, beta, eps: float, fmt: int, scale, q_row, ln_out=
 
 def _need(fn: str, name: str, t, dtype, shape, optional: bool = False):
     """Refuses a tensor that the call would misread: not on the GPU, not contiguous, of another
-    dtype (one, or a tuple of them) or size.  `shape` may be an element count (at least so many)."""
+    dtype (one, or a tuple of them) or shape.  Returns its address."""
     if t is None:
         if optional:
             return None
@@ -209,13 +209,38 @@ def _need(fn: str, name: str, t, dtype, shape, optional: bool = False):
         return t.data_ptr()
     if t.dtype is not dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
         raise TypeError(f"{fn}: {name} is {t.dtype}, expected {dtype}")
-    if t.numel() < shape if isinstance(shape, int) else t.shape != shape:
-        raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {shape}")
+    if t.shape != shape:
+        raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{fn}: {name} is not contiguous")
     if not t.is_cuda:
         raise ValueError(f"{fn}: {name} is not on the GPU")
     return t.data_ptr()
+
+
+def _need_n(fn: str, name: str, t, dtype, n: int, optional: bool = False):
+    """The same for a tensor of at least ``n`` elements whatever its shape (scalars, scale tensors)."""
+    if t is None:
+        if optional:
+            return None
+        raise TypeError(f"{fn}: {name} is required")
+    if t.dtype is dtype and t.numel() >= n and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    if t.dtype is not dtype:
+        raise TypeError(f"{fn}: {name} is {t.dtype}, expected {dtype}")
+    if t.numel() < n:
+        raise ValueError(f"{fn}: {name} has {t.numel()} elements, needs {n}")
+    raise ValueError(f"{fn}: {name} is not {'contiguous' if t.is_cuda else 'on the GPU'}")
+
+
+def _mx_bytes(rows: int, cols: int) -> int:
+    """te_scale_bytes(E8M0, rows, cols) of whole blocks."""
+    return -(-rows // 128) * 128 * (-(-cols // 128) * 4)
+
+
+def _nv_bytes(rows: int, cols: int) -> int:
+    """te_scale_bytes(UE4M3, rows, cols) of whole blocks."""
+    return -(-rows // 128) * 128 * (-(-cols // 256) * 16)
 
 
 def _norm_operands(fn, x, gamma, residual, res_out, y, rsigma):
@@ -237,9 +262,9 @@ def te_rmsnorm_fp8(x, gamma, eps: float, fmt: int, scale=None, q_row=None, resid
     fn, f32 = "te_rmsnorm_fp8", torch.float32
     px, dt, r, c, pres, pg, pro, py, prs = _norm_operands(fn, x, gamma, residual, res_out, y, rsigma)
     _check(fn, lib().te_rmsnorm_fp8(
-        px, dt, r, c, pres, pg, float(eps), fmt, _need(fn, "scale", scale, f32, 1, True),
+        px, dt, r, c, pres, pg, float(eps), fmt, _need_n(fn, "scale", scale, f32, 1, True),
         _need(fn, "q_row", q_row, torch.uint8, x.shape, True), py, pro, prs,
-        _need(fn, "amax_out", amax_out, f32, 1, True), _need(fn, "scale_inv_out", scale_inv_out, f32, 1, True),
+        _need_n(fn, "amax_out", amax_out, f32, 1, True), _need_n(fn, "scale_inv_out", scale_inv_out, f32, 1, True),
         _stream(stream)))
 
 
@@ -250,7 +275,7 @@ def te_rmsnorm_mxfp8(x, gamma, eps: float, q_row, s_row, residual=None, res_out=
     px, dt, r, c, pres, pg, pro, py, prs = _norm_operands(fn, x, gamma, residual, res_out, y, rsigma)
     _check(fn, lib().te_rmsnorm_mxfp8(
         px, dt, r, c, pres, pg, float(eps), _need(fn, "q_row", q_row, torch.uint8, x.shape),
-        _need(fn, "s_row", s_row, torch.uint8, te_scale_bytes(E8M0, r, c)), py, pro, prs, _stream(stream)))
+        _need_n(fn, "s_row", s_row, torch.uint8, _mx_bytes(r, c)), py, pro, prs, _stream(stream)))
 
 
 def te_rmsnorm_bwd_workspace_bytes(rows: int, cols: int) -> int:
@@ -265,7 +290,7 @@ def te_rmsnorm_bwd(dy, s, gamma, rsigma, dx, dgamma, workspace, dres=None, strea
         raise ValueError(f"{fn}: s has shape {tuple(s.shape)}, expected [rows, cols]")
     shape, dt = s.shape, s.dtype
     ps = _need(fn, "s", s, (torch.bfloat16, f32), shape)
-    pw = _need(fn, "workspace", workspace, f32, 0)
+    pw = _need_n(fn, "workspace", workspace, f32, 0)
     _check(fn, lib().te_rmsnorm_bwd(
         _need(fn, "dy", dy, torch.bfloat16, shape), ps, _in_dtype(s), shape[0], shape[1],
         _need(fn, "gamma", gamma, f32, shape[1:]), _need(fn, "rsigma", rsigma, f32, shape[:1]),
@@ -359,10 +384,10 @@ def te_gated_gemm_fp8(x, fx: int, w, fw: int, x_scale_inv, w_scale_inv, act: int
     T, K, F = _gated_shape(fn, x, w)
     _check(fn, lib().te_gated_gemm_fp8(
         _need(fn, "x", x, u8, (T, K)), fx, _need(fn, "w", w, u8, (2 * F, K)), fw,
-        _need(fn, "x_scale_inv", x_scale_inv, f32, 1), _need(fn, "w_scale_inv", w_scale_inv, f32, 1), act,
+        _need_n(fn, "x_scale_inv", x_scale_inv, f32, 1), _need_n(fn, "w_scale_inv", w_scale_inv, f32, 1), act,
         _need(fn, "h", h, bf, (T, F), True), _need(fn, "gu", gu, bf, (T, 2 * F), True),
-        _need(fn, "q_h", q_h, u8, (T, F), True), h_fmt, _need(fn, "h_scale", h_scale, f32, 1, True),
-        _need(fn, "h_amax", h_amax, f32, 1, True), _need(fn, "h_scale_inv", h_scale_inv, f32, 1, True), T, K, F,
+        _need(fn, "q_h", q_h, u8, (T, F), True), h_fmt, _need_n(fn, "h_scale", h_scale, f32, 1, True),
+        _need_n(fn, "h_amax", h_amax, f32, 1, True), _need_n(fn, "h_scale_inv", h_scale_inv, f32, 1, True), T, K, F,
         _stream(stream)))
 
 
@@ -373,10 +398,10 @@ def te_gated_gemm_mxfp8(x, sx, w, sw, act: int, h=None, gu=None, q_h=None, s_h=N
     fn, bf, u8 = "te_gated_gemm_mxfp8", torch.bfloat16, torch.uint8
     T, K, F = _gated_shape(fn, x, w)
     _check(fn, lib().te_gated_gemm_mxfp8(
-        _need(fn, "x", x, u8, (T, K)), fx, _need(fn, "sx", sx, u8, te_scale_bytes(E8M0, T, K)),
-        _need(fn, "w", w, u8, (2 * F, K)), fw, _need(fn, "sw", sw, u8, te_scale_bytes(E8M0, 2 * F, K)), act,
+        _need(fn, "x", x, u8, (T, K)), fx, _need_n(fn, "sx", sx, u8, _mx_bytes(T, K)),
+        _need(fn, "w", w, u8, (2 * F, K)), fw, _need_n(fn, "sw", sw, u8, _mx_bytes(2 * F, K)), act,
         _need(fn, "h", h, bf, (T, F), True), _need(fn, "gu", gu, bf, (T, 2 * F), True),
-        _need(fn, "q_h", q_h, u8, (T, F), True), _need(fn, "s_h", s_h, u8, te_scale_bytes(E8M0, T, F), True), T, K, F,
+        _need(fn, "q_h", q_h, u8, (T, F), True), _need_n(fn, "s_h", s_h, u8, _mx_bytes(T, F), True), T, K, F,
         _stream(stream)))
 
 
@@ -386,9 +411,9 @@ def te_gated_gemm_nvfp4(x, sx, gx, w, sw, gw, act: int, h=None, gu=None, stream=
     fn, bf, u8, f32 = "te_gated_gemm_nvfp4", torch.bfloat16, torch.uint8, torch.float32
     T, K, F = _gated_shape(fn, x, w, 2)
     _check(fn, lib().te_gated_gemm_nvfp4(
-        _need(fn, "x", x, u8, (T, K // 2)), _need(fn, "sx", sx, u8, te_scale_bytes(UE4M3, T, K)),
-        _need(fn, "gx", gx, f32, 1), _need(fn, "w", w, u8, (2 * F, K // 2)),
-        _need(fn, "sw", sw, u8, te_scale_bytes(UE4M3, 2 * F, K)), _need(fn, "gw", gw, f32, 1), act,
+        _need(fn, "x", x, u8, (T, K // 2)), _need_n(fn, "sx", sx, u8, _nv_bytes(T, K)),
+        _need_n(fn, "gx", gx, f32, 1), _need(fn, "w", w, u8, (2 * F, K // 2)),
+        _need_n(fn, "sw", sw, u8, _nv_bytes(2 * F, K)), _need_n(fn, "gw", gw, f32, 1), act,
         _need(fn, "h", h, bf, (T, F), True), _need(fn, "gu", gu, bf, (T, 2 * F), True), T, K, F, _stream(stream)))
 
 
@@ -409,7 +434,7 @@ def te_gated_dgrad_fp8(dy, fd: int, w2, fw: int, dy_scale_inv, w2_scale_inv, gu,
     T, F, N, pgu, pdgu = _dgrad_shape(fn, dy, w2, gu, dgu)
     _check(fn, lib().te_gated_dgrad_fp8(
         _need(fn, "dy", dy, u8, (T, N)), fd, _need(fn, "w2", w2, u8, (F, N)), fw,
-        _need(fn, "dy_scale_inv", dy_scale_inv, f32, 1), _need(fn, "w2_scale_inv", w2_scale_inv, f32, 1), pgu, act, pdgu,
+        _need_n(fn, "dy_scale_inv", dy_scale_inv, f32, 1), _need_n(fn, "w2_scale_inv", w2_scale_inv, f32, 1), pgu, act, pdgu,
         T, F, N, _stream(stream)))
 
 
@@ -419,8 +444,8 @@ def te_gated_dgrad_mxfp8(dy, sd, w2, sw, gu, act: int, dgu, fd: int = E4M3, fw: 
     fn, u8 = "te_gated_dgrad_mxfp8", torch.uint8
     T, F, N, pgu, pdgu = _dgrad_shape(fn, dy, w2, gu, dgu)
     _check(fn, lib().te_gated_dgrad_mxfp8(
-        _need(fn, "dy", dy, u8, (T, N)), fd, _need(fn, "sd", sd, u8, te_scale_bytes(E8M0, T, N)),
-        _need(fn, "w2", w2, u8, (F, N)), fw, _need(fn, "sw", sw, u8, te_scale_bytes(E8M0, F, N)), pgu, act, pdgu, T, F, N,
+        _need(fn, "dy", dy, u8, (T, N)), fd, _need_n(fn, "sd", sd, u8, _mx_bytes(T, N)),
+        _need(fn, "w2", w2, u8, (F, N)), fw, _need_n(fn, "sw", sw, u8, _mx_bytes(F, N)), pgu, act, pdgu, T, F, N,
         _stream(stream)))
 
 
@@ -430,9 +455,9 @@ def te_gated_dgrad_nvfp4(dy, sd, gd, w2, sw, gw, gu, act: int, dgu, stream=None)
     fn, u8, f32 = "te_gated_dgrad_nvfp4", torch.uint8, torch.float32
     T, F, N, pgu, pdgu = _dgrad_shape(fn, dy, w2, gu, dgu, 2)
     _check(fn, lib().te_gated_dgrad_nvfp4(
-        _need(fn, "dy", dy, u8, (T, N // 2)), _need(fn, "sd", sd, u8, te_scale_bytes(UE4M3, T, N)),
-        _need(fn, "gd", gd, f32, 1), _need(fn, "w2", w2, u8, (F, N // 2)),
-        _need(fn, "sw", sw, u8, te_scale_bytes(UE4M3, F, N)), _need(fn, "gw", gw, f32, 1), pgu, act, pdgu, T, F, N,
+        _need(fn, "dy", dy, u8, (T, N // 2)), _need_n(fn, "sd", sd, u8, _nv_bytes(T, N)),
+        _need_n(fn, "gd", gd, f32, 1), _need(fn, "w2", w2, u8, (F, N // 2)),
+        _need_n(fn, "sw", sw, u8, _nv_bytes(F, N)), _need_n(fn, "gw", gw, f32, 1), pgu, act, pdgu, T, F, N,
         _stream(stream)))
 
 

@@ -106,7 +106,6 @@ te_status te_gated_gemm_fp8(const uint8_t* x, te_dtype fx, const uint8_t* w, te_
   if (!x_scale_inv || !w_scale_inv) return TE_ERR_NULL;
   if ((s = check_operands(x, w)) != TE_OK) return s;
   if (!aligned16(h) || !aligned16(gu) || !aligned16(q_h)) return TE_ERR_ALIGN;
-  if (h_amax && cudaMemsetAsync(h_amax, 0, sizeof(float), st) != cudaSuccess) return record_cuda(cudaGetLastError());
   if (T <= kStrMaxTokens) {
     const DecodeArgs a = {x, w, static_cast<int>(T), static_cast<int>(K), static_cast<int>(F), act,
                           x_scale_inv, w_scale_inv, static_cast<__nv_bfloat16*>(h), static_cast<__nv_bfloat16*>(gu), q_h,
@@ -127,8 +126,10 @@ te_status te_gated_gemm_fp8(const uint8_t* x, te_dtype fx, const uint8_t* w, te_
     s = make_tmap_2d_view64(&ep.q, q_h, static_cast<uint64_t>(F), static_cast<uint64_t>(F), static_cast<uint64_t>(T));
     if (s != TE_OK) return s;
   }
+  if (h_amax && (s = zero_amax(h_amax, st)) != TE_OK) return s;
   return launch_gemm<kFP8, 2, kGated>(x, w, K, nullptr, nullptr, 0, x_scale_inv, w_scale_inv, nullptr, nullptr, TE_BF16,
-                                      0, T, 2 * F, K, fp8_code(fx), fp8_code(fw), st, 0, 0, ep);
+                                      0, T, 2 * F, K, fp8_code(fx), fp8_code(fw), st, 0, 0, ep,
+                                      h_amax ? kPdlOverlap : 0);
 }
 
 te_status te_gated_gemm_mxfp8(const uint8_t* x, te_dtype fx, const uint8_t* sx, const uint8_t* w, te_dtype fw,

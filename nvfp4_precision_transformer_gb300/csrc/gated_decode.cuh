@@ -70,7 +70,7 @@ __host__ inline size_t decode_smem(int T, int K, int elem) {
 }
 
 template <int W, int X, int NT>
-__global__ void __launch_bounds__(32 * kDecWarps, 1) gated_decode_kernel(const DecodeArgs a) {
+__global__ void __launch_bounds__(32 * kDecWarps, 1) gated_decode_kernel(DecodeArgs a) {
   constexpr int EB = W == kDecBF16 ? 2 : 1;
   extern __shared__ __align__(128) uint8_t dec_smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -172,7 +172,10 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1) gated_decode_kernel(const D
   }
   if (a.amax && warp < NT) {
     top = __reduce_max_sync(0xFFFFFFFFu, top);
-    if (lane == 0) atomicMax(a.amax, top);
+    if (lane == 0) {
+      dev::pdl_wait();   // its zeroing
+      atomicMax(a.amax, top);
+    }
   }
   if (a.scale_inv && blockIdx.x == 0 && threadIdx.x == 0) *a.scale_inv = __fdiv_rn(1.0f, qs);
 }
@@ -191,7 +194,16 @@ te_status launch_decode(const DecodeArgs& a, cudaStream_t st) {
   }
   const int units = a.F / 8;
   const int grid = units < num_sms() ? units : num_sms();
-  gated_decode_kernel<W, X, NT><<<grid, 32 * kDecWarps, decode_smem(a.T, a.K, W == kDecBF16 ? 2 : 1), st>>>(a);
+  const size_t smem = decode_smem(a.T, a.K, W == kDecBF16 ? 2 : 1);
+  const dim3 g(static_cast<unsigned>(grid), 1, 1), block(32 * kDecWarps, 1, 1);
+  if (a.amax) {
+    const te_status s = zero_amax(a.amax, st);
+    if (s != TE_OK) return s;
+    const cudaError_t e = launch_dependent(gated_decode_kernel<W, X, NT>, g, block, smem, st, a);
+    if (e != cudaSuccess) return record_cuda(e);
+  } else {
+    gated_decode_kernel<W, X, NT><<<g, block, smem, st>>>(a);
+  }
   count_launch();
   return launch_status();
 }

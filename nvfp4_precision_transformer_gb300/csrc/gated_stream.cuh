@@ -212,7 +212,10 @@ __global__ void __launch_bounds__(kStrThreads, 1)
     }
     if (a.amax) {
       top = __reduce_max_sync(0xFFFFFFFFu, top);
-      if (lane == 0) atomicMax(a.amax, top);
+      if (lane == 0) {
+        dev::pdl_wait();   // its zeroing
+        atomicMax(a.amax, top);
+      }
     }
     if (a.scale_inv && blockIdx.x == 0 && threadIdx.x == 64) *a.scale_inv = __fdiv_rn(1.0f, qs);
   }
@@ -248,8 +251,17 @@ te_status launch_stream(const DecodeArgs& a, uint32_t xfmt, uint32_t wfmt, cudaS
   uint32_t idesc = make_idesc(KIND, wfmt, xfmt, 128);
   idesc = (idesc & ~(0x3Fu << 17)) | (static_cast<uint32_t>(NP >> 3) << 17);
   const int tiles = (a.F + 63) / 64;
-  gated_stream_kernel<KIND, NP><<<tiles < num_sms() ? tiles : num_sms(), kStrThreads, C::kSmemTotal, st>>>(
-      tw, tx, a, idesc, static_cast<int>((row_bytes + 127) / 128), err);
+  const dim3 g(static_cast<unsigned>(tiles < num_sms() ? tiles : num_sms()), 1, 1), block(kStrThreads, 1, 1);
+  const int k_tiles = static_cast<int>((row_bytes + 127) / 128);
+  if (a.amax) {
+    s = zero_amax(a.amax, st);
+    if (s != TE_OK) return s;
+    const cudaError_t e =
+        launch_dependent(gated_stream_kernel<KIND, NP>, g, block, C::kSmemTotal, st, tw, tx, a, idesc, k_tiles, err);
+    if (e != cudaSuccess) return record_cuda(e);
+  } else {
+    gated_stream_kernel<KIND, NP><<<g, block, C::kSmemTotal, st>>>(tw, tx, a, idesc, k_tiles, err);
+  }
   count_launch();
   return launch_status();
 }

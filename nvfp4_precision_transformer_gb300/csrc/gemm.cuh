@@ -130,7 +130,8 @@ struct Cfg {
 // the kernel waits for the one before it after its set-up; it lets the next one start once it has
 // itself begun (after that wait); it waits for the one before it only at its end, being independent
 // of its results, so that what follows in the stream finds both complete.
-constexpr int kPdlWait = 1, kPdlTrigger = 2, kPdlWaitAtEnd = 4;
+// kPdlOverlap: launched beside the one before it, on whose results only the epilogue's end waits.
+constexpr int kPdlWait = 1, kPdlTrigger = 2, kPdlWaitAtEnd = 4, kPdlOverlap = 8;
 
 struct GemmArgs {
   int M, N, K;
@@ -275,8 +276,8 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, EPI>::kThreads, 1)
   }
   __syncthreads();
 
-  if (args.pdl & kPdlWait) asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (args.pdl & kPdlTrigger) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (args.pdl & kPdlWait) dev::pdl_wait();
+  if (args.pdl & kPdlTrigger) dev::pdl_trigger();
 
   // Scale atoms j = j0, j0 + dj, ... of stage `st` (shared memory) -> its TMEM slot, one copy
   // per 512-byte atom, the A atom and the two B atoms of a k-step back to back (grouped by
@@ -639,7 +640,7 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, EPI>::kThreads, 1)
     if (lane == 0) dev::bulk_wait0();
   }
 
-  if (args.pdl & kPdlWaitAtEnd) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (args.pdl & kPdlWaitAtEnd) dev::pdl_wait();
   dev::tc_fence_before();
   __syncthreads();
   if (kPair) dev::cluster_sync();  // the leader's MMAs read the peer's shared memory until here
@@ -770,7 +771,7 @@ te_status launch_gemm(const void* A, const void* B, int64_t row_bytes, const uin
     units = (tiles + waves - 1) / waves;
   }
   cfg.gridDim = dim3(static_cast<unsigned>(CG * units), 1, 1);
-  cfg.numAttrs = (pdl & (kPdlWait | kPdlWaitAtEnd)) ? 2 : 1;
+  cfg.numAttrs = (pdl & (kPdlWait | kPdlWaitAtEnd | kPdlOverlap)) ? 2 : 1;
   if (cudaLaunchKernelEx(&cfg, gemm_kernel<KIND, CG, EPI>, ta, tb, td, tsa, tsb, g, ep) != cudaSuccess)
     return record_cuda(cudaGetLastError());
   count_launch();

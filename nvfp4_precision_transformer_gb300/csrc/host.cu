@@ -27,6 +27,11 @@ int current_device() {
   return (d >= 0 && d < kMaxDevices) ? d : 0;
 }
 
+__global__ void zero_amax_kernel(unsigned int* amax) {
+  te::dev::pdl_trigger();
+  *amax = 0u;
+}
+
 // One warp waits on a barrier that nothing completes: the bounded wait gives up
 // after ~10 ms, records TE_ERR_TIMEOUT and the kernel returns normally.
 __global__ void selftest_wait_kernel(int* err) {
@@ -54,6 +59,12 @@ te_status record_cuda(cudaError_t e) {
 }
 
 void count_launch(int n) { g_launches.fetch_add(static_cast<uint64_t>(n)); }
+
+te_status zero_amax(void* amax, cudaStream_t st) {
+  zero_amax_kernel<<<1, 1, 0, st>>>(static_cast<unsigned int*>(amax));
+  count_launch();
+  return launch_status();
+}
 
 int* device_error_word() {
   const int d = current_device();

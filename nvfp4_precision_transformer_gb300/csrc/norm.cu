@@ -115,7 +115,7 @@ struct NormArgs {
 // The maximum of |y| is kept as bits (ordered as the non-negative floats are), so a NaN, whose
 // bits are above infinity's, is not lost.
 template <typename T, int WPR, bool MX>
-__global__ void __launch_bounds__(32 * cta_warps(WPR), WPR <= 8 ? 2 : 1) rmsnorm_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(32 * cta_warps(WPR), WPR <= 8 ? 2 : 1) rmsnorm_kernel(NormArgs a) {
   constexpr int GR = cta_rows(WPR);
   __shared__ float red[GR][2][WPR];
   __shared__ unsigned int top[32];
@@ -221,8 +221,12 @@ __global__ void __launch_bounds__(32 * cta_warps(WPR), WPR <= 8 ? 2 : 1) rmsnorm
     if (warp == 0) {
       lmax = __reduce_max_sync(0xFFFFFFFFu, lane < cta_warps(WPR) ? top[lane] : 0u);
       if (lane == 0) {
-        if (a.amax_whole) *a.amax = lmax;
-        else atomicMax(a.amax, lmax);
+        if (a.amax_whole) {
+          *a.amax = lmax;
+        } else {
+          dev::pdl_wait();   // its zeroing
+          atomicMax(a.amax, lmax);
+        }
       }
     }
   }
@@ -322,7 +326,7 @@ __global__ void __launch_bounds__(32 * cta_warps(WPR), WPR <= 8 ? 2 : 1) rmsnorm
     }
     if (kAhead) cur = nxt;
   }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  dev::pdl_trigger();
   // the CTA's column sums: the row groups in order
   if (GR > 1) {
     if (grp > 0) {
@@ -356,7 +360,7 @@ __global__ void __launch_bounds__(1024) dgamma_kernel(const float* __restrict__ 
                                                       float* __restrict__ dgamma) {
   __shared__ float part[32][33];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  asm volatile("griddepcontrol.wait;" ::: "memory");   // the partial sums are complete
+  dev::pdl_wait();   // the partial sums are complete
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   float t = 0.0f;
   if (c < C) {
@@ -393,17 +397,30 @@ int walk_grid(int64_t rows, int wpr) {
 template <typename T, bool MX>
 te_status launch_norm(NormArgs& a, cudaStream_t st) {
   const int wpr = warps_per_row(a.cols, kCh);
-  const int grid = walk_grid(a.rows, wpr);
+  int grid = walk_grid(a.rows, wpr);
+  if (MX) {
+    // padding rows of the scales beside few rows: a CTA per 2048 words of them
+    const int64_t want = ((a.rpad - a.rows) * (a.kpad / 4) + 2047) / 2048;
+    if (want > grid) grid = static_cast<int>(want < num_sms() ? want : num_sms());
+  }
   if (a.amax) {
     a.amax_whole = grid == 1;
-    if (grid > 1 && cudaMemsetAsync(a.amax, 0, sizeof(float), st) != cudaSuccess) return record_cuda(cudaGetLastError());
+    if (grid > 1) {
+      const te_status s = zero_amax(a.amax, st);
+      if (s != TE_OK) return s;
+    }
   }
-  switch (wpr) {
-    case 1: rmsnorm_kernel<T, 1, MX><<<grid, 256, 0, st>>>(a); break;
-    case 2: rmsnorm_kernel<T, 2, MX><<<grid, 256, 0, st>>>(a); break;
-    case 4: rmsnorm_kernel<T, 4, MX><<<grid, 256, 0, st>>>(a); break;
-    case 8: rmsnorm_kernel<T, 8, MX><<<grid, 256, 0, st>>>(a); break;
-    default: rmsnorm_kernel<T, 16, MX><<<grid, 512, 0, st>>>(a); break;
+  void (*kernel)(NormArgs) = wpr == 1   ? rmsnorm_kernel<T, 1, MX>
+                             : wpr == 2 ? rmsnorm_kernel<T, 2, MX>
+                             : wpr == 4 ? rmsnorm_kernel<T, 4, MX>
+                             : wpr == 8 ? rmsnorm_kernel<T, 8, MX>
+                                        : rmsnorm_kernel<T, 16, MX>;
+  const dim3 block(static_cast<unsigned>(32 * cta_warps(wpr)), 1, 1);
+  if (a.amax && grid > 1) {
+    const cudaError_t e = launch_dependent(kernel, dim3(static_cast<unsigned>(grid), 1, 1), block, 0, st, a);
+    if (e != cudaSuccess) return record_cuda(e);
+  } else {
+    kernel<<<grid, block, 0, st>>>(a);
   }
   count_launch();
   return launch_status();
@@ -523,18 +540,11 @@ te_status te_rmsnorm_bwd(const void* dy, const void* s, te_dtype in_dtype, int64
   count_launch();
   te_status st1 = launch_status();
   if (st1 != TE_OK) return st1;
-  // The sums' launch overlaps the end of the first kernel (programmatic dependent launch).
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((cols + 31) / 32), 1, 1);
-  cfg.blockDim = dim3(1024, 1, 1);
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, dgamma_kernel, static_cast<const float*>(workspace), grid, cols, dgamma) != cudaSuccess)
-    return record_cuda(cudaGetLastError());
+  // the sums' launch overlaps the end of the first kernel
+  const cudaError_t e = launch_dependent(dgamma_kernel, dim3(static_cast<unsigned>((cols + 31) / 32), 1, 1),
+                                         dim3(1024, 1, 1), 0, st, static_cast<const float*>(workspace), grid, cols,
+                                         dgamma);
+  if (e != cudaSuccess) return record_cuda(e);
   count_launch();
   return launch_status();
 }
