@@ -640,11 +640,12 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, EPI>::kThreads, 1)
     if (lane == 0) dev::bulk_wait0();
   }
 
-  if (args.pdl & kPdlWaitAtEnd) dev::pdl_wait();
   dev::tc_fence_before();
   __syncthreads();
   if (kPair) dev::cluster_sync();  // the leader's MMAs read the peer's shared memory until here
   dev::tc_fence_after();
+  // (only here: a warp that waits earlier holds up the loads of the whole CTA until the other kernel ends)
+  if (args.pdl & kPdlWaitAtEnd) dev::pdl_wait();
   if (warp == 1) {
     if (kPair) dev::tmem_dealloc_pair(tmem_base, C::kTmemCols);
     else dev::tmem_dealloc(tmem_base, C::kTmemCols);
