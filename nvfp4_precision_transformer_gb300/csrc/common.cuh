@@ -77,7 +77,7 @@ te_status make_tmap_2d_view64(CUtensorMap* map, const void* base, uint64_t width
 // D [M, N] = A B^T in BF16, as te_gemm_bf16 but with any M where it is not contiguous in an operand,
 // and any K where both operands are stored MN-major (no checks: the caller's).
 te_status gemm_bf16_tokens(const void* A, int a_mn, const void* B, int b_mn, void* D, te_dtype out, int accumulate,
-                           int64_t M, int64_t N, int64_t K, cudaStream_t st, int pdl = 0);
+                           int64_t M, int64_t N, int64_t K, cudaStream_t st, int pdl = 0, int max_split = 4);
 
 // Byte offset of logical scale (r, j) in the tensor-core block-scale layout;
 // kpad = number of scale columns after padding (multiple of 4).
@@ -123,7 +123,10 @@ __device__ __forceinline__ uint32_t ld_shared_cluster_u32(uint32_t caddr) {
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(caddr) : "memory");
   return v;
 }
-// All threads of both CTAs of the cluster.
+__device__ __forceinline__ void st_shared_cluster_v4(uint32_t caddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(caddr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+// All threads of every CTA of the cluster.
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }

@@ -148,6 +148,7 @@ struct GemmArgs {
   int accumulate;       // 1: D (fp32) += result, by TMA reduce-add
   uint32_t idesc;
   int a_mn, b_mn;       // BF16 only: operand stored [K, M] / [K, N]
+  int split;            // SPLIT: CTA pairs that share a tile's K
   int pdl;              // programmatic dependent launch: see kPdl*
   int raster;           // 1: the smaller operand's tiles vary fastest (see tile_coords)
   int* err;
@@ -156,6 +157,7 @@ struct GemmArgs {
 // Operands of the gated epilogues.
 struct GatedArgs {
   CUtensorMap h, g, u, q;   // kGated: h, g, u (bf16) and the 8-bit h; kDgrad: g and u, and dg (h) and du (q)
+  CUtensorMap q32;          // kGated: the 8-bit h in boxes of 32 columns, for slices of one chunk
   int F;                    // columns of h
   int act;
   int has_h, has_gu, has_q;
@@ -199,7 +201,13 @@ __device__ __forceinline__ void tile_coords(int tile, int m_tiles, int n_tiles, 
   nt = in_group / gm;
 }
 
-template <int KIND, int CG, int EPI>
+// SPLIT: few tiles for the GPU and a long contraction.  A cluster of args.split (2 or 4) CTA pairs has
+// one tile; each pair multiplies its part of K, and the accumulators are then added through
+// distributed shared memory: the epilogue warps send each slice of columns to the pair that finishes
+// it (half a tile, or a quarter), which adds the parts in the pairs' order after its own, so the
+// result does not depend on timing.  The received parts lie where the operands' ring was.
+// dX of 256 tokens, K = 1024, 2 F = 8192 (4 tiles on 76 pairs): 39 -> 19 us.
+template <int KIND, int CG, int EPI, bool SPLIT>
 __global__ void __launch_bounds__(Cfg<KIND, CG, EPI>::kThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                 const __grid_constant__ CUtensorMap tmD, const __grid_constant__ CUtensorMap tmSa,
@@ -231,10 +239,19 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, EPI>::kThreads, 1)
   const int lane = threadIdx.x & 31;
   const int num_tiles = args.m_tiles * args.n_tiles;   // m_tiles counts BM * CG rows
   // CTA pairs: rank 0 (the leader) issues the MMAs; both CTAs load, drain and store.
-  const uint32_t rank = kPair ? dev::cluster_ctarank() : 0u;
+  const uint32_t crank = kPair ? dev::cluster_ctarank() : 0u;
+  const uint32_t rank = SPLIT ? crank & 1u : crank;          // in the pair
+  const uint32_t lead = SPLIT ? crank & ~1u : 0u;            // the leader's rank in the cluster
+  const uint16_t pair_mask = static_cast<uint16_t>(3u << lead), lead_mask = static_cast<uint16_t>(1u << lead);
   const bool leader = rank == 0;
-  const int unit = kPair ? static_cast<int>(blockIdx.x >> 1) : static_cast<int>(blockIdx.x);
-  const int units = kPair ? static_cast<int>(gridDim.x >> 1) : static_cast<int>(gridDim.x);
+  const int part = SPLIT ? static_cast<int>(crank >> 1) : 0;
+  const int ctas = SPLIT ? 2 * args.split : CG;              // of a tile
+  const int unit = static_cast<int>(blockIdx.x) / ctas;
+  const int units = static_cast<int>(gridDim.x) / ctas;
+  // this pair's k-tiles
+  const int k_lo = SPLIT ? static_cast<int>(static_cast<int64_t>(args.k_tiles) * part / args.split) : 0;
+  const int k_num =
+      SPLIT ? static_cast<int>(static_cast<int64_t>(args.k_tiles) * (part + 1) / args.split) - k_lo : args.k_tiles;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -269,7 +286,7 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, EPI>::kThreads, 1)
   const uint32_t tmem_base = *tmem_slot;
   if (kPair && !leader && threadIdx.x == 0) {
     // the pair-wide allocation hands both CTAs the same columns; anything else is unusable
-    if (dev::ld_shared_cluster_u32(dev::mapa_shared(dev::smem_u32(tmem_slot), 0)) != tmem_base) {
+    if (dev::ld_shared_cluster_u32(dev::mapa_shared(dev::smem_u32(tmem_slot), lead)) != tmem_base) {
       dev::set_error(args.err, TE_ERR_UNSUPPORTED);
       *abort_flag = 1;
     }
@@ -323,12 +340,12 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, EPI>::kThreads, 1)
       for (int tile = unit; tile < num_tiles && ok; tile += units, ++it) {
         int mt, nt;
         tile_coords(tile, args.m_tiles, args.n_tiles, mt, nt, args.raster);
-        for (int kt0 = 0; kt0 < args.k_tiles; ++kt0) {
+        for (int kt0 = 0; kt0 < k_num; ++kt0) {
           // Every other tile of a CTA walks K backwards: the CTAs run their tiles in waves,
           // and a wave that starts where the previous one ended finds the panels' last
           // k-slices still in L2 (FP8, 12 layer shapes: DRAM traffic 2.16 -> 1.72 x the
           // operands, 1-2 % faster).  Only the order of the fp32 partial sums changes.
-          const int kt = (it & 1) ? args.k_tiles - 1 - kt0 : kt0;
+          const int kt = SPLIT ? k_lo + kt0 : ((it & 1) ? args.k_tiles - 1 - kt0 : kt0);
           if (!dev::mbar_wait<kPair>(&empty[stage], phase ^ 1u, abort_flag, args.err)) {
             ok = false;
             break;
@@ -346,8 +363,8 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, EPI>::kThreads, 1)
           // this CTA's B rows (kGated: the gate's or the up projection's)
           const int brow = EPI == kGated ? nt * 128 + static_cast<int>(rank) * gate_rows
                                          : nt * BN + static_cast<int>(rank) * C::kBRows;
-          const uint32_t full_c = dev::mapa_shared(dev::smem_u32(&full[stage]), 0);
-          const uint32_t sf_full_c = dev::mapa_shared(dev::smem_u32(&sf_full[stage]), 0);
+          const uint32_t full_c = dev::mapa_shared(dev::smem_u32(&full[stage]), lead);
+          const uint32_t sf_full_c = dev::mapa_shared(dev::smem_u32(&sf_full[stage]), lead);
           auto load = [&](uint8_t* dst, const CUtensorMap* map, int x, int y) {
             if (kPair) dev::tma_load_2d_pair(dst, map, full_c, x, y);
             else dev::tma_load_2d(dst, map, &full[stage], x, y);
@@ -430,7 +447,7 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, EPI>::kThreads, 1)
         }
         dev::tc_fence_after();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(as * BN);
-        for (int kt = 0; kt < args.k_tiles; ++kt) {
+        for (int kt = 0; kt < k_num; ++kt) {
           const int nstage = stage + 1 == kStages ? 0 : stage + 1;
           const uint32_t nphase = stage + 1 == kStages ? phase ^ 1u : phase;
           const uint32_t a_addr = dev::smem_u32(sA + stage * C::kABytes);
@@ -476,15 +493,15 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, EPI>::kThreads, 1)
               else dev::mma_mxf4nvf4(d_tmem, adesc, bdesc, args.idesc, sfa_t + 4 * ks, sfb_k, acc);
             }
           }
-          commit(&empty[stage], 3);   // frees the stage in both CTAs of a pair
+          commit(&empty[stage], pair_mask);   // frees the stage in both CTAs of a pair
           stage = nstage;
           phase = nphase;
         }
         if (!ok) break;
-        commit(&acc_full[as], 3);
+        commit(&acc_full[as], pair_mask);
       }
       // Every tcgen05 operation issued above completes before this commit fires.
-      commit(drain, 1);
+      commit(drain, lead_mask);
       volatile int dummy = 0;
       dev::mbar_wait(drain, 0, &dummy, args.err);
     }
@@ -536,9 +553,23 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, EPI>::kThreads, 1)
       tile_coords(tile, args.m_tiles, args.n_tiles, mt, nt, args.raster);
       const int as = it % C::kAccStages;
       const uint32_t aphase = static_cast<uint32_t>(it / C::kAccStages) & 1u;
+      // this warp's columns of the output, in chunks of 32 accumulator columns (kGated: of g, the
+      // same of u beside them)
+      int n0 = EPI == kGated ? nt * 128 + half * 64 : nt * BN + half * 128;
+      int chunks = EPI == kGated ? 2 : 4;
+      bool mine = true;      // SPLIT: whether this pair finishes (its slice of) these columns
+      const int sub = SPLIT && args.split == 4 ? part & 1 : 0;   // SPLIT in four: which half of the chunks
+      if constexpr (SPLIT) {
+        mine = args.split == 2 ? half == part : half == part >> 1;
+        if (args.split == 4) {
+          chunks /= 2;
+          n0 += 32 * chunks * sub;
+        }
+      }
       if constexpr (EPI == kDgrad)
-        est.begin(ep, (mt * CG + static_cast<int>(rank)) * BM + quarter * 32, nt * BN + half * 128, args.M);
-      if (!dev::mbar_wait<kPair>(&acc_full[as], aphase, abort_flag, args.err)) break;
+        if (mine) est.begin(ep, (mt * CG + static_cast<int>(rank)) * BM + quarter * 32, n0, chunks, args.M);
+      const bool acc_ok = dev::mbar_wait<kPair>(&acc_full[as], aphase, abort_flag, args.err);
+      if (!SPLIT && !acc_ok) break;
       dev::tc_fence_after();
       // kGated: 64 columns of g (acc[0..1]) and the same 64 of u (acc[2..3]); else 128 columns
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
@@ -550,6 +581,58 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, EPI>::kThreads, 1)
       dev::tmem_ld_wait();
 #pragma unroll
       for (int c = 0; c < 4; ++c) dev::reg_fence(acc[c]);
+      if constexpr (SPLIT) {
+        // every load of the cluster has landed and every MMA has read it: the rings are free
+        __syncwarp();
+        dev::cluster_sync();
+        const int per = chunks * (EPI == kGated ? 2 : 1);    // accumulator chunks of a slice
+        const uint32_t slot = dev::smem_u32(smem);
+        const int n_split = args.split;
+        // chunk c belongs to slice (half, own(c)), where it is the at(c)-th
+        auto own = [&](int c) { return n_split == 2 ? 0 : (EPI == kGated ? c & 1 : c >> 1); };
+        auto at = [&](int c) { return n_split == 2 ? c : (EPI == kGated ? c >> 1 : c & 1); };
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int owner = n_split == 2 ? half : 2 * half + own(c);
+          if (owner == part) continue;
+          const int from = part < owner ? part : part - 1;
+          const uint32_t dst = dev::mapa_shared(
+              slot + static_cast<uint32_t>(((from * 4 + quarter) * per + at(c)) * 4096 + lane * 16),
+              static_cast<uint32_t>(owner) * 2 + rank);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            dev::st_shared_cluster_v4(dst + 512u * i, acc[c][4 * i], acc[c][4 * i + 1], acc[c][4 * i + 2],
+                                      acc[c][4 * i + 3]);
+        }
+        dev::cluster_sync();
+        if (!acc_ok || !mine) break;
+        if (n_split == 4 && sub) {
+          // the slice's chunks to the front
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            acc[0][i] = EPI == kGated ? acc[1][i] : acc[2][i];
+            if (EPI != kGated) acc[1][i] = acc[3][i];
+            else acc[2][i] = acc[3][i];
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          // kGated keeps u in acc[2..3]; its slices of one chunk are acc[0] and acc[2]
+          const int k = n_split == 2 ? c : (EPI == kGated ? c >> 1 : c);
+          if (n_split == 4 && (EPI == kGated ? (c & 1) != 0 : c > 1)) continue;
+          for (int from = 0; from < n_split - 1; ++from) {
+            const uint4* src = reinterpret_cast<const uint4*>(smem + ((from * 4 + quarter) * per + k) * 4096 + lane * 16);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint4 v = src[32 * i];
+              acc[c][4 * i] = __float_as_uint(__uint_as_float(acc[c][4 * i]) + __uint_as_float(v.x));
+              acc[c][4 * i + 1] = __float_as_uint(__uint_as_float(acc[c][4 * i + 1]) + __uint_as_float(v.y));
+              acc[c][4 * i + 2] = __float_as_uint(__uint_as_float(acc[c][4 * i + 2]) + __uint_as_float(v.z));
+              acc[c][4 * i + 3] = __float_as_uint(__uint_as_float(acc[c][4 * i + 3]) + __uint_as_float(v.w));
+            }
+          }
+        }
+      }
       // Release: every epilogue warp of both CTAs arrives on the leader's accumulator-empty
       // barrier as soon as its own loads are complete.  In a pair the arrival is a
       // tcgen05.commit multicast to the leader (it tracks no tcgen05 operation of this
@@ -558,7 +641,7 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, EPI>::kThreads, 1)
       // single-accumulator kinds (NVFP4 / MXFP8 5-11 % faster at K = 4096).
       dev::tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
+      if (!SPLIT && lane == 0) {
         dev::tc_fence_after();
         if (kPair) dev::tc_commit_pair(&acc_empty[as], 1);
         else dev::mbar_arrive(&acc_empty[as]);
@@ -566,7 +649,7 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, EPI>::kThreads, 1)
 
       if constexpr (EPI == kGated) {
         est.template tile<KIND == kMXFP8>(ep, acc, alpha, (mt * CG + static_cast<int>(rank)) * BM + quarter * 32,
-                                          nt * 128 + half * 64, args.M);
+                                          n0, chunks, args.M);
         continue;
       }
       if constexpr (EPI == kDgrad) {
@@ -577,7 +660,6 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, EPI>::kThreads, 1)
       // Stage 32 rows x 64 bytes at a time in this warp's shared-memory box and write it
       // with a TMA store (the store clips rows >= M and columns >= N).
       const int m0 = (mt * CG + static_cast<int>(rank)) * BM + quarter * 32;
-      const int n0 = nt * BN + half * 128;
       // One 32-row x 64-byte box: lane-row words w[0..15] -> staging buffer -> TMA store.
       auto store_box = [&](const uint32_t (&w)[16], int nb) {
         if (lane == 0) dev::bulk_wait_read0();  // the previous box has left the staging buffer
@@ -604,7 +686,7 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, EPI>::kThreads, 1)
 #pragma unroll
           for (int bx = 0; bx < 8; ++bx) {
             const int nb = n0 + bx * 16;
-            if (nb >= args.N) break;
+            if (nb >= args.N || (SPLIT && bx >= 2 * chunks)) break;
             uint32_t w[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -617,7 +699,7 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, EPI>::kThreads, 1)
 #pragma unroll
           for (int bx = 0; bx < 4; ++bx) {
             const int nb = n0 + bx * 32;
-            if (nb >= args.N) break;
+            if (nb >= args.N || (SPLIT && bx >= chunks)) break;
             uint32_t w[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -640,6 +722,13 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, EPI>::kThreads, 1)
     if (lane == 0) dev::bulk_wait0();
   }
 
+  if constexpr (SPLIT) {
+    if (warp < 2) {   // the other warps' part in the epilogue's two barriers
+      __syncwarp();
+      dev::cluster_sync();
+      dev::cluster_sync();
+    }
+  }
   dev::tc_fence_before();
   __syncthreads();
   if (kPair) dev::cluster_sync();  // the leader's MMAs read the peer's shared memory until here
@@ -669,15 +758,18 @@ uint32_t make_idesc(int kind, uint32_t afmt, uint32_t bfmt, int m) {
   return d;
 }
 
-template <int KIND, int CG = 1, int EPI = kPlain>
+template <int KIND, int CG = 1, int EPI = kPlain, bool SPLIT = false>
 te_status launch_gemm(const void* A, const void* B, int64_t row_bytes, const uint8_t* sfa, const uint8_t* sfb,
                       int64_t sf_katoms, const float* alpha_a, const float* alpha_b, const float* bias, void* D,
                       te_dtype out, int accumulate, int64_t M, int64_t N, int64_t K, uint32_t afmt, uint32_t bfmt,
                       cudaStream_t st, int a_mn = 0, int b_mn = 0,
-                      const typename EpiParam<EPI>::type& ep = typename EpiParam<EPI>::type(), int pdl = 0) {
+                      const typename EpiParam<EPI>::type& ep = typename EpiParam<EPI>::type(), int pdl = 0,
+                      int max_split = 4) {
   using C = Cfg<KIND, CG, EPI>;
+  static_assert(!SPLIT || (CG == 2 && !C::kBlockScaled), "split K: pairs, BF16 and FP8");
   static bool attr_set[64] = {false};
-  static int max_clusters[64] = {0};
+  static int max_clusters[64] = {0};      // CTA pairs at once; SPLIT: clusters of two and of four pairs
+  static int max_clusters4[64] = {0};
   int dev_id = 0;
   cudaGetDevice(&dev_id);
   if (dev_id < 0 || dev_id >= 64) return TE_ERR_CUDA;
@@ -695,15 +787,27 @@ te_status launch_gemm(const void* A, const void* B, int64_t row_bytes, const uin
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (!attr_set[dev_id]) {
-    if (cudaFuncSetAttribute(gemm_kernel<KIND, CG, EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemTotal) !=
+    if (cudaFuncSetAttribute(gemm_kernel<KIND, CG, EPI, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemTotal) !=
         cudaSuccess)
       return record_cuda(cudaGetLastError());
     int n = num_sms() / CG;
-    if (CG > 1) {
+    if (SPLIT) {
+      for (int pairs = 4; pairs >= 2; pairs -= 2) {
+        attr[0].val.clusterDim.x = static_cast<unsigned>(2 * pairs);
+        cfg.gridDim = dim3(static_cast<unsigned>(num_sms() / (2 * pairs) * 2 * pairs), 1, 1);
+        int mc = 0;
+        if (cudaOccupancyMaxActiveClusters(&mc, gemm_kernel<KIND, CG, EPI, SPLIT>, &cfg) != cudaSuccess) {
+          cudaGetLastError();   // no such cluster: not taken
+          mc = 0;
+        }
+        (pairs == 4 ? max_clusters4 : max_clusters)[dev_id] = mc;
+      }
+      n = max_clusters[dev_id];
+    } else if (CG > 1) {
       // clusters that can be resident at once (a GPC may leave an SM unpaired)
       cfg.gridDim = dim3(CG * n, 1, 1);
       int mc = 0;
-      if (cudaOccupancyMaxActiveClusters(&mc, gemm_kernel<KIND, CG, EPI>, &cfg) != cudaSuccess || mc <= 0)
+      if (cudaOccupancyMaxActiveClusters(&mc, gemm_kernel<KIND, CG, EPI, SPLIT>, &cfg) != cudaSuccess || mc <= 0)
         return record_cuda(cudaGetLastError());
       n = mc < n ? mc : n;
     }
@@ -763,6 +867,19 @@ te_status launch_gemm(const void* A, const void* B, int64_t row_bytes, const uin
   g.pdl = pdl;
   g.err = err;
   const int tiles = g.m_tiles * g.n_tiles;
+  g.split = 1;
+  if constexpr (SPLIT) {
+    // Four pairs a tile where they all fit at once, else two, and where the k-tiles saved (0.27 us each)
+    // outweigh the exchange (4 us).  One pair / shared: gated BF16 128 tokens, K = 1024, F = 1024 (8 tiles
+    // of 16 k-tiles) 10.1 / 11.1 us, K = 1536 12.2 / 11.6, K = 2048 14.5 / 12.4; in two, 32 tiles of 32
+    // k-tiles 14.9 / 15.4, of 64 23.3 / 19.9, of 128 41.7 / 33.6.
+    if (max_split >= 4 && tiles <= max_clusters4[dev_id] && g.k_tiles >= 24) g.split = 4;
+    else if (max_split >= 2 && tiles <= max_clusters[dev_id] && g.k_tiles >= 48) g.split = 2;
+    if (g.split == 1)
+      return launch_gemm<KIND, CG, EPI, false>(A, B, row_bytes, sfa, sfb, sf_katoms, alpha_a, alpha_b, bias, D, out,
+                                               accumulate, M, N, K, afmt, bfmt, st, a_mn, b_mn, ep, pdl);
+    attr[0].val.clusterDim.x = static_cast<unsigned>(2 * g.split);
+  }
   // The fewest CTA pairs that keep the number of waves: every pair runs the same number of
   // tiles (within one), and the SMs left idle leave their share of the power budget to the
   // busy ones (FP8 / MXFP8 layer GEMMs 1.4-1.7 % faster than with one pair per two SMs).
@@ -771,9 +888,9 @@ te_status launch_gemm(const void* A, const void* B, int64_t row_bytes, const uin
     const int waves = (tiles + units - 1) / units;
     units = (tiles + waves - 1) / waves;
   }
-  cfg.gridDim = dim3(static_cast<unsigned>(CG * units), 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(SPLIT ? 2 * g.split * tiles : CG * units), 1, 1);
   cfg.numAttrs = (pdl & (kPdlWait | kPdlWaitAtEnd | kPdlOverlap)) ? 2 : 1;
-  if (cudaLaunchKernelEx(&cfg, gemm_kernel<KIND, CG, EPI>, ta, tb, td, tsa, tsb, g, ep) != cudaSuccess)
+  if (cudaLaunchKernelEx(&cfg, gemm_kernel<KIND, CG, EPI, SPLIT>, ta, tb, td, tsa, tsb, g, ep) != cudaSuccess)
     return record_cuda(cudaGetLastError());
   count_launch();
   return launch_status();

@@ -327,7 +327,8 @@ def test_dgrad_in_place():
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("T,K,Fc,N", [(1, 16, 16, 16), (3, 208, 272, 80), (33, 64, 144, 48), (100, 768, 128, 768),
-                                      (129, 80, 400, 64), (257, 96, 1040, 32), (1001, 48, 80, 112)])
+                                      (129, 80, 400, 64), (257, 96, 1040, 32), (1001, 48, 80, 112),
+                                      (70, 96, 784, 1552), (1700, 304, 1600, 1600), (300, 400, 3200, 64)])
 @pytest.mark.parametrize("actk,dwt", [("silu", torch.bfloat16), ("gelu", torch.float32)])
 def test_bwd_bf16(T, K, Fc, N, actk, dwt):
     dy, w2, gu = _bwd_inputs(T, Fc, N)
@@ -369,6 +370,33 @@ def test_streams_graphs_and_repeats():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(h, o["h"].t)
+
+
+# contractions long enough for a tile to be shared by two or four CTA pairs, with few tiles (four), more
+# (two), ragged edges, and parts of unequal length
+SHARED = [(70, 3216, 16), (100, 3200, 144), (129, 4112, 272), (300, 6160, 1600), (513, 3216, 400), (65, 8208, 128)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,K,Fc", SHARED)
+@pytest.mark.parametrize("kind,actk,outs,fmt", [("bf16", "silu", ("h", "gu"), "e4m3"), ("fp8", "gelu", ("h", "gu", "q"), "e4m3"),
+                                                ("fp8", "silu", ("q",), "e5m2")])
+def test_shared_contraction(T, K, Fc, kind, actk, outs, fmt):
+    _check_forward(kind, T, K, Fc, actk, outs, fmt)
+    # and the same bits every time
+    x, w, o = _forward(kind, T, K, Fc, actk, outs, fmt=fmt)
+    _, _, p = _forward(kind, T, K, Fc, actk, outs, fmt=fmt, xw=(x, w))
+    for k in ("h", "gu", "q"):
+        if o.get(k):
+            assert torch.equal(o[k].t, p[k].t)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,Fc,N", [(1, 16, 3216), (70, 272, 3200), (300, 144, 4112), (300, 2640, 6160)])
+@pytest.mark.parametrize("actk", ["silu", "gelu"])
+def test_shared_contraction_dgrad(T, Fc, N, actk):
+    d, w, gu, o = _dgrad("fp8", T, Fc, N, actk)
+    _check_dgu(o.np(), d.v, w.v.T, gu.cpu().double().numpy(), actk, N)
 
 
 @pytest.mark.gpu
