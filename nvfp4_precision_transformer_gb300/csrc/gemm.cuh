@@ -83,13 +83,14 @@ struct Cfg {
   static constexpr int kBRows = BN / CG;                      // B rows staged by one CTA
   static constexpr bool kBlockScaled = KIND >= kMXFP8;
   // Staging of the epilogue per warp: 2 KB boxes of 32 rows x 64 bytes.  kGated writes up to seven
-  // boxes a tile through two of them; kDgrad holds a g box and a u box twice.
-  static constexpr int kStgBytes = EPI == kPlain ? 2048 : (EPI == kGated ? 4096 : 8192);
+  // boxes a tile through two of them; kDgrad holds a g box and a u box (twice, with a stage less, was
+  // slower where it matters: 15872 tokens, N = 4096, F = 16384 FP8 841 / 740 us, BF16 1296 / 1270; N = 768,
+  // F = 2048 73 / 79).
+  static constexpr int kStgBytes = EPI == kPlain ? 2048 : 4096;
   // Stages: what 227 KB hold beside the staging.
   static constexpr int kStages = !kPair ? (KIND == kNVFP4 ? 3 : 4)
                                         : (EPI == kPlain   ? (KIND == kNVFP4 ? 5 : 6)
-                                           : EPI == kGated ? (kBlockScaled ? 5 : 6)
-                                                           : (kBlockScaled ? 4 : 5));
+                                                            : (kBlockScaled ? 5 : 6));
   static constexpr int kAccStages = kBlockScaled ? 1 : 2;
   // The scale copies (NVFP4 12, MXFP8 3 per k-tile) go out from copier warps of their own,
   // so the tensor pipe overlaps them with the MMAs (pairs: NVFP4 +12 %, MXFP8 +11 %).  One
@@ -117,7 +118,7 @@ struct Cfg {
   static constexpr int kSmemSfb = kSmemSfa + kStages * kSfaBytes;
   static constexpr int kSmemStage = kSmemSfb + kStages * kSfbBytes;      // epilogue staging
   static constexpr int kSmemBar = kSmemStage + kEpiWarps * kStgBytes;
-  static constexpr int kEpiBars = EPI == kDgrad ? 2 * kEpiWarps : 0;      // a barrier per warp and g / u buffer
+  static constexpr int kEpiBars = EPI == kDgrad ? kEpiWarps : 0;          // a barrier per warp for its g and u
   static constexpr int kBarBytes = EPI == kDgrad ? 384 : 256;
   static constexpr int kSmemTotal = kSmemBar + kBarBytes + 1024;  // barriers + alignment slack
   static_assert((4 * kStages + 5 + kEpiBars) * 8 + 8 <= kBarBytes, "barrier area");
@@ -231,7 +232,7 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, EPI>::kThreads, 1)
   uint64_t* drain = acc_empty + 2;
   uint64_t* sf_ready = drain + 1;  // [kStages]: the stage's scale factors are in TMEM
   uint64_t* sf_full = sf_ready + kStages;   // [kStages]: the stage's scale atoms have landed (block-scaled kinds)
-  uint64_t* epi_bar = sf_full + kStages;    // kDgrad: [kEpiWarps][2], the warp's g and u boxes have landed
+  uint64_t* epi_bar = sf_full + kStages;    // kDgrad: [kEpiWarps], the warp's g and u boxes have landed
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(epi_bar + C::kEpiBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -546,7 +547,7 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, EPI>::kThreads, 1)
     const float alpha = (args.alpha_a ? __ldg(args.alpha_a) : 1.0f) * (args.alpha_b ? __ldg(args.alpha_b) : 1.0f);
     typename EpiState<EPI>::type est;
     if constexpr (EPI == kGated) est.init(ep, stg, lane);
-    if constexpr (EPI == kDgrad) est.init(stg, epi_bar + 2 * (warp - 2), lane);
+    if constexpr (EPI == kDgrad) est.init(stg, epi_bar + (warp - 2), lane);
     int it = 0;
     for (int tile = unit; tile < num_tiles; tile += units, ++it) {
       int mt, nt;

@@ -203,7 +203,7 @@ def test_few_tokens(T, K, Fc, kind, outs, fmt):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T", [5, 200])
+@pytest.mark.parametrize("T", [5, 40, 200])
 @pytest.mark.parametrize("fx,fw", [("e4m3", "e5m2"), ("e5m2", "e4m3"), ("e5m2", "e5m2")])
 def test_fp8_operand_formats(T, fx, fw):
     a, b = _inputs(T, 208, 144, 5)
