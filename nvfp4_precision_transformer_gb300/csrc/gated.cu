@@ -1,6 +1,6 @@
 // Entry points of the gated feed-forward projections: h = act(x Wg^T) * (x Wu^T) in one kernel, and
 // its backward pass.  The kernels are gemm_kernel with the gated epilogues (gemm.cuh).
-#include "gated_stream.cuh"
+#include "gated_stream_block.cuh"
 
 namespace te {
 namespace {
@@ -144,6 +144,17 @@ te_status te_gated_gemm_mxfp8(const uint8_t* x, te_dtype fx, const uint8_t* sx, 
   if ((s = check_operands(x, w)) != TE_OK) return s;
   if ((s = check_operands(sx, sw)) != TE_OK) return s;
   if (!aligned16(h) || !aligned16(gu) || !aligned16(q_h) || !aligned16(s_h)) return TE_ERR_ALIGN;
+  if (T <= kStrMaxTokens) {
+    DecodeArgs a = {x, w, static_cast<int>(T), static_cast<int>(K), static_cast<int>(F), act};
+    a.h = static_cast<__nv_bfloat16*>(h);
+    a.gu = static_cast<__nv_bfloat16*>(gu);
+    a.q = q_h;
+    a.sx = sx;
+    a.sw = sw;
+    a.s_kpad = (K / 32 + 3) / 4 * 4;
+    a.s_h = s_h;
+    return launch_stream_block<kMXFP8>(a, fp8_code(fx), fp8_code(fw), static_cast<cudaStream_t>(stream));
+  }
   GatedArgs ep = {};
   if ((s = bf16_outputs(&ep, h, gu, T, F, act)) != TE_OK) return s;
   if (q_h) {
@@ -168,6 +179,15 @@ te_status te_gated_gemm_nvfp4(const uint8_t* x, const uint8_t* sx, const float* 
   if ((s = check_operands(x, w)) != TE_OK) return s;
   if ((s = check_operands(sx, sw)) != TE_OK) return s;
   if (!aligned16(h) || !aligned16(gu)) return TE_ERR_ALIGN;
+  if (T <= kStrMaxTokens) {
+    DecodeArgs a = {x, w, static_cast<int>(T), static_cast<int>(K), static_cast<int>(F), act, gx, gw};
+    a.h = static_cast<__nv_bfloat16*>(h);
+    a.gu = static_cast<__nv_bfloat16*>(gu);
+    a.sx = sx;
+    a.sw = sw;
+    a.s_kpad = (K / 16 + 15) / 16 * 16;
+    return launch_stream_block<kNVFP4>(a, 1u, 1u, static_cast<cudaStream_t>(stream));
+  }
   GatedArgs ep = {};
   if ((s = bf16_outputs(&ep, h, gu, T, F, act)) != TE_OK) return s;
   return launch_gemm<kNVFP4, 2, kGated>(x, w, K / 2, sx, sw, (K / 16 + 15) / 16 * 4, gx, gw, nullptr, nullptr, TE_BF16,

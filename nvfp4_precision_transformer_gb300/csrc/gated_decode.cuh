@@ -36,6 +36,12 @@ struct DecodeArgs {
   int q_e5m2;
   unsigned int* amax;
   float* scale_inv;
+  // block-scaled operands (gated_stream_block.cuh): scales in the tensor-core layout, their padded
+  // columns, and those of an MXFP8 h
+  const uint8_t* sx;
+  const uint8_t* sw;
+  int64_t s_kpad;
+  uint8_t* s_h;
 };
 
 __device__ __forceinline__ uint4 ld_stream(const uint8_t* p) {

@@ -203,6 +203,35 @@ def test_few_tokens(T, K, Fc, kind, outs, fmt):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,K,Fc", [(1, 4128, 1280), (8, 8256, 128), (5, 160, 4992), (2, 64, 2560), (9, 4128, 128),
+                                    (7, 13696, 128)])
+@pytest.mark.parametrize("kind,actk,outs", [("mxfp8", "silu", ("q",)), ("mxfp8", "gelu", ("h", "gu", "q")),
+                                            ("mxfp8", "silu", ("gu",)), ("nvfp4", "gelu", ("h", "gu"))])
+def test_few_tokens_block_scaled(T, K, Fc, kind, actk, outs):
+    """Several steps of the streaming kernels, more runs of columns than SMs, and lengths past what they hold."""
+    _check_forward(kind, T, K, Fc, actk, outs)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [3, 40])
+@pytest.mark.parametrize("fx,fw", [("e4m3", "e5m2"), ("e5m2", "e4m3"), ("e5m2", "e5m2")])
+def test_mxfp8_operand_formats(T, fx, fw):
+    a, b = _inputs(T, 224, 128, 5)
+    ops = []
+    for v, f in ((a, fx), (b, fw)):
+        q, sc = Q.mxfp8_quantize(v.astype(np.float32), f)
+        ops.append((_dev(q), _dev(_tiles(sc, 4)), Q.mxfp8_dequant(q, sc, f)))
+    (x, sx, xv), (w, sw, wv) = ops
+    h = Out(T, 128)
+    te.te_gated_gemm_mxfp8(x, sx, w, sw, te.ACT_SILU, h=h.t, fx=FMT[fx], fw=FMT[fw])
+    torch.cuda.synchronize()
+    h64, g64, u64 = gated(xv, wv, "silu")
+    S = np.abs(xv) @ np.abs(wv).T * (228 * E23)
+    err = _sizes(g64, u64, S[:, :128], S[:, 128:], "silu")
+    assert np.all(np.abs(h.np() - h64) <= BF * (np.abs(h64) + err) + err)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T", [5, 40, 200])
 @pytest.mark.parametrize("fx,fw", [("e4m3", "e5m2"), ("e5m2", "e4m3"), ("e5m2", "e5m2")])
 def test_fp8_operand_formats(T, fx, fw):
