@@ -5,7 +5,8 @@
  *   per-tensor amax -> DelayedScaling / CurrentScaling scale update ->
  *   saturating FP8 cast / MXFP8 / NVFP4 block quantizers (row-wise and
  *   column-wise copies from one read) -> tensor-core GEMMs (tcgen05 + TMEM,
- *   TMA-fed) with the dequantization scale and bias applied in the epilogue.
+ *   TMA-fed) with the dequantization scale and bias applied in the epilogue;
+ *   beside them RMSNorm with 8-bit outputs and the gated feed-forward projections.
  *
  * Conventions shared by every entry point
  *  - All tensor pointers are DEVICE pointers owned by the caller (for example
@@ -338,7 +339,10 @@ te_status te_gemm_nvfp4(const uint8_t* A, const uint8_t* sA, const float* gA, co
  *   h  bf16 [T, F];   gu bf16 [T, 2 F]: g, then u -- what the backward pass keeps.
  * K % 16 == 0 and F % 16 == 0 (BF16, FP8); K % 32 == 0 and F % 128 == 0 (MXFP8, NVFP4: the
  * two halves of w start at whole 128-row groups of the scale layout).  T = 0 is a no-op but
- * for the amax and 1 / scale. */
+ * for the amax and 1 / scale.  Which kernel a call takes goes by its sizes alone (few tokens
+ * have kernels of their own), and sums run in a fixed order, so the same call gives the same
+ * bits every time.  The first call on a device looks up attributes and addresses: make it
+ * before any stream capture. */
 enum { TE_ACT_SILU = 0, TE_ACT_GELU = 1 };
 
 te_status te_gated_gemm_bf16(const void* x, const void* w, int act, void* h, void* gu, int64_t T, int64_t K, int64_t F,

@@ -3,8 +3,9 @@
 The compute lives in ``libte_gb300.so`` (hand-written CUDA for sm_103a behind
 the C ABI in ``include/te_gb300.h``); this package is the thin Python side:
 ``_lib`` binds the C entry points by name, ``linear`` composes them into the
-per-recipe linear-layer steps (Fprop / Dgrad / Wgrad) and ``shapes`` derives
-the GEMM shapes of a transformer layer from its configuration.
+per-recipe linear-layer steps (Fprop / Dgrad / Wgrad), ``gated`` into the gated
+feed-forward block (RMSNorm, gated projections, down projection) and ``shapes``
+derives the GEMM shapes of a transformer layer from its configuration.
 """
 from ._lib import (  # noqa: F401
     ACT_GELU, ACT_SILU, ALGO_MAX, ALGO_MOST_RECENT, BF16, K_MAJOR, MN_MAJOR, E2M1, E4M3, E5M2, E8M0, F32, NVFP4_2D, NVFP4_RHT_COL, NVFP4_SR, UE4M3,
