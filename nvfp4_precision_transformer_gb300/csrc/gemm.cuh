@@ -205,8 +205,7 @@ __device__ __forceinline__ void tile_coords(int tile, int m_tiles, int n_tiles, 
 // SPLIT: few tiles for the GPU and a long contraction.  A cluster of args.split (2 or 4) CTA pairs has
 // one tile; each pair multiplies its part of K, and the accumulators are then added through
 // distributed shared memory: the epilogue warps send each slice of columns to the pair that finishes
-// it (half a tile, or a quarter), which adds the parts in the pairs' order after its own, so the
-// result does not depend on timing.  The received parts lie where the operands' ring was.
+// it, which adds the parts in the pairs' order after its own, so the result does not depend on timing.  The received parts lie where the operands' ring was.
 // dX of 256 tokens, K = 1024, 2 F = 8192 (4 tiles on 76 pairs): 39 -> 19 us.
 template <int KIND, int CG, int EPI, bool SPLIT>
 __global__ void __launch_bounds__(Cfg<KIND, CG, EPI>::kThreads, 1)
@@ -558,14 +557,17 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, EPI>::kThreads, 1)
       // same of u beside them)
       int n0 = EPI == kGated ? nt * 128 + half * 64 : nt * BN + half * 128;
       int chunks = EPI == kGated ? 2 : 4;
-      bool mine = true;      // SPLIT: whether this pair finishes (its slice of) these columns
-      const int sub = SPLIT && args.split == 4 ? part & 1 : 0;   // SPLIT in four: which half of the chunks
+      // SPLIT: the slice of them that this pair finishes.  Of every warp's columns each of two pairs takes
+      // one half, each of four a quarter (kGated, whose warps have two chunks of h: a half of one half of
+      // the warps), so that as many warps as can have some share the epilogue's latency.
+      bool mine = true;
+      int sub = 0;
       if constexpr (SPLIT) {
-        mine = args.split == 2 ? half == part : half == part >> 1;
-        if (args.split == 4) {
-          chunks /= 2;
-          n0 += 32 * chunks * sub;
-        }
+        const bool by_half = EPI == kGated && args.split == 4;
+        mine = !by_half || half == part >> 1;
+        sub = by_half ? part & 1 : part;
+        chunks /= by_half ? 2 : args.split;
+        n0 += 32 * chunks * sub;
       }
       if constexpr (EPI == kDgrad)
         if (mine) est.begin(ep, (mt * CG + static_cast<int>(rank)) * BM + quarter * 32, n0, chunks, args.M);
@@ -586,20 +588,22 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, EPI>::kThreads, 1)
         // every load of the cluster has landed and every MMA has read it: the rings are free
         __syncwarp();
         dev::cluster_sync();
-        const int per = chunks * (EPI == kGated ? 2 : 1);    // accumulator chunks of a slice
-        const uint32_t slot = dev::smem_u32(smem);
         const int n_split = args.split;
-        // chunk c belongs to slice (half, own(c)), where it is the at(c)-th
-        auto own = [&](int c) { return n_split == 2 ? 0 : (EPI == kGated ? c & 1 : c >> 1); };
-        auto at = [&](int c) { return n_split == 2 ? c : (EPI == kGated ? c >> 1 : c & 1); };
+        const bool by_half = EPI == kGated && n_split == 4;
+        const int per = EPI == kGated ? 2 : 4 / n_split;     // accumulator chunks of a slice
+        const int senders = by_half ? 4 : 8;                 // warps of a CTA with a slice for one pair
+        const int who = by_half ? quarter : warp - 2;
+        const uint32_t slot = dev::smem_u32(smem);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const int owner = n_split == 2 ? half : 2 * half + own(c);
+          // chunk c goes to pair `owner`, where it is the at-th of its slice
+          const int owner = EPI == kGated ? (by_half ? 2 * half : 0) + (c & 1) : (n_split == 2 ? c >> 1 : c);
+          const int at = EPI == kGated ? c >> 1 : (n_split == 2 ? c & 1 : 0);
           if (owner == part) continue;
           const int from = part < owner ? part : part - 1;
-          const uint32_t dst = dev::mapa_shared(
-              slot + static_cast<uint32_t>(((from * 4 + quarter) * per + at(c)) * 4096 + lane * 16),
-              static_cast<uint32_t>(owner) * 2 + rank);
+          const uint32_t dst =
+              dev::mapa_shared(slot + static_cast<uint32_t>(((from * senders + who) * per + at) * 4096 + lane * 16),
+                               static_cast<uint32_t>(owner) * 2 + rank);
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             dev::st_shared_cluster_v4(dst + 512u * i, acc[c][4 * i], acc[c][4 * i + 1], acc[c][4 * i + 2],
@@ -607,29 +611,31 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, EPI>::kThreads, 1)
         }
         dev::cluster_sync();
         if (!acc_ok || !mine) break;
-        if (n_split == 4 && sub) {
-          // the slice's chunks to the front
+        // the slice's chunks to the front (kGated: g's to acc[0], u's to acc[2])
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            acc[0][i] = EPI == kGated ? acc[1][i] : acc[2][i];
-            if (EPI != kGated) acc[1][i] = acc[3][i];
-            else acc[2][i] = acc[3][i];
+        for (int i = 0; i < 32; ++i) {
+          if (EPI == kGated) {
+            if (sub) acc[0][i] = acc[1][i], acc[2][i] = acc[3][i];
+          } else if (n_split == 2) {
+            if (sub) acc[0][i] = acc[2][i], acc[1][i] = acc[3][i];
+          } else {
+            acc[0][i] = sub == 0 ? acc[0][i] : (sub == 1 ? acc[1][i] : (sub == 2 ? acc[2][i] : acc[3][i]));
           }
         }
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          // kGated keeps u in acc[2..3]; its slices of one chunk are acc[0] and acc[2]
-          const int k = n_split == 2 ? c : (EPI == kGated ? c >> 1 : c);
-          if (n_split == 4 && (EPI == kGated ? (c & 1) != 0 : c > 1)) continue;
+        for (int k = 0; k < 2; ++k) {
+          if (k >= per) break;
           for (int from = 0; from < n_split - 1; ++from) {
-            const uint4* src = reinterpret_cast<const uint4*>(smem + ((from * 4 + quarter) * per + k) * 4096 + lane * 16);
+            const uint4* src =
+                reinterpret_cast<const uint4*>(smem + ((from * senders + who) * per + k) * 4096 + lane * 16);
+            uint32_t(&d)[32] = acc[EPI == kGated ? 2 * k : k];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const uint4 v = src[32 * i];
-              acc[c][4 * i] = __float_as_uint(__uint_as_float(acc[c][4 * i]) + __uint_as_float(v.x));
-              acc[c][4 * i + 1] = __float_as_uint(__uint_as_float(acc[c][4 * i + 1]) + __uint_as_float(v.y));
-              acc[c][4 * i + 2] = __float_as_uint(__uint_as_float(acc[c][4 * i + 2]) + __uint_as_float(v.z));
-              acc[c][4 * i + 3] = __float_as_uint(__uint_as_float(acc[c][4 * i + 3]) + __uint_as_float(v.w));
+              d[4 * i] = __float_as_uint(__uint_as_float(d[4 * i]) + __uint_as_float(v.x));
+              d[4 * i + 1] = __float_as_uint(__uint_as_float(d[4 * i + 1]) + __uint_as_float(v.y));
+              d[4 * i + 2] = __float_as_uint(__uint_as_float(d[4 * i + 2]) + __uint_as_float(v.z));
+              d[4 * i + 3] = __float_as_uint(__uint_as_float(d[4 * i + 3]) + __uint_as_float(v.w));
             }
           }
         }
@@ -871,9 +877,9 @@ te_status launch_gemm(const void* A, const void* B, int64_t row_bytes, const uin
   g.split = 1;
   if constexpr (SPLIT) {
     // Four pairs a tile where they all fit at once, else two, and where the k-tiles saved (0.27 us each)
-    // outweigh the exchange (4 us).  One pair / shared: gated BF16 128 tokens, K = 1024, F = 1024 (8 tiles
+    // outweigh the exchange (3 us).  One pair / shared: gated BF16 128 tokens, K = 1024, F = 1024 (8 tiles
     // of 16 k-tiles) 10.1 / 11.1 us, K = 1536 12.2 / 11.6, K = 2048 14.5 / 12.4; in two, 32 tiles of 32
-    // k-tiles 14.9 / 15.4, of 64 23.3 / 19.9, of 128 41.7 / 33.6.
+    // k-tiles 14.9 / 15.4, of 64 23.3 / 19.0, of 128 41.7 / 32.9.
     if (max_split >= 4 && tiles <= max_clusters4[dev_id] && g.k_tiles >= 24) g.split = 4;
     else if (max_split >= 2 && tiles <= max_clusters[dev_id] && g.k_tiles >= 48) g.split = 2;
     if (g.split == 1)
