@@ -182,6 +182,9 @@ def fp8_gemm_traffic():
         h = hashlib.sha256()
         for name in ("gemm.cu", "common.cuh"):
             h.update(open(os.path.join(csrc, name), "rb").read())
+        for name in ("gemm.cuh", "gated_epilogue.inc"):   # where the kernel has parts of its own there
+            if os.path.exists(os.path.join(csrc, name)):
+                h.update(open(os.path.join(csrc, name), "rb").read())
         if d.get("kernel_source_sha256_prefix") != h.hexdigest()[:16]:
             return None, d.get("algorithmic_bytes_per_launch"), "GEMM source changed since the ncu capture"
         return int(d["traffic_bytes_per_launch"]), int(d["algorithmic_bytes_per_launch"]), d.get("how")

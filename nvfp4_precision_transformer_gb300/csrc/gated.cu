@@ -1,5 +1,6 @@
 // Entry points of the gated feed-forward projections: h = act(x Wg^T) * (x Wu^T) in one kernel, and
-// its backward pass.  The kernels are gemm_kernel with the gated epilogues (gemm.cuh).
+// its backward pass.  The kernels are gemm_kernel with the gated epilogues (gemm.cuh), and those of
+// gated_decode.cuh, gated_stream.cuh and gated_stream_block.cuh for few tokens.
 #include "gated_stream_block.cuh"
 
 namespace te {

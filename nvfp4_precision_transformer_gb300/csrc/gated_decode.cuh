@@ -7,8 +7,7 @@
 // same thread.  The 16 warps split K; a lane's 16-byte piece of a weight row is loaded straight into
 // the registers the instruction reads it from (the order of k inside a block is free, as long as x
 // follows it), four blocks ahead and across units, so the loads never wait for the arithmetic.
-// Each unit ends with the warps' partial sums added in warp
-// order through shared memory.  One token, K = 4096, F = 16384: BF16 42.7 us (6.28 TB/s; gemm_kernel,
+// Each unit ends with the warps' partial sums added in warp order through shared memory.  One token, K = 4096, F = 16384: BF16 42.7 us (6.28 TB/s; gemm_kernel,
 // whose SMs all read the one line of x at the same time, 84.0), FP8 23.9 us (5.61 TB/s; 43.4).
 #pragma once
 
@@ -58,7 +57,7 @@ __device__ __forceinline__ uint4 ld_stream(const uint8_t* p) {
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1))
 template <int W, int X>
 __device__ __forceinline__ void mma_dec(float4& c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                          uint32_t b1) {
+                                        uint32_t b1) {
   if (W == kDecBF16) TE_DEC_MMA("m16n8k16.row.col.f32.bf16.bf16.f32");
   else if (W == kDecE4M3 && X == kDecE4M3) TE_DEC_MMA("m16n8k32.row.col.f32.e4m3.e4m3.f32");
   else if (W == kDecE4M3) TE_DEC_MMA("m16n8k32.row.col.f32.e4m3.e5m2.f32");

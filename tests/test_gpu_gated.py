@@ -278,6 +278,29 @@ def test_fp8_amax_keeps_nan_and_ignores_the_ragged_edge(T):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T", [3, 40, 70, 200])
+def test_rows_past_the_last_token_stay_out(T):
+    """A weight that is not finite makes the tile's rows past the last token NaN (zero times infinity):
+    they reach neither the amax nor the padding of the scales."""
+    a, b = _inputs(T, 64, 128, 4)
+    x, w = Operand(np.abs(a) + 0.1, "fp8"), Operand(b, "fp8", "e5m2")
+    w.q[5, 7] = 0x7C                                           # +inf in a gate row: g = +inf, h = +-inf
+    h, q, amax = Out(T, 128), Out(T, 128, dtype=torch.uint8), G.scalar(-1.0)
+    te.te_gated_gemm_fp8(x.q, te.E4M3, w.q, te.E5M2, x.inv, w.inv, te.ACT_SILU, h=h.t, q_h=q.t, h_scale=G.scalar(1.0),
+                         h_amax=amax)
+    torch.cuda.synchronize()
+    assert np.isinf(h.np()[:, 5]).all() and np.isfinite(np.delete(h.np(), 5, 1)).all()
+    assert np.isposinf(amax.item())
+    x, w = Operand(a, "mxfp8"), Operand(b, "mxfp8")
+    w.q[5, 7] = 0x7F                                           # NaN
+    q, s = Out(T, 128, dtype=torch.uint8), Out(te.te_scale_bytes(te.E8M0, T, 128), dtype=torch.uint8)
+    te.te_gated_gemm_mxfp8(x.q, x.s, w.q, w.s, te.ACT_SILU, q_h=q.t, s_h=s.t)
+    torch.cuda.synchronize()
+    raw = s.np()
+    assert int(raw.astype(np.int64).sum()) == int(te.te_scale_unswizzle(te.E8M0, T, 128, raw).astype(np.int64).sum())
+
+
+@pytest.mark.gpu
 def test_no_tokens():
     w = torch.zeros(64, 32, dtype=torch.bfloat16, device=G.DEV)
     x = torch.zeros(0, 32, dtype=torch.bfloat16, device=G.DEV)
