@@ -23,13 +23,10 @@ int num_sms();
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// *amax = 0 before kernels that atomicMax into it.  The zeroing is a launch of its own, but the kernel
-// after it, launched with launch_dependent(), runs beside it and waits (pdl_wait) only before its
-// atomics: a memset in its place costs the small calls 4 us (RMSNorm 1023 x 768 8.3 -> 4.4).
-te_status zero_amax(void* amax, cudaStream_t st);
-
-// Launch that may start before the kernel before it in the stream has ended; pdl_wait() in the kernel
-// waits for that one to be complete.
+// Programmatic dependent launch: a kernel launched this way may be set up before the kernel before it in
+// the stream has ended.  It calls pdl_wait(), which returns when that one is complete, before its first
+// access to global memory, and pdl_trigger() after that, so that the next one may be set up beside it
+// (RMSNorm 15872 x 4096 93.2 -> 91.9 us a call among others, its backward pass 83.6 -> 81.1).
 template <typename... Params, typename... Args>
 inline cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
                                     Args... args) {
@@ -45,6 +42,10 @@ inline cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 b
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
 }
+
+// *amax = 0 before kernels that atomicMax into it, as a dependent launch between two others: a memset
+// in its place costs the small calls 4 us (RMSNorm 1023 x 768 8.3 -> 4.7).
+te_status zero_amax(void* amax, cudaStream_t st);
 
 inline te_status launch_status() {
   cudaError_t e = cudaGetLastError();

@@ -83,8 +83,9 @@ te_status te_gated_gemm_bf16(const void* x, const void* w, int act, void* h, voi
   }
   GatedArgs ep = {};
   if ((s = bf16_outputs(&ep, h, gu, T, F, act)) != TE_OK) return s;
-  return launch_gemm<kBF16, 2, kGated, true>(x, w, K * 2, nullptr, nullptr, 0, nullptr, nullptr, nullptr, nullptr, TE_BF16, 0,
-                                       T, 2 * F, K, 1u, 1u, static_cast<cudaStream_t>(stream), 0, 0, ep);
+  return launch_gemm<kBF16, 2, kGated, true>(x, w, K * 2, nullptr, nullptr, 0, nullptr, nullptr, nullptr, nullptr,
+                                             TE_BF16, 0, T, 2 * F, K, 1u, 1u, static_cast<cudaStream_t>(stream), 0, 0, ep,
+                                             kPdlChain);
 }
 
 te_status te_gated_gemm_fp8(const uint8_t* x, te_dtype fx, const uint8_t* w, te_dtype fw, const float* x_scale_inv,
@@ -130,9 +131,9 @@ te_status te_gated_gemm_fp8(const uint8_t* x, te_dtype fx, const uint8_t* w, te_
     if (s != TE_OK) return s;
   }
   if (h_amax && (s = zero_amax(h_amax, st)) != TE_OK) return s;
-  return launch_gemm<kFP8, 2, kGated, true>(x, w, K, nullptr, nullptr, 0, x_scale_inv, w_scale_inv, nullptr, nullptr, TE_BF16,
-                                      0, T, 2 * F, K, fp8_code(fx), fp8_code(fw), st, 0, 0, ep,
-                                      h_amax ? kPdlOverlap : 0);
+  return launch_gemm<kFP8, 2, kGated, true>(x, w, K, nullptr, nullptr, 0, x_scale_inv, w_scale_inv, nullptr, nullptr,
+                                            TE_BF16, 0, T, 2 * F, K, fp8_code(fx), fp8_code(fw), st, 0, 0, ep,
+                                            kPdlChain);
 }
 
 te_status te_gated_gemm_mxfp8(const uint8_t* x, te_dtype fx, const uint8_t* sx, const uint8_t* w, te_dtype fw,
@@ -168,7 +169,7 @@ te_status te_gated_gemm_mxfp8(const uint8_t* x, te_dtype fx, const uint8_t* sx, 
   }
   return launch_gemm<kMXFP8, 2, kGated>(x, w, K, sx, sw, (K / 32 + 3) / 4, nullptr, nullptr, nullptr, nullptr, TE_BF16,
                                         0, T, 2 * F, K, fp8_code(fx), fp8_code(fw), static_cast<cudaStream_t>(stream), 0,
-                                        0, ep);
+                                        0, ep, kPdlChain);
 }
 
 te_status te_gated_gemm_nvfp4(const uint8_t* x, const uint8_t* sx, const float* gx, const uint8_t* w, const uint8_t* sw,
@@ -192,7 +193,7 @@ te_status te_gated_gemm_nvfp4(const uint8_t* x, const uint8_t* sx, const float* 
   GatedArgs ep = {};
   if ((s = bf16_outputs(&ep, h, gu, T, F, act)) != TE_OK) return s;
   return launch_gemm<kNVFP4, 2, kGated>(x, w, K / 2, sx, sw, (K / 16 + 15) / 16 * 4, gx, gw, nullptr, nullptr, TE_BF16,
-                                        0, T, 2 * F, K, 1u, 1u, static_cast<cudaStream_t>(stream), 0, 0, ep);
+                                        0, T, 2 * F, K, 1u, 1u, static_cast<cudaStream_t>(stream), 0, 0, ep, kPdlChain);
 }
 
 te_status te_gated_dgrad_fp8(const uint8_t* dy, te_dtype fd, const uint8_t* w2, te_dtype fw, const float* dy_scale_inv,
@@ -207,7 +208,7 @@ te_status te_gated_dgrad_fp8(const uint8_t* dy, te_dtype fd, const uint8_t* w2, 
   if ((s = dgrad_args(&ep, gu, dgu, T, F, act)) != TE_OK) return s;
   return launch_gemm<kFP8, 2, kDgrad, true>(dy, w2, N, nullptr, nullptr, 0, dy_scale_inv, w2_scale_inv, nullptr, nullptr,
                                       TE_BF16, 0, T, F, N, fp8_code(fd), fp8_code(fw),
-                                      static_cast<cudaStream_t>(stream), 0, 0, ep);
+                                      static_cast<cudaStream_t>(stream), 0, 0, ep, kPdlChain);
 }
 
 te_status te_gated_dgrad_mxfp8(const uint8_t* dy, te_dtype fd, const uint8_t* sd, const uint8_t* w2, te_dtype fw,
@@ -221,8 +222,8 @@ te_status te_gated_dgrad_mxfp8(const uint8_t* dy, te_dtype fd, const uint8_t* sd
   GatedArgs ep = {};
   if ((s = dgrad_args(&ep, gu, dgu, T, F, act)) != TE_OK) return s;
   return launch_gemm<kMXFP8, 2, kDgrad>(dy, w2, N, sd, sw, (N / 32 + 3) / 4, nullptr, nullptr, nullptr, nullptr, TE_BF16,
-                                        0, T, F, N, fp8_code(fd), fp8_code(fw), static_cast<cudaStream_t>(stream), 0, 0,
-                                        ep);
+                                        0, T, F, N, fp8_code(fd), fp8_code(fw), static_cast<cudaStream_t>(stream), 0,
+                                        0, ep, kPdlChain);
 }
 
 te_status te_gated_dgrad_nvfp4(const uint8_t* dy, const uint8_t* sd, const float* gd, const uint8_t* w2,
@@ -236,7 +237,7 @@ te_status te_gated_dgrad_nvfp4(const uint8_t* dy, const uint8_t* sd, const float
   GatedArgs ep = {};
   if ((s = dgrad_args(&ep, gu, dgu, T, F, act)) != TE_OK) return s;
   return launch_gemm<kNVFP4, 2, kDgrad>(dy, w2, N / 2, sd, sw, (N / 16 + 15) / 16 * 4, gd, gw, nullptr, nullptr, TE_BF16,
-                                        0, T, F, N, 1u, 1u, static_cast<cudaStream_t>(stream), 0, 0, ep);
+                                        0, T, F, N, 1u, 1u, static_cast<cudaStream_t>(stream), 0, 0, ep, kPdlChain);
 }
 
 te_status te_gated_bwd_bf16(const void* x, const void* w, const void* w2, const void* dy, const void* gu, int act,
@@ -263,8 +264,8 @@ te_status te_gated_bwd_bf16(const void* x, const void* w, const void* w2, const 
   // dh = dY W2 (W2 [N, F] read MN-major), dg and du in its epilogue.  The next kernel is set up while
   // this one drains, and dW, which reads the same dGU, runs beside dX wherever that leaves SMs idle
   // (1001 tokens, K = N = 768, F = 2048: dX has 12 tiles for 76 pairs).
-  s = launch_gemm<kBF16, 2, kDgrad, true>(dy, w2, N * 2, nullptr, nullptr, 0, nullptr, nullptr, nullptr, nullptr, TE_BF16, 0,
-                                    T, F, N, 1u, 1u, st, 0, 1, ep, (dx || dw) ? kPdlTrigger : 0);
+  s = launch_gemm<kBF16, 2, kDgrad, true>(dy, w2, N * 2, nullptr, nullptr, 0, nullptr, nullptr, nullptr, nullptr,
+                                          TE_BF16, 0, T, F, N, 1u, 1u, st, 0, 1, ep, kPdlChain);
   // dX = dGU W (W [2 F, K] MN-major);  dW = dGU^T X (both MN-major).  dX's tiles are shared between CTA
   // pairs only as far as dW's fit beside them, where they fit at all.
   int share = 4;
@@ -274,9 +275,9 @@ te_status te_gated_bwd_bf16(const void* x, const void* w, const void* w2, const 
     if (tx <= free_pairs) share = 4 * tx <= free_pairs ? 4 : (2 * tx <= free_pairs ? 2 : 1);
   }
   if (s == TE_OK && dx)
-    s = gemm_bf16_tokens(dgu, 0, w, 1, dx, TE_BF16, 0, T, K, 2 * F, st, kPdlWait | (dw ? kPdlTrigger : 0), share);
+    s = gemm_bf16_tokens(dgu, 0, w, 1, dx, TE_BF16, 0, T, K, 2 * F, st, kPdlChain, share);
   if (s == TE_OK && dw)
-    s = gemm_bf16_tokens(dgu, 1, x, 1, dw, dw_dtype, accumulate, 2 * F, K, T, st, dx ? kPdlWaitAtEnd : kPdlWait);
+    s = gemm_bf16_tokens(dgu, 1, x, 1, dw, dw_dtype, accumulate, 2 * F, K, T, st, dx ? kPdlWaitAtEnd : kPdlChain);
   return s;
 }
 

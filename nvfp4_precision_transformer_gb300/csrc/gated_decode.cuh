@@ -1,14 +1,16 @@
 // The gated projections of a few tokens (decoding): the two weight halves are read once from HBM and
 // everything else is small, so the kernel is a stream over w.
 //
-// One persistent CTA of 16 warps per SM keeps x in shared memory.  A unit of work is eight columns
-// of h: eight gate rows and the eight up rows beside them are one 16-row operand of
-// mma.m16n8 (tokens are its n), whose accumulator layout puts g and u of the same element in the
-// same thread.  The 16 warps split K; a lane's 16-byte piece of a weight row is loaded straight into
-// the registers the instruction reads it from (the order of k inside a block is free, as long as x
-// follows it), four blocks ahead and across units, so the loads never wait for the arithmetic.
-// Each unit ends with the warps' partial sums added in warp order through shared memory.  One token, K = 4096, F = 16384: BF16 42.7 us (6.28 TB/s; gemm_kernel,
-// whose SMs all read the one line of x at the same time, 84.0), FP8 23.9 us (5.61 TB/s; 43.4).
+// One persistent CTA of 16 warps per SM keeps x in shared memory.  A unit of work is eight columns of
+// h: eight gate rows and the eight up rows beside them are one 16-row operand of mma.m16n8 (tokens
+// are its n), whose accumulator layout puts g and u of the same element in the same thread.  The 16
+// warps split K; a lane's 16-byte piece of a weight row is loaded straight into the registers the
+// instruction reads it from (the order of k inside a block is free, as long as x follows it), four
+// blocks ahead and across units, so the loads never wait for the arithmetic.  Each unit ends with the
+// warps' partial sums added in warp order through shared memory.
+//
+// One token, K = 4096, F = 16384: BF16 42.7 us (6.28 TB/s; gemm_kernel, whose SMs all read the one line
+// of x at the same time, 84.0), FP8 23.9 us (5.61 TB/s; 43.4).
 #pragma once
 
 #include "gemm.cuh"
@@ -102,6 +104,8 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1) gated_decode_kernel(DecodeA
       }
     }
   };
+  dev::pdl_wait();
+  dev::pdl_trigger();
   int unit = static_cast<int>(blockIdx.x);
   fetch(unit, 0);
 
@@ -154,7 +158,8 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1) gated_decode_kernel(DecodeA
         s.x += p.x, s.y += p.y, s.z += p.z, s.w += p.w;
       }
       const int f = unit * 8 + r;
-      const float2 g2 = __fmul2_rn(make_float2(s.x, s.y), both(alpha)), u2 = __fmul2_rn(make_float2(s.z, s.w), both(alpha));
+      const float2 g2 = __fmul2_rn(make_float2(s.x, s.y), both(alpha));
+      const float2 u2 = __fmul2_rn(make_float2(s.z, s.w), both(alpha));
       const float2 h2 = __fmul2_rn(gate_act(g2, a.act), u2);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -177,10 +182,7 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1) gated_decode_kernel(DecodeA
   }
   if (a.amax && warp < NT) {
     top = __reduce_max_sync(0xFFFFFFFFu, top);
-    if (lane == 0) {
-      dev::pdl_wait();   // its zeroing
-      atomicMax(a.amax, top);
-    }
+    if (lane == 0) atomicMax(a.amax, top);
   }
   if (a.scale_inv && blockIdx.x == 0 && threadIdx.x == 0) *a.scale_inv = __fdiv_rn(1.0f, qs);
 }
@@ -204,11 +206,9 @@ te_status launch_decode(const DecodeArgs& a, cudaStream_t st) {
   if (a.amax) {
     const te_status s = zero_amax(a.amax, st);
     if (s != TE_OK) return s;
-    const cudaError_t e = launch_dependent(gated_decode_kernel<W, X, NT>, g, block, smem, st, a);
-    if (e != cudaSuccess) return record_cuda(e);
-  } else {
-    gated_decode_kernel<W, X, NT><<<g, block, smem, st>>>(a);
   }
+  const cudaError_t e = launch_dependent(gated_decode_kernel<W, X, NT>, g, block, smem, st, a);
+  if (e != cudaSuccess) return record_cuda(e);
   count_launch();
   return launch_status();
 }

@@ -1,18 +1,20 @@
-// The gated projections of up to 64 tokens that the kernel of gated_decode.cuh does not take: still a stream over the weights, but with too much matrix
-// work for mma.sync.  The operands change places against gemm_kernel: the weights are the 128-row
-// operand of the MMA (64 gate rows and the 64 up rows beside them) and the tokens its N (32 or 64), so
-// a stage is 16 KB of weights and 4 or 8 KB of x, and ten (eight) of them fit where gemm_kernel has
-// six with as much x as weights: 160 KB of weights in flight per SM.  One CTA per SM, no pairs: tiles
-// of 64 columns of h, and a CTA with one tile more than another has that much more of the bandwidth
-// at the end.
+// The gated projections of up to 64 tokens that the kernel of gated_decode.cuh does not take: still a
+// stream over the weights, but with too much matrix work for mma.sync.  The operands change places
+// against gemm_kernel: the weights are the 128-row operand of the MMA (64 gate rows and the 64 up rows
+// beside them) and the tokens its N (32 or 64), so a stage is 16 KB of weights and 4 or 8 KB of x, and
+// ten (eight) of them fit where gemm_kernel has six with as much x as weights: 160 KB of weights in
+// flight per SM.  One CTA per SM, no pairs: tiles of 64 columns of h, and a CTA with one tile more than
+// another has that much more of the bandwidth at the end.
 //
 // warp 0 TMA producer, warp 1 MMA issuer, warps 2-5 epilogue.  Accumulator lanes 0-63 hold g and 64-127
 // u of the tile's columns, tokens along the TMEM columns: the g warps hand the second half of the
 // tokens to the u warps through shared memory and get the first half's u back, and each thread then
-// has one column of h for half of the tokens; neighbouring lanes write neighbouring columns.
+// has one column of h for half of the tokens; neighbouring lanes write neighbouring columns.  (Tiles of
+// 128 columns without the exchange, as gated_stream_block.cuh has them, are as fast at F = 16384 but
+// leave more SMs idle at smaller F: 24 tokens, K = F = 4096 BF16 18.7 us here, 25.3 so.)
 //
-// 24 tokens, K = 4096, F = 16384: BF16 45.3 us (5.92 TB/s; gemm_kernel 51.5), FP8 25.6 us (5.24 TB/s;
-// 33.2); 64 tokens 47.9 / 52.5 and 27.9 / 30.1.  gemm_kernel's six stages turn round in about 1.7 us
+// 24 tokens, K = 4096, F = 16384: BF16 45.1 us (5.96 TB/s; gemm_kernel 51.5), FP8 25.6 us (5.25 TB/s;
+// 33.2); 64 tokens 48.2 / 52.5 and 28.0 / 30.1.  gemm_kernel's six stages turn round in about 1.7 us
 // (load, MMA, commit), which bounds what an SM can have in flight; these turn round in less and are more.
 #pragma once
 
@@ -82,6 +84,8 @@ __global__ void __launch_bounds__(kStrThreads, 1)
   __syncthreads();
   dev::tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  dev::pdl_wait();
+  dev::pdl_trigger();
 
   if (warp == 0) {
     if (lane == 0) {
@@ -212,10 +216,7 @@ __global__ void __launch_bounds__(kStrThreads, 1)
     }
     if (a.amax) {
       top = __reduce_max_sync(0xFFFFFFFFu, top);
-      if (lane == 0) {
-        dev::pdl_wait();   // its zeroing
-        atomicMax(a.amax, top);
-      }
+      if (lane == 0) atomicMax(a.amax, top);
     }
     if (a.scale_inv && blockIdx.x == 0 && threadIdx.x == 64) *a.scale_inv = __fdiv_rn(1.0f, qs);
   }
@@ -253,15 +254,10 @@ te_status launch_stream(const DecodeArgs& a, uint32_t xfmt, uint32_t wfmt, cudaS
   const int tiles = (a.F + 63) / 64;
   const dim3 g(static_cast<unsigned>(tiles < num_sms() ? tiles : num_sms()), 1, 1), block(kStrThreads, 1, 1);
   const int k_tiles = static_cast<int>((row_bytes + 127) / 128);
-  if (a.amax) {
-    s = zero_amax(a.amax, st);
-    if (s != TE_OK) return s;
-    const cudaError_t e =
-        launch_dependent(gated_stream_kernel<KIND, NP>, g, block, C::kSmemTotal, st, tw, tx, a, idesc, k_tiles, err);
-    if (e != cudaSuccess) return record_cuda(e);
-  } else {
-    gated_stream_kernel<KIND, NP><<<g, block, C::kSmemTotal, st>>>(tw, tx, a, idesc, k_tiles, err);
-  }
+  if (a.amax && (s = zero_amax(a.amax, st)) != TE_OK) return s;
+  const cudaError_t e =
+      launch_dependent(gated_stream_kernel<KIND, NP>, g, block, C::kSmemTotal, st, tw, tx, a, idesc, k_tiles, err);
+  if (e != cudaSuccess) return record_cuda(e);
   count_launch();
   return launch_status();
 }

@@ -127,12 +127,12 @@ struct Cfg {
   static_assert(kSmemTotal <= 232448, "shared memory budget");
 };
 
-// Programmatic dependent launch, for kernels that follow one another inside one call (bits of pdl):
-// the kernel waits for the one before it after its set-up; it lets the next one start once it has
-// itself begun (after that wait); it waits for the one before it only at its end, being independent
-// of its results, so that what follows in the stream finds both complete.
-// kPdlOverlap: launched beside the one before it, on whose results only the epilogue's end waits.
-constexpr int kPdlWait = 1, kPdlTrigger = 2, kPdlWaitAtEnd = 4, kPdlOverlap = 8;
+// Programmatic dependent launch (bits of pdl): the kernel waits for the one before it after its set-up;
+// it lets the next one be set up once it has itself begun (after that wait); it waits for the one
+// before it only at its end, being independent of its results, so that what follows in the stream
+// finds both complete.
+constexpr int kPdlWait = 1, kPdlTrigger = 2, kPdlWaitAtEnd = 4;
+constexpr int kPdlChain = kPdlWait | kPdlTrigger;
 
 struct GemmArgs {
   int M, N, K;
@@ -896,7 +896,7 @@ te_status launch_gemm(const void* A, const void* B, int64_t row_bytes, const uin
     units = (tiles + waves - 1) / waves;
   }
   cfg.gridDim = dim3(static_cast<unsigned>(SPLIT ? 2 * g.split * tiles : CG * units), 1, 1);
-  cfg.numAttrs = (pdl & (kPdlWait | kPdlWaitAtEnd | kPdlOverlap)) ? 2 : 1;
+  cfg.numAttrs = (pdl & (kPdlWait | kPdlWaitAtEnd)) ? 2 : 1;
   if (cudaLaunchKernelEx(&cfg, gemm_kernel<KIND, CG, EPI, SPLIT>, ta, tb, td, tsa, tsb, g, ep) != cudaSuccess)
     return record_cuda(cudaGetLastError());
   count_launch();

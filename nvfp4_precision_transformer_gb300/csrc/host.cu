@@ -28,6 +28,7 @@ int current_device() {
 }
 
 __global__ void zero_amax_kernel(unsigned int* amax) {
+  te::dev::pdl_wait();
   te::dev::pdl_trigger();
   *amax = 0u;
 }
@@ -61,7 +62,9 @@ te_status record_cuda(cudaError_t e) {
 void count_launch(int n) { g_launches.fetch_add(static_cast<uint64_t>(n)); }
 
 te_status zero_amax(void* amax, cudaStream_t st) {
-  zero_amax_kernel<<<1, 1, 0, st>>>(static_cast<unsigned int*>(amax));
+  const cudaError_t e = launch_dependent(zero_amax_kernel, dim3(1, 1, 1), dim3(1, 1, 1), 0, st,
+                                         static_cast<unsigned int*>(amax));
+  if (e != cudaSuccess) return record_cuda(e);
   count_launch();
   return launch_status();
 }

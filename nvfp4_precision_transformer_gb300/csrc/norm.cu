@@ -128,6 +128,8 @@ __global__ void __launch_bounds__(32 * cta_warps(WPR), WPR <= 8 ? 2 : 1) rmsnorm
   const T* x = static_cast<const T*>(a.x);
   const T* res = static_cast<const T*>(a.res);
   const int col0 = (wr * kCh * 32 + lane) * 8;   // chunk t starts at col0 + 256 t
+  dev::pdl_wait();
+  dev::pdl_trigger();
   const float sc = !MX && a.scale ? *a.scale : 1.0f;
   unsigned int lmax = 0;
 
@@ -226,7 +228,6 @@ __global__ void __launch_bounds__(32 * cta_warps(WPR), WPR <= 8 ? 2 : 1) rmsnorm
         if (a.amax_whole) {
           *a.amax = lmax;
         } else {
-          dev::pdl_wait();   // its zeroing
           atomicMax(a.amax, lmax);
         }
       }
@@ -250,7 +251,7 @@ struct NormBwdArgs {
 // second row would take the registers of the second CTA's warps: 151 us without, 152 with it
 // (30000 x 768: 59.9 / 74.7), four chunks 217.
 template <typename T, int WPR, int CH>
-__global__ void __launch_bounds__(32 * cta_warps(WPR), WPR <= 8 ? 2 : 1) rmsnorm_bwd_kernel(const NormBwdArgs a) {
+__global__ void __launch_bounds__(32 * cta_warps(WPR), WPR <= 8 ? 2 : 1) rmsnorm_bwd_kernel(NormBwdArgs a) {
   constexpr int GR = cta_rows(WPR);
   constexpr bool kAhead = sizeof(T) == 2 && CH == 2;   // the next row's loads before this row is reduced
   __shared__ float red[GR][2][WPR];
@@ -288,6 +289,7 @@ __global__ void __launch_bounds__(32 * cta_warps(WPR), WPR <= 8 ? 2 : 1) rmsnorm
       }
     }
   };
+  dev::pdl_wait();
   RowRegs cur;
   int64_t row = static_cast<int64_t>(blockIdx.x) * GR + grp;
   if (kAhead) load(cur, row);
@@ -363,6 +365,7 @@ __global__ void __launch_bounds__(1024) dgamma_kernel(const float* __restrict__ 
   __shared__ float part[32][33];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   dev::pdl_wait();   // the partial sums are complete
+  dev::pdl_trigger();
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   float t = 0.0f;
   if (c < C) {
@@ -418,28 +421,23 @@ te_status launch_norm(NormArgs& a, cudaStream_t st) {
                              : wpr == 8 ? rmsnorm_kernel<T, 8, MX>
                                         : rmsnorm_kernel<T, 16, MX>;
   const dim3 block(static_cast<unsigned>(32 * cta_warps(wpr)), 1, 1);
-  if (a.amax && grid > 1) {
-    const cudaError_t e = launch_dependent(kernel, dim3(static_cast<unsigned>(grid), 1, 1), block, 0, st, a);
-    if (e != cudaSuccess) return record_cuda(e);
-  } else {
-    kernel<<<grid, block, 0, st>>>(a);
-  }
+  const cudaError_t e = launch_dependent(kernel, dim3(static_cast<unsigned>(grid), 1, 1), block, 0, st, a);
+  if (e != cudaSuccess) return record_cuda(e);
   count_launch();
   return launch_status();
 }
 
 template <typename T>
-void launch_norm_bwd(const NormBwdArgs& a, int wpr, int grid, cudaStream_t st) {
+cudaError_t launch_norm_bwd(const NormBwdArgs& a, int wpr, int grid, cudaStream_t st) {
+  void (*kernel)(NormBwdArgs) = wpr == 1                    ? rmsnorm_bwd_kernel<T, 1, 2>
+                                : wpr == 2                  ? rmsnorm_bwd_kernel<T, 2, 2>
+                                : wpr == 4                  ? rmsnorm_bwd_kernel<T, 4, 2>
+                                : wpr == 8                  ? rmsnorm_bwd_kernel<T, 8, 2>
+                                : a.cols <= 16 * 32 * 8 * 2 ? rmsnorm_bwd_kernel<T, 16, 2>
+                                                            : rmsnorm_bwd_kernel<T, 16, 4>;
   const size_t smem = static_cast<size_t>(cta_rows(wpr) - 1) * static_cast<size_t>(a.cols) * sizeof(float);
-  switch (wpr) {
-    case 1: rmsnorm_bwd_kernel<T, 1, 2><<<grid, 256, smem, st>>>(a); break;
-    case 2: rmsnorm_bwd_kernel<T, 2, 2><<<grid, 256, smem, st>>>(a); break;
-    case 4: rmsnorm_bwd_kernel<T, 4, 2><<<grid, 256, smem, st>>>(a); break;
-    case 8: rmsnorm_bwd_kernel<T, 8, 2><<<grid, 256, smem, st>>>(a); break;
-    default:
-      if (a.cols <= 16 * 32 * 8 * 2) rmsnorm_bwd_kernel<T, 16, 2><<<grid, 512, smem, st>>>(a);
-      else rmsnorm_bwd_kernel<T, 16, 4><<<grid, 512, smem, st>>>(a);
-  }
+  return launch_dependent(kernel, dim3(static_cast<unsigned>(grid), 1, 1),
+                          dim3(static_cast<unsigned>(32 * cta_warps(wpr)), 1, 1), smem, st, a);
 }
 
 te_status check_norm(const void* x, te_dtype in, int64_t rows, int64_t cols, const float* gamma, float eps,
@@ -537,13 +535,12 @@ te_status te_rmsnorm_bwd(const void* dy, const void* s, te_dtype in_dtype, int64
   NormBwdArgs a = {static_cast<const __nv_bfloat16*>(dy), s, dres, gamma, rsigma, rows, cols, dx, workspace};
   const int wpr = warps_per_row(cols, 2);
   const int grid = walk_grid(rows, wpr);
-  if (in_dtype == TE_BF16) launch_norm_bwd<__nv_bfloat16>(a, wpr, grid, st);
-  else launch_norm_bwd<float>(a, wpr, grid, st);
+  cudaError_t e = in_dtype == TE_BF16 ? launch_norm_bwd<__nv_bfloat16>(a, wpr, grid, st)
+                                      : launch_norm_bwd<float>(a, wpr, grid, st);
+  if (e != cudaSuccess) return record_cuda(e);
   count_launch();
-  te_status st1 = launch_status();
-  if (st1 != TE_OK) return st1;
   // the sums' launch overlaps the end of the first kernel
-  const cudaError_t e = launch_dependent(dgamma_kernel, dim3(static_cast<unsigned>((cols + 31) / 32), 1, 1),
+  e = launch_dependent(dgamma_kernel, dim3(static_cast<unsigned>((cols + 31) / 32), 1, 1),
                                          dim3(1024, 1, 1), 0, st, static_cast<const float*>(workspace), grid, cols,
                                          dgamma);
   if (e != cudaSuccess) return record_cuda(e);

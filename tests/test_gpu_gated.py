@@ -424,6 +424,61 @@ def test_streams_graphs_and_repeats():
         assert torch.equal(h, o["h"].t)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 24, 300])
+def test_calls_set_up_early_wait_for_their_inputs(T):
+    """Kernels are set up before what is in front of them in the stream has ended: a chain of norm, gated
+    projections (all kinds of kernels) and a copy, whose input comes late, by an event, from another
+    stream, from a copy or a memset, gives the bits that it gives one call at a time; eagerly and in a graph."""
+    K, Fc = 512, 1280
+    g = torch.Generator().manual_seed(3)
+    xs = [torch.randn(T, K, generator=g).bfloat16().to(G.DEV) for _ in range(4)]
+    w = torch.randn(2 * Fc, K, generator=g).mul(0.06).to(G.DEV)
+    gamma, w16, one = torch.ones(K, device=G.DEV), w.bfloat16(), G.scalar(1.0)
+    w8 = (w * 64).to(torch.float8_e4m3fn).view(torch.uint8)
+    x, y = torch.zeros_like(xs[0]), torch.empty_like(xs[0])
+    q, hq, amax, qamax = G.u8(T, K), G.u8(T, Fc), G.scalar(), G.scalar()
+    h16 = torch.empty(T, Fc, dtype=torch.bfloat16, device=G.DEV)
+    side, late = torch.cuda.Stream(), torch.zeros(64 << 20, device=G.DEV)
+
+    def chain(i, how):
+        if how == "event":
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                late.add_(1.0)                                  # some 0.1 ms before x arrives
+                x.copy_(xs[i])
+            torch.cuda.current_stream().wait_stream(side)
+        elif how == "copy":
+            late.add_(1.0)
+            x.copy_(xs[i])
+        else:
+            x.copy_(xs[i])
+            late.zero_()
+        te.te_rmsnorm_fp8(x, gamma, 1e-5, te.E4M3, one, q, y=y, amax_out=qamax)
+        te.te_gated_gemm_bf16(y, w16, te.ACT_SILU, h=h16)
+        te.te_gated_gemm_fp8(q, te.E4M3, w8, te.E4M3, one, one, te.ACT_SILU, q_h=hq, h_scale=one, h_amax=amax)
+        x.zero_()                                               # and nothing reads x afterwards
+        return [t.clone() for t in (y, h16, hq, amax, qamax)]
+
+    want = []
+    for i in range(4):
+        want.append(chain(i, "plain"))
+        torch.cuda.synchronize()
+    for how in ("plain", "event", "copy"):
+        got = [chain(i % 4, how) for i in range(12)]
+        torch.cuda.synchronize()
+        for i, outs in enumerate(got):
+            assert all(torch.equal(a, b) for a, b in zip(outs, want[i % 4])), (how, i)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = [chain(i, how) for i in range(4)]
+        for _ in range(3):
+            graph.replay()
+        torch.cuda.synchronize()
+        for i, outs in enumerate(got):
+            assert all(torch.equal(a, b) for a, b in zip(outs, want[i])), (how, i, "graph")
+
+
 # contractions long enough for a tile to be shared by two or four CTA pairs, with few tiles (four), more
 # (two), ragged edges, and parts of unequal length
 SHARED = [(70, 3216, 16), (100, 3200, 144), (129, 4112, 272), (300, 6160, 1600), (513, 3216, 400), (65, 8208, 128)]
