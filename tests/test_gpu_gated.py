@@ -380,7 +380,8 @@ def test_dgrad_in_place():
 @pytest.mark.gpu
 @pytest.mark.parametrize("T,K,Fc,N", [(1, 16, 16, 16), (3, 208, 272, 80), (33, 64, 144, 48), (100, 768, 128, 768),
                                       (129, 80, 400, 64), (257, 96, 1040, 32), (1001, 48, 80, 112),
-                                      (70, 96, 784, 1552), (1700, 304, 1600, 1600), (300, 400, 3200, 64)])
+                                      (70, 96, 784, 1552), (1700, 304, 1600, 1600), (300, 400, 3200, 64),
+                                      (2100, 2304, 2560, 1600)])
 @pytest.mark.parametrize("actk,dwt", [("silu", torch.bfloat16), ("gelu", torch.float32)])
 def test_bwd_bf16(T, K, Fc, N, actk, dwt):
     dy, w2, gu = _bwd_inputs(T, Fc, N)
@@ -481,7 +482,9 @@ def test_calls_set_up_early_wait_for_their_inputs(T):
 
 # contractions long enough for a tile to be shared by two or four CTA pairs, with few tiles (four), more
 # (two), ragged edges, and parts of unequal length
-SHARED = [(70, 3216, 16), (100, 3200, 144), (129, 4112, 272), (300, 6160, 1600), (513, 3216, 400), (65, 8208, 128)]
+# and a last, partial wave behind full ones
+SHARED = [(70, 3216, 16), (100, 3200, 144), (129, 4112, 272), (300, 6160, 1600), (513, 3216, 400), (65, 8208, 128),
+          (2100, 3216, 1280), (1300, 6160, 2048)]
 
 
 @pytest.mark.gpu
@@ -507,7 +510,8 @@ def test_shared_contraction_dgrad(T, Fc, N, actk):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T,K,Fc,N", [(1001, 768, 2048, 768), (60, 64, 1040, 2048), (3000, 1024, 1024, 256)])
+@pytest.mark.parametrize("T,K,Fc,N", [(1001, 768, 2048, 768), (60, 64, 1040, 2048), (3000, 1024, 1024, 256),
+                                      (2100, 2304, 2560, 1600)])
 def test_bwd_overlap_and_graph(T, K, Fc, N):
     """dX and dW overlap and start while dGU's kernel drains: twenty calls in a row, eager and in a
     graph, give the bits that calls on their own give, and what follows in the stream sees both."""
