@@ -27,7 +27,9 @@ namespace {
   e -= 8;
   return max(-127, min(127, e));
 }
-[[maybe_unused]] __device__ __forceinline__ float mx_mult(int E) { return __uint_as_float(static_cast<uint32_t>(127 - E) << 23); }
+[[maybe_unused]] __device__ __forceinline__ float mx_mult(int E) {
+  return __uint_as_float(static_cast<uint32_t>(127 - E) << 23);
+}
 
 }  // namespace
 }  // namespace te

@@ -24,8 +24,8 @@ inline uint32_t f8_code(te_dtype f) { return f == TE_E5M2 ? 1u : 0u; }
 
 te_status gemm_bf16_tokens(const void* A, int a_mn, const void* B, int b_mn, void* D, te_dtype out, int accumulate,
                            int64_t M, int64_t N, int64_t K, cudaStream_t st, int pdl, int max_split) {
-  return launch_gemm<kBF16, 2, kPlain, true>(A, B, K * 2, nullptr, nullptr, 0, nullptr, nullptr, nullptr, D, out, accumulate, M, N, K,
-                               1u, 1u, st, a_mn, b_mn, NoEpiArgs(), pdl, max_split);
+  return launch_gemm<kBF16, 2, kPlain, true>(A, B, K * 2, nullptr, nullptr, 0, nullptr, nullptr, nullptr, D, out,
+                                             accumulate, M, N, K, 1u, 1u, st, a_mn, b_mn, NoEpiArgs(), pdl, max_split);
 }
 
 }  // namespace te

@@ -186,8 +186,8 @@ __global__ void __launch_bounds__(32 * cta_warps(WPR), WPR <= 8 ? 2 : 1) rmsnorm
         const int e = mx_exponent(__uint_as_float(m));
         mul = mx_mult(e);
         if (live && (lane & 3) == 0)
-          a.s_row[scale_offset(static_cast<uint64_t>(row), static_cast<uint64_t>(col >> 5), static_cast<uint64_t>(a.kpad))] =
-              static_cast<uint8_t>(e + 127);
+          a.s_row[scale_offset(static_cast<uint64_t>(row), static_cast<uint64_t>(col >> 5),
+                               static_cast<uint64_t>(a.kpad))] = static_cast<uint8_t>(e + 127);
       } else if (live) {
         lmax = max(lmax, m);
       }
