@@ -12,6 +12,7 @@ import ctypes
 import os
 
 import numpy as np
+import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libte_gb300.so")
@@ -120,19 +121,20 @@ def _ptr(t):
     return t.data_ptr()
 
 
+_bf16, _f32, _u8 = torch.bfloat16, torch.float32, torch.uint8
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
-        import torch
         # the handle alone: building a Stream object takes 3 us, as long as a small kernel
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
+        return _raw_stream(torch.cuda.current_device()) if _raw_stream else torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
 
 
 def _in_dtype(x):
-    import torch
     if x.dtype == torch.bfloat16:
         return BF16
     if x.dtype == torch.float32:
@@ -205,7 +207,7 @@ def _need(fn: str, name: str, t, dtype, shape, optional: bool = False):
         if optional:
             return None
         raise TypeError(f"{fn}: {name} is required")
-    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.is_cuda:
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
         return t.data_ptr()
     if t.dtype is not dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
         raise TypeError(f"{fn}: {name} is {t.dtype}, expected {dtype}")
@@ -244,38 +246,35 @@ def _nv_bytes(rows: int, cols: int) -> int:
 
 
 def _norm_operands(fn, x, gamma, residual, res_out, y, rsigma):
-    import torch
     if x.dim() != 2:
         raise ValueError(f"{fn}: x has shape {tuple(x.shape)}, expected [rows, cols]")
-    shape = x.shape
-    px = _need(fn, "x", x, (torch.bfloat16, torch.float32), shape)
-    dt = x.dtype
-    return (px, _in_dtype(x), shape[0], shape[1], _need(fn, "residual", residual, dt, shape, True),
-            _need(fn, "gamma", gamma, torch.float32, shape[1:]), _need(fn, "res_out", res_out, dt, shape, True),
-            _need(fn, "y", y, torch.bfloat16, shape, True), _need(fn, "rsigma", rsigma, torch.float32, shape[:1], True))
+    shape, dt = x.shape, x.dtype
+    rows, cols = shape
+    px = _need(fn, "x", x, dt if dt is _bf16 or dt is _f32 else (_bf16, _f32), shape)
+    return (px, F32 if dt is _f32 else BF16, rows, cols, _need(fn, "residual", residual, dt, shape, True),
+            _need(fn, "gamma", gamma, _f32, (cols,)), _need(fn, "res_out", res_out, dt, shape, True),
+            _need(fn, "y", y, _bf16, shape, True), _need(fn, "rsigma", rsigma, _f32, (rows,), True))
 
 
 def te_rmsnorm_fp8(x, gamma, eps: float, fmt: int, scale=None, q_row=None, residual=None, res_out=None, y=None,
                    rsigma=None, amax_out=None, scale_inv_out=None, stream=None):
     """RMSNorm of x (+ residual), its output in FP8 with a per-tensor scale (and / or y in bf16)."""
-    import torch
-    fn, f32 = "te_rmsnorm_fp8", torch.float32
+    fn = "te_rmsnorm_fp8"
     px, dt, r, c, pres, pg, pro, py, prs = _norm_operands(fn, x, gamma, residual, res_out, y, rsigma)
     _check(fn, lib().te_rmsnorm_fp8(
-        px, dt, r, c, pres, pg, float(eps), fmt, _need_n(fn, "scale", scale, f32, 1, True),
-        _need(fn, "q_row", q_row, torch.uint8, x.shape, True), py, pro, prs,
-        _need_n(fn, "amax_out", amax_out, f32, 1, True), _need_n(fn, "scale_inv_out", scale_inv_out, f32, 1, True),
+        px, dt, r, c, pres, pg, float(eps), fmt, _need_n(fn, "scale", scale, _f32, 1, True),
+        _need(fn, "q_row", q_row, _u8, x.shape, True), py, pro, prs,
+        _need_n(fn, "amax_out", amax_out, _f32, 1, True), _need_n(fn, "scale_inv_out", scale_inv_out, _f32, 1, True),
         _stream(stream)))
 
 
 def te_rmsnorm_mxfp8(x, gamma, eps: float, q_row, s_row, residual=None, res_out=None, y=None, rsigma=None, stream=None):
     """RMSNorm of x (+ residual), its output in MXFP8 (E4M3 codes, E8M0 scales in the tensor-core layout)."""
-    import torch
     fn = "te_rmsnorm_mxfp8"
     px, dt, r, c, pres, pg, pro, py, prs = _norm_operands(fn, x, gamma, residual, res_out, y, rsigma)
     _check(fn, lib().te_rmsnorm_mxfp8(
-        px, dt, r, c, pres, pg, float(eps), _need(fn, "q_row", q_row, torch.uint8, x.shape),
-        _need_n(fn, "s_row", s_row, torch.uint8, _mx_bytes(r, c)), py, pro, prs, _stream(stream)))
+        px, dt, r, c, pres, pg, float(eps), _need(fn, "q_row", q_row, _u8, x.shape),
+        _need_n(fn, "s_row", s_row, _u8, _mx_bytes(r, c)), py, pro, prs, _stream(stream)))
 
 
 def te_rmsnorm_bwd_workspace_bytes(rows: int, cols: int) -> int:
@@ -284,18 +283,17 @@ def te_rmsnorm_bwd_workspace_bytes(rows: int, cols: int) -> int:
 
 def te_rmsnorm_bwd(dy, s, gamma, rsigma, dx, dgamma, workspace, dres=None, stream=None):
     """Gradients of te_rmsnorm_*: dx (of x and of the residual) and dgamma."""
-    import torch
-    fn, f32 = "te_rmsnorm_bwd", torch.float32
+    fn = "te_rmsnorm_bwd"
     if s.dim() != 2:
         raise ValueError(f"{fn}: s has shape {tuple(s.shape)}, expected [rows, cols]")
     shape, dt = s.shape, s.dtype
-    ps = _need(fn, "s", s, (torch.bfloat16, f32), shape)
-    pw = _need_n(fn, "workspace", workspace, f32, 0)
+    ps = _need(fn, "s", s, (_bf16, _f32), shape)
+    pw = _need_n(fn, "workspace", workspace, _f32, 0)
     _check(fn, lib().te_rmsnorm_bwd(
-        _need(fn, "dy", dy, torch.bfloat16, shape), ps, _in_dtype(s), shape[0], shape[1],
-        _need(fn, "gamma", gamma, f32, shape[1:]), _need(fn, "rsigma", rsigma, f32, shape[:1]),
+        _need(fn, "dy", dy, _bf16, shape), ps, _in_dtype(s), shape[0], shape[1],
+        _need(fn, "gamma", gamma, _f32, shape[1:]), _need(fn, "rsigma", rsigma, _f32, shape[:1]),
         _need(fn, "dres", dres, dt, shape, True), _need(fn, "dx", dx, dt, shape),
-        _need(fn, "dgamma", dgamma, f32, shape[1:]), pw, workspace.numel() * 4, _stream(stream)))
+        _need(fn, "dgamma", dgamma, _f32, shape[1:]), pw, workspace.numel() * 4, _stream(stream)))
 
 
 def te_quantize_mxfp8(x, q_row=None, s_row=None, q_col=None, s_col=None, stream=None):
@@ -315,7 +313,6 @@ def te_quantize_nvfp4(x, flags: int = 0, rht_signs: int = 0, seed: int = 0, offs
 
 
 def _out_dtype(d):
-    import torch
     if d.dtype == torch.bfloat16:
         return BF16
     if d.dtype == torch.float32:
@@ -368,112 +365,104 @@ def _gated_shape(fn, x, w, packed: int = 1):
 
 def te_gated_gemm_bf16(x, w, act: int, h=None, gu=None, stream=None):
     """h = act(x Wg^T) * (x Wu^T) in bf16 and / or the pre-activations gu = [g, u]."""
-    import torch
-    fn, bf = "te_gated_gemm_bf16", torch.bfloat16
+    fn = "te_gated_gemm_bf16"
     T, K, F = _gated_shape(fn, x, w)
     _check(fn, lib().te_gated_gemm_bf16(
-        _need(fn, "x", x, bf, (T, K)), _need(fn, "w", w, bf, (2 * F, K)), act, _need(fn, "h", h, bf, (T, F), True),
-        _need(fn, "gu", gu, bf, (T, 2 * F), True), T, K, F, _stream(stream)))
+        _need(fn, "x", x, _bf16, (T, K)), _need(fn, "w", w, _bf16, (2 * F, K)), act,
+        _need(fn, "h", h, _bf16, (T, F), True), _need(fn, "gu", gu, _bf16, (T, 2 * F), True), T, K, F,
+        _stream(stream)))
 
 
 def te_gated_gemm_fp8(x, fx: int, w, fw: int, x_scale_inv, w_scale_inv, act: int, h=None, gu=None, q_h=None,
                       h_fmt: int = E4M3, h_scale=None, h_amax=None, h_scale_inv=None, stream=None):
     """te_gated_gemm_bf16 on per-tensor scaled FP8 operands; q_h is h in FP8 for the down projection."""
-    import torch
-    fn, bf, u8, f32 = "te_gated_gemm_fp8", torch.bfloat16, torch.uint8, torch.float32
+    fn = "te_gated_gemm_fp8"
     T, K, F = _gated_shape(fn, x, w)
     _check(fn, lib().te_gated_gemm_fp8(
-        _need(fn, "x", x, u8, (T, K)), fx, _need(fn, "w", w, u8, (2 * F, K)), fw,
-        _need_n(fn, "x_scale_inv", x_scale_inv, f32, 1), _need_n(fn, "w_scale_inv", w_scale_inv, f32, 1), act,
-        _need(fn, "h", h, bf, (T, F), True), _need(fn, "gu", gu, bf, (T, 2 * F), True),
-        _need(fn, "q_h", q_h, u8, (T, F), True), h_fmt, _need_n(fn, "h_scale", h_scale, f32, 1, True),
-        _need_n(fn, "h_amax", h_amax, f32, 1, True), _need_n(fn, "h_scale_inv", h_scale_inv, f32, 1, True), T, K, F,
+        _need(fn, "x", x, _u8, (T, K)), fx, _need(fn, "w", w, _u8, (2 * F, K)), fw,
+        _need_n(fn, "x_scale_inv", x_scale_inv, _f32, 1), _need_n(fn, "w_scale_inv", w_scale_inv, _f32, 1), act,
+        _need(fn, "h", h, _bf16, (T, F), True), _need(fn, "gu", gu, _bf16, (T, 2 * F), True),
+        _need(fn, "q_h", q_h, _u8, (T, F), True), h_fmt, _need_n(fn, "h_scale", h_scale, _f32, 1, True),
+        _need_n(fn, "h_amax", h_amax, _f32, 1, True), _need_n(fn, "h_scale_inv", h_scale_inv, _f32, 1, True), T, K, F,
         _stream(stream)))
 
 
 def te_gated_gemm_mxfp8(x, sx, w, sw, act: int, h=None, gu=None, q_h=None, s_h=None, fx: int = E4M3, fw: int = E4M3,
                         stream=None):
     """te_gated_gemm_bf16 on MXFP8 operands; q_h, s_h are h in MXFP8 for the down projection."""
-    import torch
-    fn, bf, u8 = "te_gated_gemm_mxfp8", torch.bfloat16, torch.uint8
+    fn = "te_gated_gemm_mxfp8"
     T, K, F = _gated_shape(fn, x, w)
     _check(fn, lib().te_gated_gemm_mxfp8(
-        _need(fn, "x", x, u8, (T, K)), fx, _need_n(fn, "sx", sx, u8, _mx_bytes(T, K)),
-        _need(fn, "w", w, u8, (2 * F, K)), fw, _need_n(fn, "sw", sw, u8, _mx_bytes(2 * F, K)), act,
-        _need(fn, "h", h, bf, (T, F), True), _need(fn, "gu", gu, bf, (T, 2 * F), True),
-        _need(fn, "q_h", q_h, u8, (T, F), True), _need_n(fn, "s_h", s_h, u8, _mx_bytes(T, F), True), T, K, F,
+        _need(fn, "x", x, _u8, (T, K)), fx, _need_n(fn, "sx", sx, _u8, _mx_bytes(T, K)),
+        _need(fn, "w", w, _u8, (2 * F, K)), fw, _need_n(fn, "sw", sw, _u8, _mx_bytes(2 * F, K)), act,
+        _need(fn, "h", h, _bf16, (T, F), True), _need(fn, "gu", gu, _bf16, (T, 2 * F), True),
+        _need(fn, "q_h", q_h, _u8, (T, F), True), _need_n(fn, "s_h", s_h, _u8, _mx_bytes(T, F), True), T, K, F,
         _stream(stream)))
 
 
 def te_gated_gemm_nvfp4(x, sx, gx, w, sw, gw, act: int, h=None, gu=None, stream=None):
     """te_gated_gemm_bf16 on NVFP4 operands (packed codes, block scales, tensor scales)."""
-    import torch
-    fn, bf, u8, f32 = "te_gated_gemm_nvfp4", torch.bfloat16, torch.uint8, torch.float32
+    fn = "te_gated_gemm_nvfp4"
     T, K, F = _gated_shape(fn, x, w, 2)
     _check(fn, lib().te_gated_gemm_nvfp4(
-        _need(fn, "x", x, u8, (T, K // 2)), _need_n(fn, "sx", sx, u8, _nv_bytes(T, K)),
-        _need_n(fn, "gx", gx, f32, 1), _need(fn, "w", w, u8, (2 * F, K // 2)),
-        _need_n(fn, "sw", sw, u8, _nv_bytes(2 * F, K)), _need_n(fn, "gw", gw, f32, 1), act,
-        _need(fn, "h", h, bf, (T, F), True), _need(fn, "gu", gu, bf, (T, 2 * F), True), T, K, F, _stream(stream)))
+        _need(fn, "x", x, _u8, (T, K // 2)), _need_n(fn, "sx", sx, _u8, _nv_bytes(T, K)),
+        _need_n(fn, "gx", gx, _f32, 1), _need(fn, "w", w, _u8, (2 * F, K // 2)),
+        _need_n(fn, "sw", sw, _u8, _nv_bytes(2 * F, K)), _need_n(fn, "gw", gw, _f32, 1), act,
+        _need(fn, "h", h, _bf16, (T, F), True), _need(fn, "gu", gu, _bf16, (T, 2 * F), True), T, K, F, _stream(stream)))
 
 
 def _dgrad_shape(fn, dy, w2, gu, dgu, packed: int = 1):
     """(T, F, N) of dy [T, N / packed] and W2's col copy [F, N / packed], and the pointers of gu and dgu."""
-    import torch
     if dy.dim() != 2 or w2.dim() != 2 or dy.shape[1] != w2.shape[1]:
         raise ValueError(f"{fn}: dy {tuple(dy.shape)} and w2 {tuple(w2.shape)} are not [T, N] and [F, N]")
     T, F = dy.shape[0], w2.shape[0]
-    return (T, F, dy.shape[1] * packed, _need(fn, "gu", gu, torch.bfloat16, (T, 2 * F)),
-            _need(fn, "dgu", dgu, torch.bfloat16, (T, 2 * F)))
+    return (T, F, dy.shape[1] * packed, _need(fn, "gu", gu, _bf16, (T, 2 * F)),
+            _need(fn, "dgu", dgu, _bf16, (T, 2 * F)))
 
 
 def te_gated_dgrad_fp8(dy, fd: int, w2, fw: int, dy_scale_inv, w2_scale_inv, gu, act: int, dgu, stream=None):
     """Gradients of the pre-activations from dy's row copy [T, N] and W2's col copy [F, N] in FP8."""
-    import torch
-    fn, u8, f32 = "te_gated_dgrad_fp8", torch.uint8, torch.float32
+    fn = "te_gated_dgrad_fp8"
     T, F, N, pgu, pdgu = _dgrad_shape(fn, dy, w2, gu, dgu)
     _check(fn, lib().te_gated_dgrad_fp8(
-        _need(fn, "dy", dy, u8, (T, N)), fd, _need(fn, "w2", w2, u8, (F, N)), fw,
-        _need_n(fn, "dy_scale_inv", dy_scale_inv, f32, 1), _need_n(fn, "w2_scale_inv", w2_scale_inv, f32, 1), pgu, act, pdgu,
-        T, F, N, _stream(stream)))
+        _need(fn, "dy", dy, _u8, (T, N)), fd, _need(fn, "w2", w2, _u8, (F, N)), fw,
+        _need_n(fn, "dy_scale_inv", dy_scale_inv, _f32, 1), _need_n(fn, "w2_scale_inv", w2_scale_inv, _f32, 1), pgu,
+        act, pdgu, T, F, N, _stream(stream)))
 
 
 def te_gated_dgrad_mxfp8(dy, sd, w2, sw, gu, act: int, dgu, fd: int = E4M3, fw: int = E4M3, stream=None):
     """te_gated_dgrad_fp8 on MXFP8 copies."""
-    import torch
-    fn, u8 = "te_gated_dgrad_mxfp8", torch.uint8
+    fn = "te_gated_dgrad_mxfp8"
     T, F, N, pgu, pdgu = _dgrad_shape(fn, dy, w2, gu, dgu)
     _check(fn, lib().te_gated_dgrad_mxfp8(
-        _need(fn, "dy", dy, u8, (T, N)), fd, _need_n(fn, "sd", sd, u8, _mx_bytes(T, N)),
-        _need(fn, "w2", w2, u8, (F, N)), fw, _need_n(fn, "sw", sw, u8, _mx_bytes(F, N)), pgu, act, pdgu, T, F, N,
+        _need(fn, "dy", dy, _u8, (T, N)), fd, _need_n(fn, "sd", sd, _u8, _mx_bytes(T, N)),
+        _need(fn, "w2", w2, _u8, (F, N)), fw, _need_n(fn, "sw", sw, _u8, _mx_bytes(F, N)), pgu, act, pdgu, T, F, N,
         _stream(stream)))
 
 
 def te_gated_dgrad_nvfp4(dy, sd, gd, w2, sw, gw, gu, act: int, dgu, stream=None):
     """te_gated_dgrad_fp8 on NVFP4 copies."""
-    import torch
-    fn, u8, f32 = "te_gated_dgrad_nvfp4", torch.uint8, torch.float32
+    fn = "te_gated_dgrad_nvfp4"
     T, F, N, pgu, pdgu = _dgrad_shape(fn, dy, w2, gu, dgu, 2)
     _check(fn, lib().te_gated_dgrad_nvfp4(
-        _need(fn, "dy", dy, u8, (T, N // 2)), _need_n(fn, "sd", sd, u8, _nv_bytes(T, N)),
-        _need_n(fn, "gd", gd, f32, 1), _need(fn, "w2", w2, u8, (F, N // 2)),
-        _need_n(fn, "sw", sw, u8, _nv_bytes(F, N)), _need_n(fn, "gw", gw, f32, 1), pgu, act, pdgu, T, F, N,
+        _need(fn, "dy", dy, _u8, (T, N // 2)), _need_n(fn, "sd", sd, _u8, _nv_bytes(T, N)),
+        _need_n(fn, "gd", gd, _f32, 1), _need(fn, "w2", w2, _u8, (F, N // 2)),
+        _need_n(fn, "sw", sw, _u8, _nv_bytes(F, N)), _need_n(fn, "gw", gw, _f32, 1), pgu, act, pdgu, T, F, N,
         _stream(stream)))
 
 
 def te_gated_bwd_bf16(x, w, w2, dy, gu, act: int, dgu, dx=None, dw=None, accumulate: int = 0, stream=None):
     """The BF16 backward pass: dgu from dy [T, N] and w2 [N, F], then dx = dgu w and dw (+)= dgu^T x."""
-    import torch
-    fn, bf = "te_gated_bwd_bf16", torch.bfloat16
+    fn = "te_gated_bwd_bf16"
     T, K, F = _gated_shape(fn, x, w)
     if dy.dim() != 2:
         raise ValueError(f"{fn}: dy has shape {tuple(dy.shape)}, expected [T, N]")
     N = dy.shape[1]
     _check(fn, lib().te_gated_bwd_bf16(
-        _need(fn, "x", x, bf, (T, K)), _need(fn, "w", w, bf, (2 * F, K)), _need(fn, "w2", w2, bf, (N, F)),
-        _need(fn, "dy", dy, bf, (T, N)), _need(fn, "gu", gu, bf, (T, 2 * F)), act,
-        _need(fn, "dgu", dgu, bf, (T, 2 * F)), _need(fn, "dx", dx, bf, (T, K), True),
-        _need(fn, "dw", dw, (bf, torch.float32), (2 * F, K), True), BF16 if dw is None else _out_dtype(dw),
+        _need(fn, "x", x, _bf16, (T, K)), _need(fn, "w", w, _bf16, (2 * F, K)), _need(fn, "w2", w2, _bf16, (N, F)),
+        _need(fn, "dy", dy, _bf16, (T, N)), _need(fn, "gu", gu, _bf16, (T, 2 * F)), act,
+        _need(fn, "dgu", dgu, _bf16, (T, 2 * F)), _need(fn, "dx", dx, _bf16, (T, K), True),
+        _need(fn, "dw", dw, (_bf16, _f32), (2 * F, K), True), BF16 if dw is None else _out_dtype(dw),
         int(accumulate), T, K, F, N, _stream(stream)))
 
 
