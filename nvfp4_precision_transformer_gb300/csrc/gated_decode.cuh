@@ -224,16 +224,28 @@ te_status launch_decode(const DecodeArgs& a, cudaStream_t st) {
 }
 
 // Whether this kernel takes the call, or the one of gated_stream.cuh (us, this / that):
-//   K = 4096, F = 16384 (BF16 268 MB of weights, FP8 134): T = 1 42.7 / 47.7 and 23.9 / 25.2, T = 8
-//   43.5 / 44.6 and 24.7 / 25.7, T = 16 51.3 / 45.2 and 29.9 / 25.7, T = 24 86.6 / 45.3;
-//   K = 2048, F = 5632 (46 and 23 MB): T = 8 10.8 / 12.4 and 8.2 / 8.7, T = 16 12.3 / 12.4 and 9.4 / 8.6;
-//   K = 768, F = 2048 (6.3 and 3.1 MB): T = 16 4.7 / 7.2 and 4.0 / 5.7, T = 32 5.9 / 7.2 and 5.3 / 5.7.
-// Up to eight tokens it is the faster one at every size: no tensor memory to set up, and the loads go
-// out at once.  Beyond, its matrix rate (512 multiply-adds a clock and SM) and its shared memory, taken
-// from the L1 that the loads in flight pass through, cost more than that saves unless w is small.
+//   T = 1, BF16: K = 4096, F = 1024 6.0 / 7.4, F = 4096 14.2 / 14.8, F = 16384 42.4 / 47.9; K = 5120,
+//   F = 1024 7.6 / 8.4, F = 4096 18.1 / 16.6; K = 8192, F = 1024 9.8 / 11.1, F = 4096 25.9 / 24.3;
+//   K = 2048, F = 16384 23.0 / 26.1; K = 1024, F = 4096 6.2 / 6.6, F = 16384 15.2 / 14.9; K = 512,
+//   F = 4096 4.9 / 5.2, F = 16384 12.2 / 9.7;
+//   T = 1, FP8: K = 4096, F = 1024 4.4 / 5.5, F = 16384 24.4 / 25.3; K = 2048, F = 4096 6.7 / 6.6, F = 16384
+//   16.5 / 15.0; K = 512, F = 4096 4.8 / 4.3, F = 16384 11.8 / 7.3;
+//   T = 16: BF16 K = 768, F = 2048 4.3 / 5.5, K = 1024, F = 4096 6.8 / 6.9, F = 8192 9.7 / 9.2, K = 2048,
+//   F = 1024 5.7 / 5.8; FP8 K = 768, F = 2048 3.7 / 5.1, K = 1024, F = 2048 4.1 / 5.0, F = 4096 5.9 / 5.5;
+//   T = 24: BF16 K = 1024, F = 2048 5.5 / 5.8, K = 2048, F = 1024 6.8 / 6.2; FP8 K = 2048, F = 1024 4.9 / 5.2.
+// No tensor memory to set up and loads that go out at once make it the faster one up to eight tokens, but
+// for many columns of a short K (each column's sum over the warp's lanes is then most of its work) and for
+// few warps on a long K.  Beyond, its matrix rate (512 multiply-adds a clock and SM) and its shared memory
+// for x, taken from the L1 that the loads in flight pass through, cost more than that saves unless both x
+// and w are small.
 inline bool decodes(int64_t T, int64_t K, int64_t F, int elem) {
   if (T > 8 * kDecMaxTiles || K > (1 << 17)) return false;
-  if (T > 8 && 2 * F * K * elem > (int64_t(16) << 20)) return false;
+  const int64_t row = K * elem;
+  if (T > 8) {
+    if (T * row >= (1 << 16) || F > 2048 * elem) return false;
+  } else if (K > 4096 ? F > 1024 : (row < 4096 && F > 2048 && F > 4 * row)) {
+    return false;
+  }
   return decode_smem(static_cast<int>(T), static_cast<int>(K), elem) <= 232448;
 }
 

@@ -11,7 +11,8 @@
 // tokens to the u warps through shared memory and get the first half's u back, and each thread then
 // has one column of h for half of the tokens; neighbouring lanes write neighbouring columns.  (Tiles of
 // 128 columns without the exchange, as gated_stream_block.cuh has them, are as fast at F = 16384 but
-// leave more SMs idle at smaller F: 24 tokens, K = F = 4096 BF16 18.7 us here, 25.3 so.)
+// leave more SMs idle at smaller F: 24 tokens, K = F = 4096 BF16 18.7 us here, 25.3 so, with one CTA a
+// tile.)  Where the tiles leave SMs idle, clusters of 2, 4 or 8 CTAs share a tile's K (below).
 //
 // 24 tokens, K = 4096, F = 16384: BF16 45.1 us (5.96 TB/s; gemm_kernel 51.5), FP8 25.6 us (5.25 TB/s;
 // 33.2); 64 tokens 48.2 / 52.5 and 28.0 / 30.1.  gemm_kernel's six stages turn round in about 1.7 us
@@ -42,7 +43,46 @@ struct StrCfg {
   static_assert(NP == 32 || NP == 64, "whole tcgen05.ld chunks, power-of-two TMEM columns");
 };
 
-template <int KIND, int NP>
+// A CTA's walk: its first tile and the step to the next, and its part of the k-tiles where a cluster shares
+// a tile's K (SPLIT).  Each role makes its own: kept in registers from the start of the kernel on, the same
+// numbers cost 0.3 us a call.
+template <bool SPLIT>
+struct Walk {
+  int split, part, tile, step, k_lo, k_num;
+  __device__ __forceinline__ explicit Walk(int k_tiles)
+      : split(1), part(0), tile(static_cast<int>(blockIdx.x)), step(static_cast<int>(gridDim.x)), k_lo(0),
+        k_num(k_tiles) {
+    if constexpr (SPLIT) {
+      asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(split));
+      part = static_cast<int>(dev::cluster_ctarank());
+      tile /= split;
+      step /= split;
+      k_lo = k_tiles * part / split;
+      k_num = k_tiles * (part + 1) / split - k_lo;
+    }
+  }
+};
+
+// What the CTAs of a cluster send one another: four tokens of a row of an accumulator in 16 bytes, the
+// tokens of group i going to CTA i % split, where the parts of CTA 0, 1, ... of its j-th group lie in
+// rows of `rows`.
+__device__ __forceinline__ uint32_t kpart_offset(int from, int j, int per, int rows, int row) {
+  return static_cast<uint32_t>(((from * per + j) * rows + row) * 16);
+}
+// Tokens 4 i to 4 i + 3 of this thread's row to their owner's buffer (at the start of shared memory).
+template <int N>
+__device__ __forceinline__ void kpart_send(const uint32_t (&acc)[N], int at, uint32_t buffer, int split, int part, int group,
+                                           int per, int rows, int row) {
+  const int owner = group & (split - 1), j = group / split;
+  dev::st_shared_cluster_v4(
+      dev::mapa_shared(buffer + kpart_offset(part, j, per, rows, row), static_cast<uint32_t>(owner)), acc[at],
+      acc[at + 1], acc[at + 2], acc[at + 3]);
+}
+
+// SPLIT: a cluster of `split` CTAs has one tile and each of them a part of K; they add their accumulators
+// through distributed shared memory, every one of them for its groups of four tokens and in the CTAs'
+// order, so the result does not depend on timing.
+template <int KIND, int NP, bool SPLIT>
 __global__ void __launch_bounds__(kStrThreads, 1)
     gated_stream_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                         const __grid_constant__ DecodeArgs a, uint32_t idesc, int k_tiles, int* err) {
@@ -89,20 +129,21 @@ __global__ void __launch_bounds__(kStrThreads, 1)
 
   if (warp == 0) {
     if (lane == 0) {
+      const Walk<SPLIT> w(k_tiles);
       int stage = 0;
       uint32_t phase = 0;
       int issued = 0;
       bool ok = true;
-      for (int tile = static_cast<int>(blockIdx.x); tile < tiles && ok; tile += static_cast<int>(gridDim.x)) {
-        for (int kt = 0; kt < k_tiles; ++kt) {
+      for (int tile = w.tile; tile < tiles && ok; tile += w.step) {
+        for (int kt = 0; kt < w.k_num; ++kt) {
           if (!dev::mbar_wait(&empty[stage], phase ^ 1u, abort_flag, err)) {
             ok = false;
             break;
           }
           dev::mbar_expect_tx(&full[stage], C::kA + C::kB);
-          dev::tma_load_2d(sA + stage * C::kA, &tmW, &full[stage], kt * 128, tile * 64);
-          dev::tma_load_2d(sA + stage * C::kA + 64 * 128, &tmW, &full[stage], kt * 128, a.F + tile * 64);
-          dev::tma_load_2d(sB + stage * C::kB, &tmX, &full[stage], kt * 128, 0);
+          dev::tma_load_2d(sA + stage * C::kA, &tmW, &full[stage], (w.k_lo + kt) * 128, tile * 64);
+          dev::tma_load_2d(sA + stage * C::kA + 64 * 128, &tmW, &full[stage], (w.k_lo + kt) * 128, a.F + tile * 64);
+          dev::tma_load_2d(sB + stage * C::kB, &tmX, &full[stage], (w.k_lo + kt) * 128, 0);
           ++issued;
           if (++stage == S) stage = 0, phase ^= 1u;
         }
@@ -116,15 +157,16 @@ __global__ void __launch_bounds__(kStrThreads, 1)
     }
   } else if (warp == 1) {
     if (lane == 0) {
+      const Walk<SPLIT> w(k_tiles);
       int stage = 0, it = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int tile = static_cast<int>(blockIdx.x); tile < tiles && ok; tile += static_cast<int>(gridDim.x), ++it) {
+      for (int tile = w.tile; tile < tiles && ok; tile += w.step, ++it) {
         const int as = it & 1;
         if (!dev::mbar_wait(&acc_empty[as], (static_cast<uint32_t>(it >> 1) & 1u) ^ 1u, abort_flag, err)) break;
         dev::tc_fence_after();
         const uint32_t d = tmem_base + static_cast<uint32_t>(as * NP);
-        for (int kt = 0; kt < k_tiles; ++kt) {
+        for (int kt = 0; kt < w.k_num; ++kt) {
           if (!dev::mbar_wait(&full[stage], phase, abort_flag, err)) {
             ok = false;
             break;
@@ -148,25 +190,48 @@ __global__ void __launch_bounds__(kStrThreads, 1)
       dev::mbar_wait(drain, 0, &dummy, err);
     }
   } else {
+    const Walk<SPLIT> w(k_tiles);
     const int quarter = warp & 3;
     const bool up = quarter >= 2;                 // lanes 64-127 of the accumulator: u
     const int fl = (quarter & 1) * 32 + lane;     // column of the tile
     const float alpha = (a.alpha_a ? __ldg(a.alpha_a) : 1.0f) * (a.alpha_b ? __ldg(a.alpha_b) : 1.0f);
     const float qs = a.q ? __ldg(a.q_scale) : 1.0f;
     unsigned int top = 0;
+    // g and u of tokens t0 and t0 + 1, column f
+    auto emit = [&](float2 g, float2 u, int t0, int f) {
+      const float2 h = __fmul2_rn(gate_act(g, a.act), u);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int64_t t = t0 + j;
+        if (t < a.T && f < a.F) {
+          const float gv = j ? g.y : g.x, uv = j ? u.y : u.x, hv = j ? h.y : h.x;
+          if (a.gu) {
+            a.gu[t * 2 * a.F + f] = __float2bfloat16_rn(gv);
+            a.gu[t * 2 * a.F + a.F + f] = __float2bfloat16_rn(uv);
+          }
+          if (a.h) a.h[t * a.F + f] = __float2bfloat16_rn(hv);
+          if (a.q) {
+            top = max(top, __float_as_uint(hv) & 0x7FFFFFFFu);
+            a.q[t * a.F + f] = static_cast<uint8_t>(a.q_e5m2 ? cvt_e5m2x2(hv * qs, 0.0f) : cvt_e4m3x2(hv * qs, 0.0f));
+          }
+        }
+      }
+    };
     int it = 0;
     bool ok = true;
-    for (int tile = static_cast<int>(blockIdx.x); tile < tiles; tile += static_cast<int>(gridDim.x), ++it) {
+    for (int tile = w.tile; tile < tiles; tile += w.step, ++it) {
       const int as = it & 1;
       if (!dev::mbar_wait(&acc_full[as], static_cast<uint32_t>(it >> 1) & 1u, abort_flag, err)) ok = false;
-      // the four warps leave together: the exchange below has barriers of all of them
-      int all_ok;
-      asm volatile(
-          "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}\n"
-          : "=r"(all_ok)
-          : "r"(static_cast<int>(ok))
-          : "memory");
-      if (!all_ok) break;
+      if (!SPLIT) {
+        // the four warps leave together: the exchange below has barriers of all of them
+        int all_ok;
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}\n"
+            : "=r"(all_ok)
+            : "r"(static_cast<int>(ok))
+            : "memory");
+        if (!all_ok) break;
+      }
       dev::tc_fence_after();
       uint32_t acc[NP / 32][32];
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(as * NP);
@@ -177,6 +242,28 @@ __global__ void __launch_bounds__(kStrThreads, 1)
       for (int c = 0; c < NP / 32; ++c) dev::reg_fence(acc[c]);
       dev::tc_fence_before();
       __syncwarp();
+      if constexpr (SPLIT) {
+        dev::cluster_sync();   // every load of the cluster has landed and every MMA has read it: the rings are free
+        const int per = NP / 4 / w.split, row = quarter * 32 + lane;
+#pragma unroll
+        for (int i = 0; i < NP / 4; ++i)
+          if (4 * i < a.T) kpart_send(acc[i / 8], 4 * (i % 8), dev::smem_u32(smem), w.split, w.part, i, per, 128, row);
+        dev::cluster_sync();
+        if (!ok) break;
+        const int col = row & 63, hi = row >> 6;   // this thread: a column, two tokens of the four
+        for (int j = 0; j < per; ++j) {
+          const int t0 = 4 * (j * w.split + w.part);
+          if (t0 >= a.T) break;
+          float2 g = make_float2(0.0f, 0.0f), u = g;
+          for (int from = 0; from < w.split; ++from) {
+            const uint8_t* p = smem + kpart_offset(from, j, per, 128, col) + 8 * hi;
+            g = __fadd2_rn(g, *reinterpret_cast<const float2*>(p));
+            u = __fadd2_rn(u, *reinterpret_cast<const float2*>(p + 64 * 16));
+          }
+          emit(__fmul2_rn(g, both(alpha)), __fmul2_rn(u, both(alpha)), t0 + 2 * hi, tile * 64 + col);
+        }
+        break;
+      }
       if (lane == 0) dev::mbar_arrive(&acc_empty[as]);
       // g warps give away the second half of the tokens, u warps the first
 #pragma unroll
@@ -194,23 +281,7 @@ __global__ void __launch_bounds__(kStrThreads, 1)
             __uint_as_float(up ? acc[(n + NP / 2 + 1) / 32][(n + NP / 2 + 1) % 32] : acc[(n + 1) / 32][(n + 1) % 32]));
         const float2 got = make_float2(ex[n0 * 64 + fl], ex[(n0 + 1) * 64 + fl]);
         const float2 g = __fmul2_rn(up ? got : mine, both(alpha)), u = __fmul2_rn(up ? mine : got, both(alpha));
-        const float2 h = __fmul2_rn(gate_act(g, a.act), u);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int64_t t = n0 + j;
-          if (t < a.T && f < a.F) {
-            const float gv = j ? g.y : g.x, uv = j ? u.y : u.x, hv = j ? h.y : h.x;
-            if (a.gu) {
-              a.gu[t * 2 * a.F + f] = __float2bfloat16_rn(gv);
-              a.gu[t * 2 * a.F + a.F + f] = __float2bfloat16_rn(uv);
-            }
-            if (a.h) a.h[t * a.F + f] = __float2bfloat16_rn(hv);
-            if (a.q) {
-              top = max(top, __float_as_uint(hv) & 0x7FFFFFFFu);
-              a.q[t * a.F + f] = static_cast<uint8_t>(a.q_e5m2 ? cvt_e5m2x2(hv * qs, 0.0f) : cvt_e4m3x2(hv * qs, 0.0f));
-            }
-          }
-        }
+        emit(g, u, n0, f);
       }
       // (the exchange is written again only after the next tile's first barrier)
     }
@@ -221,28 +292,90 @@ __global__ void __launch_bounds__(kStrThreads, 1)
     if (a.scale_inv && blockIdx.x == 0 && threadIdx.x == 64) *a.scale_inv = __fdiv_rn(1.0f, qs);
   }
 
+  if constexpr (SPLIT) {
+    if (warp < 2) {   // the other warps' part in the epilogue's two barriers
+      __syncwarp();
+      dev::cluster_sync();
+      dev::cluster_sync();
+    }
+  }
   dev::tc_fence_before();
   __syncthreads();
   dev::tc_fence_after();
   if (warp == 1) dev::tmem_dealloc(tmem_base, C::kCols);
 }
 
+// The CTAs that share a tile's K: as many of 2, 4 and 8 as the tiles leave SMs for and K has k-tiles for.
+// most[i]: clusters of 2 << i CTAs that run at once.  One CTA a tile / shared, one token MXFP8 (24 tokens
+// BF16): F = 2048, K = 2048 9.0 / 6.3 us (8.3 / 7.2), K = 4096 14.7 / 8.0 (17.3 / 9.7), K = 8192 26.0 / 11.5
+// (30.6 / 14.8); F = 4096, K = 16384 48.8 / 25.0 (58.1 / 45.0).  The exchange takes about 1 us: MXFP8
+// K = 768 (6 k-tiles) 5.4 / 4.9, K = 512 4.2 / 4.0, K = 256 (2) 3.4 / 3.7.
+inline int stream_split(int tiles, int k_tiles, const int (&most)[3]) {
+  for (int i = 2; i >= 0; --i)
+    if (tiles <= most[i] && k_tiles >= (2 << i) && k_tiles > 2) return 2 << i;
+  return 1;
+}
+
+// Once a device: the shared memory of the two forms of a kernel, and how many clusters of 2, 4 and 8 CTAs
+// of the shared form run at once.
+struct StreamSetup {
+  bool done;
+  int most[3];
+  template <typename... P>
+  te_status set(void (*single)(P...), void (*shared)(P...), int threads, int smem) {
+    if (done) return TE_OK;
+    if (cudaFuncSetAttribute(single, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+        cudaFuncSetAttribute(shared, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+      return record_cuda(cudaGetLastError());
+    for (int i = 0; i < 3; ++i) {
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim = {2u << i, 1u, 1u};
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(2u << i, 1, 1);
+      cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+      cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      if (cudaOccupancyMaxActiveClusters(&most[i], shared, &cfg) != cudaSuccess) return record_cuda(cudaGetLastError());
+    }
+    done = true;
+    return TE_OK;
+  }
+};
+
+// launch_dependent of clusters of `split` CTAs.
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent_clusters(void (*kernel)(Params...), int split, dim3 grid, dim3 block, size_t smem,
+                                      cudaStream_t st, Args... args) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {static_cast<unsigned>(split), 1u, 1u};
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
 template <int KIND, int NP>
 te_status launch_stream(const DecodeArgs& a, uint32_t xfmt, uint32_t wfmt, cudaStream_t st) {
   using C = StrCfg<NP>;
-  static bool attr_set[64] = {false};
+  static StreamSetup setup[64] = {};
   int dev_id = 0;
   cudaGetDevice(&dev_id);
   if (dev_id < 0 || dev_id >= 64) return TE_ERR_CUDA;
-  if (!attr_set[dev_id]) {
-    if (cudaFuncSetAttribute(gated_stream_kernel<KIND, NP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             C::kSmemTotal) != cudaSuccess)
-      return record_cuda(cudaGetLastError());
-    attr_set[dev_id] = true;
-  }
+  te_status s = setup[dev_id].set(gated_stream_kernel<KIND, NP, false>, gated_stream_kernel<KIND, NP, true>, kStrThreads,
+                                  C::kSmemTotal);
+  if (s != TE_OK) return s;
   const uint64_t row_bytes = static_cast<uint64_t>(a.K) * (KIND == kBF16 ? 2 : 1);
   CUtensorMap tw, tx;
-  te_status s = make_tmap_2d(&tw, a.w, row_bytes, 2 * static_cast<uint64_t>(a.F), 64);
+  s = make_tmap_2d(&tw, a.w, row_bytes, 2 * static_cast<uint64_t>(a.F), 64);
   if (s != TE_OK) return s;
   s = make_tmap_2d(&tx, a.x, row_bytes, static_cast<uint64_t>(a.T), NP);
   if (s != TE_OK) return s;
@@ -252,11 +385,16 @@ te_status launch_stream(const DecodeArgs& a, uint32_t xfmt, uint32_t wfmt, cudaS
   uint32_t idesc = make_idesc(KIND, wfmt, xfmt, 128);
   idesc = (idesc & ~(0x3Fu << 17)) | (static_cast<uint32_t>(NP >> 3) << 17);
   const int tiles = (a.F + 63) / 64;
-  const dim3 g(static_cast<unsigned>(tiles < num_sms() ? tiles : num_sms()), 1, 1), block(kStrThreads, 1, 1);
   const int k_tiles = static_cast<int>((row_bytes + 127) / 128);
+  const int split = stream_split(tiles, k_tiles, setup[dev_id].most);
+  const int grid = split > 1 ? split * tiles : (tiles < num_sms() ? tiles : num_sms());
   if (a.amax && (s = zero_amax(a.amax, st)) != TE_OK) return s;
+  const dim3 g(static_cast<unsigned>(grid), 1, 1), block(kStrThreads, 1, 1);
   const cudaError_t e =
-      launch_dependent(gated_stream_kernel<KIND, NP>, g, block, C::kSmemTotal, st, tw, tx, a, idesc, k_tiles, err);
+      split > 1 ? launch_dependent_clusters(gated_stream_kernel<KIND, NP, true>, split, g, block, C::kSmemTotal, st, tw,
+                                            tx, a, idesc, k_tiles, err)
+                : launch_dependent(gated_stream_kernel<KIND, NP, false>, g, block, C::kSmemTotal, st, tw, tx, a, idesc,
+                                   k_tiles, err);
   if (e != cudaSuccess) return record_cuda(e);
   count_launch();
   return launch_status();

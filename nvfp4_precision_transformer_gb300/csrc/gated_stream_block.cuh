@@ -37,7 +37,32 @@ struct StbCfg {
   static_assert(2 * NP <= kSfBase && kSfBase + kStages * kSfCols <= 512, "TMEM");
 };
 
-template <int KIND, int NP>
+// g and u of tokens t0 and t0 + 1 (the same in the whole warp), column f0 + lane: every output.
+template <int KIND>
+__device__ __forceinline__ void stb_emit(const DecodeArgs& a, float2 g2, float2 u2, int t0, int f0, int lane) {
+  const float2 h2 = __fmul2_rn(gate_act(g2, a.act), u2);
+  const int f = f0 + lane;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int64_t t = t0 + j;
+    if (t >= a.T) break;
+    const float gv = j ? g2.y : g2.x, uv = j ? u2.y : u2.x, hv = j ? h2.y : h2.x;
+    if (a.gu) {
+      a.gu[t * 2 * a.F + f] = __float2bfloat16_rn(gv);
+      a.gu[t * 2 * a.F + a.F + f] = __float2bfloat16_rn(uv);
+    }
+    if (a.h) a.h[t * a.F + f] = __float2bfloat16_rn(hv);
+    if (KIND == kMXFP8 && a.q) {
+      const int e = mx_exponent(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(hv) & 0x7FFFFFFFu)));
+      a.q[t * a.F + f] = static_cast<uint8_t>(cvt_e4m3x2(hv * mx_mult(e), 0.0f));
+      if (lane == 0)
+        a.s_h[scale_offset(static_cast<uint64_t>(t), static_cast<uint64_t>(f0 >> 5),
+                           static_cast<uint64_t>(a.F >> 5))] = static_cast<uint8_t>(e + 127);
+    }
+  }
+}
+
+template <int KIND, int NP, bool SPLIT>   // SPLIT: as in gated_stream_kernel
 __global__ void __launch_bounds__(kStbThreads, 1)
     gated_stream_block_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                               const __grid_constant__ DecodeArgs a, uint32_t idesc, int k_tiles, int* err) {
@@ -83,26 +108,27 @@ __global__ void __launch_bounds__(kStbThreads, 1)
 
   if (warp == 0) {
     if (lane == 0) {
+      const Walk<SPLIT> w(k_tiles);
       int stage = 0, issued = 0;
       uint32_t phase = 0;
       bool ok = true;
       const int64_t katoms = a.s_kpad >> 2;   // scale atoms of a 128-row group
-      for (int tile = static_cast<int>(blockIdx.x); tile < tiles && ok; tile += static_cast<int>(gridDim.x)) {
-        for (int kt = 0; kt < k_tiles; ++kt) {
+      for (int tile = w.tile; tile < tiles && ok; tile += w.step) {
+        for (int kt = 0; kt < w.k_num; ++kt) {
           if (!dev::mbar_wait(&empty[stage], phase ^ 1u, abort_flag, err)) {
             ok = false;
             break;
           }
           uint64_t* bar = &full[stage];
           uint8_t* sf = sSf + stage * 3 * C::kSf;
-          const int64_t katom = static_cast<int64_t>(kt) * C::kAtoms;
+          const int64_t katom = static_cast<int64_t>(w.k_lo + kt) * C::kAtoms;
           dev::mbar_expect_tx(bar, C::kStage);
           dev::bulk_load(sf, a.sw + (tile * katoms + katom) * 512, C::kSf, bar);
           dev::bulk_load(sf + C::kSf, a.sw + ((tiles + tile) * katoms + katom) * 512, C::kSf, bar);
           dev::bulk_load(sf + 2 * C::kSf, a.sx + katom * 512, C::kSf, bar);
-          dev::tma_load_2d(smem + stage * 2 * C::kA, &tmW, bar, kt * 128, tile * 128);
-          dev::tma_load_2d(smem + stage * 2 * C::kA + C::kA, &tmW, bar, kt * 128, a.F + tile * 128);
-          dev::tma_load_2d(sB + stage * C::kB, &tmX, bar, kt * 128, 0);
+          dev::tma_load_2d(smem + stage * 2 * C::kA, &tmW, bar, (w.k_lo + kt) * 128, tile * 128);
+          dev::tma_load_2d(smem + stage * 2 * C::kA + C::kA, &tmW, bar, (w.k_lo + kt) * 128, a.F + tile * 128);
+          dev::tma_load_2d(sB + stage * C::kB, &tmX, bar, (w.k_lo + kt) * 128, 0);
           ++issued;
           if (++stage == S) stage = 0, phase ^= 1u;
         }
@@ -116,11 +142,12 @@ __global__ void __launch_bounds__(kStbThreads, 1)
     }
   } else if (warp == 6) {
     if (lane == 0) {
+      const Walk<SPLIT> w(k_tiles);
       int stage = 0, last = -1;
       uint32_t phase = 0, last_phase = 0;
       bool ok = true;
-      for (int tile = static_cast<int>(blockIdx.x); tile < tiles && ok; tile += static_cast<int>(gridDim.x)) {
-        for (int kt = 0; kt < k_tiles; ++kt) {
+      for (int tile = w.tile; tile < tiles && ok; tile += w.step) {
+        for (int kt = 0; kt < w.k_num; ++kt) {
           // full of this phase also means that the MMAs that read the slot before have completed
           if (!dev::mbar_wait(&full[stage], phase, abort_flag, err)) {
             ok = false;
@@ -148,13 +175,14 @@ __global__ void __launch_bounds__(kStbThreads, 1)
     }
   } else if (warp == 1) {
     if (lane == 0) {
+      const Walk<SPLIT> w(k_tiles);
       int stage = 0, it = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int tile = static_cast<int>(blockIdx.x); tile < tiles && ok; tile += static_cast<int>(gridDim.x), ++it) {
+      for (int tile = w.tile; tile < tiles && ok; tile += w.step, ++it) {
         if (!dev::mbar_wait(acc_empty, (static_cast<uint32_t>(it) & 1u) ^ 1u, abort_flag, err)) break;
         dev::tc_fence_after();
-        for (int kt = 0; kt < k_tiles; ++kt) {
+        for (int kt = 0; kt < w.k_num; ++kt) {
           // the scales in tensor memory: the stage's operands have landed too, on the same barrier
           if (!dev::mbar_wait(&full[stage], phase, abort_flag, err) ||
               !dev::mbar_wait(&sf_ready[stage], phase, abort_flag, err)) {
@@ -190,15 +218,58 @@ __global__ void __launch_bounds__(kStbThreads, 1)
       dev::mbar_wait(drain, 0, &dummy, err);
     }
   } else {
+    const Walk<SPLIT> w(k_tiles);
     const int quarter = warp & 3;
     const float alpha = (a.alpha_a ? __ldg(a.alpha_a) : 1.0f) * (a.alpha_b ? __ldg(a.alpha_b) : 1.0f);
     int it = 0;
-    for (int tile = static_cast<int>(blockIdx.x); tile < tiles; tile += static_cast<int>(gridDim.x), ++it) {
-      const bool ok = dev::mbar_wait(acc_full, static_cast<uint32_t>(it) & 1u, abort_flag, err);
-      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+    for (int tile = w.tile; tile < tiles; tile += w.step, ++it) {
+      const bool ok = __all_sync(0xFFFFFFFFu, dev::mbar_wait(acc_full, static_cast<uint32_t>(it) & 1u, abort_flag, err));
+      if (!SPLIT && !ok) break;
       dev::tc_fence_after();
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
-      const int f0 = tile * 128 + quarter * 32, f = f0 + lane;
+      const int f0 = tile * 128 + quarter * 32;
+      if constexpr (SPLIT) {
+        // every load of the cluster has landed and every MMA has read it: the rings are free
+        dev::cluster_sync();
+        const int per = NP / 4 / w.split, row = quarter * 32 + lane;
+        const uint32_t buffer = dev::smem_u32(smem);
+#pragma unroll
+        for (int c = 0; c < NP / 32; ++c) {
+          if (32 * c >= a.T && c > 0) break;
+          uint32_t g[32], u[32];
+          dev::tmem_ld_32x32b_x32(taddr + 32 * c, g);
+          dev::tmem_ld_32x32b_x32(taddr + NP + 32 * c, u);
+          dev::tmem_ld_wait();
+          dev::reg_fence(g);
+          dev::reg_fence(u);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (32 * c + 4 * i < a.T) {
+              kpart_send(g, 4 * i, buffer, w.split, w.part, 8 * c + i, per, 256, row);
+              kpart_send(u, 4 * i, buffer, w.split, w.part, 8 * c + i, per, 256, 128 + row);
+            }
+        }
+        dev::cluster_sync();
+        if (!ok) break;
+        for (int j = 0; j < per; ++j) {
+          const int t0 = 4 * (j * w.split + w.part);
+          if (t0 >= a.T) break;
+          float2 g[2] = {}, u[2] = {};
+          for (int from = 0; from < w.split; ++from) {
+            const uint8_t* p = smem + kpart_offset(from, j, per, 256, row);
+            const float4 gv = *reinterpret_cast<const float4*>(p);
+            const float4 uv = *reinterpret_cast<const float4*>(p + 128 * 16);
+            g[0] = __fadd2_rn(g[0], make_float2(gv.x, gv.y));
+            g[1] = __fadd2_rn(g[1], make_float2(gv.z, gv.w));
+            u[0] = __fadd2_rn(u[0], make_float2(uv.x, uv.y));
+            u[1] = __fadd2_rn(u[1], make_float2(uv.z, uv.w));
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            stb_emit<KIND>(a, __fmul2_rn(g[i], both(alpha)), __fmul2_rn(u[i], both(alpha)), t0 + 2 * i, f0, lane);
+        }
+        break;
+      }
 #pragma unroll
       for (int c = 0; c < NP / 32; ++c) {
         if (32 * c >= a.T && c > 0) break;
@@ -216,26 +287,7 @@ __global__ void __launch_bounds__(kStbThreads, 1)
 #pragma unroll
         for (int i = 0; i < 32; i += 2) {
           const float2 g2 = __fmul2_rn(pair_of(g, i), both(alpha)), u2 = __fmul2_rn(pair_of(u, i), both(alpha));
-          const float2 h2 = __fmul2_rn(gate_act(g2, a.act), u2);
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int64_t t = 32 * c + i + j;
-            if (t >= a.T) break;
-            const float gv = j ? g2.y : g2.x, uv = j ? u2.y : u2.x, hv = j ? h2.y : h2.x;
-            if (a.gu) {
-              a.gu[t * 2 * a.F + f] = __float2bfloat16_rn(gv);
-              a.gu[t * 2 * a.F + a.F + f] = __float2bfloat16_rn(uv);
-            }
-            if (a.h) a.h[t * a.F + f] = __float2bfloat16_rn(hv);
-            if (KIND == kMXFP8 && a.q) {
-              const int e = mx_exponent(
-                  __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(hv) & 0x7FFFFFFFu)));
-              a.q[t * a.F + f] = static_cast<uint8_t>(cvt_e4m3x2(hv * mx_mult(e), 0.0f));
-              if (lane == 0)
-                a.s_h[scale_offset(static_cast<uint64_t>(t), static_cast<uint64_t>(f0 >> 5),
-                                   static_cast<uint64_t>(a.F >> 5))] = static_cast<uint8_t>(e + 127);
-            }
-          }
+          stb_emit<KIND>(a, g2, u2, 32 * c + i, f0, lane);
         }
       }
     }
@@ -251,6 +303,13 @@ __global__ void __launch_bounds__(kStbThreads, 1)
     }
   }
 
+  if constexpr (SPLIT) {
+    if (warp < 2 || warp == 6) {   // the other warps' part in the epilogue's two barriers
+      __syncwarp();
+      dev::cluster_sync();
+      dev::cluster_sync();
+    }
+  }
   dev::tc_fence_before();
   __syncthreads();
   dev::tc_fence_after();
@@ -260,19 +319,16 @@ __global__ void __launch_bounds__(kStbThreads, 1)
 template <int KIND, int NP>
 te_status launch_stream_block(const DecodeArgs& a, uint32_t xfmt, uint32_t wfmt, cudaStream_t st) {
   using C = StbCfg<KIND, NP>;
-  static bool attr_set[64] = {false};
+  static StreamSetup setup[64] = {};
   int dev_id = 0;
   cudaGetDevice(&dev_id);
   if (dev_id < 0 || dev_id >= 64) return TE_ERR_CUDA;
-  if (!attr_set[dev_id]) {
-    if (cudaFuncSetAttribute(gated_stream_block_kernel<KIND, NP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             C::kSmemTotal) != cudaSuccess)
-      return record_cuda(cudaGetLastError());
-    attr_set[dev_id] = true;
-  }
+  te_status s = setup[dev_id].set(gated_stream_block_kernel<KIND, NP, false>, gated_stream_block_kernel<KIND, NP, true>,
+                                  kStbThreads, C::kSmemTotal);
+  if (s != TE_OK) return s;
   const uint64_t row_bytes = static_cast<uint64_t>(a.K) / (KIND == kMXFP8 ? 1 : 2);
   CUtensorMap tw, tx;
-  te_status s = make_tmap_2d(&tw, a.w, row_bytes, 2 * static_cast<uint64_t>(a.F), 128);
+  s = make_tmap_2d(&tw, a.w, row_bytes, 2 * static_cast<uint64_t>(a.F), 128);
   if (s != TE_OK) return s;
   s = make_tmap_2d(&tx, a.x, row_bytes, static_cast<uint64_t>(a.T), NP);
   if (s != TE_OK) return s;
@@ -282,9 +338,15 @@ te_status launch_stream_block(const DecodeArgs& a, uint32_t xfmt, uint32_t wfmt,
   uint32_t idesc = make_idesc(KIND, wfmt, xfmt, 128);
   idesc = (idesc & ~(0x3Fu << 17)) | (static_cast<uint32_t>(NP >> 3) << 17);
   const int tiles = a.F / 128;
-  const dim3 g(static_cast<unsigned>(tiles < num_sms() ? tiles : num_sms()), 1, 1), block(kStbThreads, 1, 1);
-  const cudaError_t e = launch_dependent(gated_stream_block_kernel<KIND, NP>, g, block, C::kSmemTotal, st, tw, tx, a,
-                                         idesc, static_cast<int>((row_bytes + 127) / 128), err);
+  const int k_tiles = static_cast<int>((row_bytes + 127) / 128);
+  const int split = stream_split(tiles, k_tiles, setup[dev_id].most);
+  const int grid = split > 1 ? split * tiles : (tiles < num_sms() ? tiles : num_sms());
+  const dim3 g(static_cast<unsigned>(grid), 1, 1), block(kStbThreads, 1, 1);
+  const cudaError_t e =
+      split > 1 ? launch_dependent_clusters(gated_stream_block_kernel<KIND, NP, true>, split, g, block, C::kSmemTotal,
+                                            st, tw, tx, a, idesc, k_tiles, err)
+                : launch_dependent(gated_stream_block_kernel<KIND, NP, false>, g, block, C::kSmemTotal, st, tw, tx, a,
+                                   idesc, k_tiles, err);
   if (e != cudaSuccess) return record_cuda(e);
   count_launch();
   return launch_status();

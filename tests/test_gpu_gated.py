@@ -610,3 +610,57 @@ def test_library_refusals():
 
     assert bwd(K=24) == 2 and bwd(dt=te.E4M3) == 4 and bwd(acc=1) == 4 and bwd(acc=2) == 8
     assert bwd(x=None) == 1 and bwd(w=None) == 1 and bwd(dgu=None) == 1 and bwd(dx=odd) == 3 and bwd(dw=odd) == 3
+
+
+def _twice(kind, T, K, Fc, actk, outs, fmt="e4m3"):
+    """The outputs of a second call on the same operands are the first's, bit for bit."""
+    x, w, o = _forward(kind, T, K, Fc, actk, outs, fmt=fmt)
+    _, _, p = _forward(kind, T, K, Fc, actk, outs, fmt=fmt, xw=(x, w))
+    for name in ("h", "gu", "q", "s", "amax"):
+        a, b = o.get(name), p.get(name)
+        if a is not None:
+            a, b = (a.t, b.t) if isinstance(a, Out) else (a, b)
+            assert torch.equal(a, b), name
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,K,Fc", [(9, 4112, 16), (13, 2064, 512), (33, 4112, 1040), (64, 2048, 2048), (27, 4096, 2576),
+                                    (62, 528, 4864), (63, 528, 4880), (1, 4608, 1536), (7, 8208, 1088), (12, 16400, 80)])
+@pytest.mark.parametrize("kind,actk,outs,fmt", [("bf16", "silu", ("h", "gu"), "e4m3"),
+                                                ("fp8", "gelu", ("h", "gu", "q"), "e5m2")])
+def test_few_tokens_shared_contraction(T, K, Fc, kind, actk, outs, fmt):
+    """Few columns on a long row: 2, 4 or 8 CTAs share it, with parts of unequal length, a ragged last
+    k-tile, tokens that end inside a group of four, and the sizes on both sides of the rule."""
+    _check_forward(kind, T, K, Fc, actk, outs, fmt)
+    _twice(kind, T, K, Fc, actk, outs, fmt)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,K,Fc", [(1, 320, 128), (3, 1056, 256), (6, 2080, 1024), (30, 4128, 2048), (64, 2048, 4096),
+                                    (33, 8224, 128), (61, 800, 9728), (40, 800, 9856)])
+@pytest.mark.parametrize("kind,actk,outs", [("mxfp8", "silu", ("h", "gu", "q")), ("nvfp4", "gelu", ("h", "gu"))])
+def test_few_tokens_shared_contraction_block_scaled(T, K, Fc, kind, actk, outs):
+    _check_forward(kind, T, K, Fc, actk, outs)
+    _twice(kind, T, K, Fc, actk, outs)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [10, 42])
+def test_shared_contraction_keeps_what_is_not_finite_in_its_row_and_column(T):
+    a, b = _inputs(T, 4096, 256, 8)
+    x, w = Operand(np.abs(a) + 0.1, "fp8"), Operand(b, "fp8", "e5m2")
+    w.q[5, 3000] = 0x7C                                        # +inf in a gate row
+    h, q, amax = Out(T, 256), Out(T, 256, dtype=torch.uint8), G.scalar(-1.0)
+    te.te_gated_gemm_fp8(x.q, te.E4M3, w.q, te.E5M2, x.inv, w.inv, te.ACT_SILU, h=h.t, q_h=q.t, h_scale=G.scalar(1.0),
+                         h_amax=amax)
+    torch.cuda.synchronize()
+    assert np.isinf(h.np()[:, 5]).all() and np.isfinite(np.delete(h.np(), 5, 1)).all() and np.isposinf(amax.item())
+    x, w = Operand(a, "mxfp8"), Operand(b, "mxfp8")
+    x.q[T - 1, 100] = 0x7F                                     # NaN
+    h, q = Out(T, 256), Out(T, 256, dtype=torch.uint8)
+    s = Out(te.te_scale_bytes(te.E8M0, T, 256), dtype=torch.uint8)
+    te.te_gated_gemm_mxfp8(x.q, x.s, w.q, w.s, te.ACT_SILU, h=h.t, q_h=q.t, s_h=s.t)
+    torch.cuda.synchronize()
+    assert np.isnan(h.np()[T - 1]).all() and np.isfinite(h.np()[:T - 1]).all()
+    raw = s.np()
+    assert int(raw.astype(np.int64).sum()) == int(te.te_scale_unswizzle(te.E8M0, T, 256, raw).astype(np.int64).sum())
