@@ -79,7 +79,9 @@ te_status te_gated_gemm_bf16(const void* x, const void* w, int act, void* h, voi
                           static_cast<__nv_bfloat16*>(h), static_cast<__nv_bfloat16*>(gu), nullptr, nullptr, 0, nullptr,
                           nullptr};
     if (decodes(T, K, F, 2)) return launch_decode<kDecBF16, kDecBF16>(a, static_cast<cudaStream_t>(stream));
-    return launch_stream<kBF16>(a, 1u, 1u, static_cast<cudaStream_t>(stream));
+    bool taken;
+    s = launch_stream<kBF16>(a, 1u, 1u, static_cast<cudaStream_t>(stream), &taken);
+    if (taken || s != TE_OK) return s;
   }
   GatedArgs ep = {};
   if ((s = bf16_outputs(&ep, h, gu, T, F, act)) != TE_OK) return s;
@@ -112,10 +114,14 @@ te_status te_gated_gemm_fp8(const uint8_t* x, te_dtype fx, const uint8_t* w, te_
     const DecodeArgs a = {x, w, static_cast<int>(T), static_cast<int>(K), static_cast<int>(F), act,
                           x_scale_inv, w_scale_inv, static_cast<__nv_bfloat16*>(h), static_cast<__nv_bfloat16*>(gu), q_h,
                           h_scale, h_fmt == TE_E5M2, reinterpret_cast<unsigned int*>(h_amax), h_scale_inv};
-    if (!decodes(T, K, F, 1)) return launch_stream<kFP8>(a, fp8_code(fx), fp8_code(fw), st);
-    if (fw == TE_E4M3)
-      return fx == TE_E4M3 ? launch_decode<kDecE4M3, kDecE4M3>(a, st) : launch_decode<kDecE4M3, kDecE5M2>(a, st);
-    return fx == TE_E4M3 ? launch_decode<kDecE5M2, kDecE4M3>(a, st) : launch_decode<kDecE5M2, kDecE5M2>(a, st);
+    if (decodes(T, K, F, 1)) {
+      if (fw == TE_E4M3)
+        return fx == TE_E4M3 ? launch_decode<kDecE4M3, kDecE4M3>(a, st) : launch_decode<kDecE4M3, kDecE5M2>(a, st);
+      return fx == TE_E4M3 ? launch_decode<kDecE5M2, kDecE4M3>(a, st) : launch_decode<kDecE5M2, kDecE5M2>(a, st);
+    }
+    bool taken;
+    s = launch_stream<kFP8>(a, fp8_code(fx), fp8_code(fw), st, &taken);
+    if (taken || s != TE_OK) return s;
   }
   GatedArgs ep = {};
   if ((s = bf16_outputs(&ep, h, gu, T, F, act)) != TE_OK) return s;
@@ -155,7 +161,9 @@ te_status te_gated_gemm_mxfp8(const uint8_t* x, te_dtype fx, const uint8_t* sx, 
     a.sw = sw;
     a.s_kpad = (K / 32 + 3) / 4 * 4;
     a.s_h = s_h;
-    return launch_stream_block<kMXFP8>(a, fp8_code(fx), fp8_code(fw), static_cast<cudaStream_t>(stream));
+    bool taken;
+    s = launch_stream_block<kMXFP8>(a, fp8_code(fx), fp8_code(fw), static_cast<cudaStream_t>(stream), &taken);
+    if (taken || s != TE_OK) return s;
   }
   GatedArgs ep = {};
   if ((s = bf16_outputs(&ep, h, gu, T, F, act)) != TE_OK) return s;
@@ -188,7 +196,9 @@ te_status te_gated_gemm_nvfp4(const uint8_t* x, const uint8_t* sx, const float* 
     a.sx = sx;
     a.sw = sw;
     a.s_kpad = (K / 16 + 15) / 16 * 16;
-    return launch_stream_block<kNVFP4>(a, 1u, 1u, static_cast<cudaStream_t>(stream));
+    bool taken;
+    s = launch_stream_block<kNVFP4>(a, 1u, 1u, static_cast<cudaStream_t>(stream), &taken);
+    if (taken || s != TE_OK) return s;
   }
   GatedArgs ep = {};
   if ((s = bf16_outputs(&ep, h, gu, T, F, act)) != TE_OK) return s;

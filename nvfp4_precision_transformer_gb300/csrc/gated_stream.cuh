@@ -1,10 +1,11 @@
-// The gated projections of up to 64 tokens that the kernel of gated_decode.cuh does not take: still a
+// The gated projections of up to 128 tokens that the kernel of gated_decode.cuh does not take: still a
 // stream over the weights, but with too much matrix work for mma.sync.  The operands change places
 // against gemm_kernel: the weights are the 128-row operand of the MMA (64 gate rows and the 64 up rows
-// beside them) and the tokens its N (32 or 64), so a stage is 16 KB of weights and 4 or 8 KB of x, and
-// ten (eight) of them fit where gemm_kernel has six with as much x as weights: 160 KB of weights in
+// beside them) and the tokens its N (32, 64 or 128), so a stage is 16 KB of weights and 4, 8 or 16 KB of
+// x, and ten (eight, six) of them fit where gemm_kernel has six with as much x as weights: 160 KB of weights in
 // flight per SM.  One CTA per SM, no pairs: tiles of 64 columns of h, and a CTA with one tile more than
-// another has that much more of the bandwidth at the end.
+// another has that much more of the bandwidth at the end.  From 65 tokens on only where the tiles are
+// shared (stream_takes has the rule).
 //
 // warp 0 TMA producer, warp 1 MMA issuer, warps 2-5 epilogue.  Accumulator lanes 0-63 hold g and 64-127
 // u of the tile's columns, tokens along the TMEM columns: the g warps hand the second half of the
@@ -25,7 +26,7 @@ namespace te {
 namespace {
 
 constexpr int kStrThreads = 32 * 6;
-constexpr int64_t kStrMaxTokens = 64;
+constexpr int64_t kStrMaxTokens = 128;   // 64 where a tile's K is not shared
 constexpr int kStrMaxStages = 12;
 
 template <int NP>   // tokens, padded
@@ -40,7 +41,8 @@ struct StrCfg {
   static constexpr int kSmemTotal = kSmemBar + 512 + 1024;
   static constexpr int kCols = 2 * NP;   // two accumulators
   static_assert(kSmemTotal <= 232448 && (2 * kStages + 5) * 8 + 16 <= 512, "shared memory");
-  static_assert(NP == 32 || NP == 64, "whole tcgen05.ld chunks, power-of-two TMEM columns");
+  static_assert(NP == 32 || NP == 64 || NP == 128, "whole tcgen05.ld chunks, power-of-two TMEM columns");
+  static_assert(NP / 4 * 128 * 16 <= kSmemX, "the shared accumulators' parts");
 };
 
 // A CTA's walk: its first tile and the step to the next, and its part of the k-tiles where a cluster shares
@@ -233,21 +235,25 @@ __global__ void __launch_bounds__(kStrThreads, 1)
         if (!all_ok) break;
       }
       dev::tc_fence_after();
-      uint32_t acc[NP / 32][32];
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(as * NP);
-#pragma unroll
-      for (int c = 0; c < NP / 32; ++c) dev::tmem_ld_32x32b_x32(taddr + 32 * c, acc[c]);
-      dev::tmem_ld_wait();
-#pragma unroll
-      for (int c = 0; c < NP / 32; ++c) dev::reg_fence(acc[c]);
-      dev::tc_fence_before();
-      __syncwarp();
       if constexpr (SPLIT) {
-        dev::cluster_sync();   // every load of the cluster has landed and every MMA has read it: the rings are free
+        // every load of the cluster has landed and every MMA has read it: the rings are free
+        __syncwarp();
+        dev::cluster_sync();
         const int per = NP / 4 / w.split, row = quarter * 32 + lane;
 #pragma unroll
-        for (int i = 0; i < NP / 4; ++i)
-          if (4 * i < a.T) kpart_send(acc[i / 8], 4 * (i % 8), dev::smem_u32(smem), w.split, w.part, i, per, 128, row);
+        for (int c = 0; c < NP / 32; ++c) {
+          if (32 * c >= a.T) break;
+          uint32_t acc[32];
+          dev::tmem_ld_32x32b_x32(taddr + 32 * c, acc);
+          dev::tmem_ld_wait();
+          dev::reg_fence(acc);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (32 * c + 4 * i < a.T)
+              kpart_send(acc, 4 * i, dev::smem_u32(smem), w.split, w.part, 8 * c + i, per, 128, row);
+        }
+        dev::tc_fence_before();
         dev::cluster_sync();
         if (!ok) break;
         const int col = row & 63, hi = row >> 6;   // this thread: a column, two tokens of the four
@@ -264,6 +270,14 @@ __global__ void __launch_bounds__(kStrThreads, 1)
         }
         break;
       }
+      uint32_t acc[NP / 32][32];
+#pragma unroll
+      for (int c = 0; c < NP / 32; ++c) dev::tmem_ld_32x32b_x32(taddr + 32 * c, acc[c]);
+      dev::tmem_ld_wait();
+#pragma unroll
+      for (int c = 0; c < NP / 32; ++c) dev::reg_fence(acc[c]);
+      dev::tc_fence_before();
+      __syncwarp();
       if (lane == 0) dev::mbar_arrive(&acc_empty[as]);
       // g warps give away the second half of the tokens, u warps the first
 #pragma unroll
@@ -316,6 +330,33 @@ inline int stream_split(int tiles, int k_tiles, const int (&most)[3]) {
   return 1;
 }
 
+// Whether a call runs here or in gemm_kernel, whose time hardly depends on the tokens while the exchange's
+// and the outputs' part of this one's grows with them: up to 32 tokens always, beyond where K has the
+// k-tiles to pay for them.  Here / there, us:
+//   65 and 128 tokens: BF16 K = 4096, F = 2048 11.2 and 13.1 / 16.8, F = 4096 (split 2) 17.3 and 20.3 / 20.0,
+//   K = 8192, F = 2048 16.2 and 18.4 / 28.6; FP8 K = F = 2048 7.5 and 9.2 / 9.3, K = F = 4096 (split 2) 12.1
+//   and 15.1 / 14.1; MXFP8 K = F = 2048 (16 k-tiles) 9.5 and 12.2 / 10.2, K = 4096, F = 2048 11.5 and 14.2 /
+//   15.4, F = 8192 (split 2) 19.2 and 23.2 / 18.2; NVFP4 K = 4096, F = 2048 (16) 9.4 and 11.7 / 11.0;
+//   33 and 64 tokens, few k-tiles: BF16 K = 512, F = 4096 (split 2) 7.0 and 8.1 / 7.6, F = 16384 13.6 and
+//   14.2 / 12.2; FP8 K = 1024, F = 16384 13.5 and 14.2 / 11.9; MXFP8 K = 1024, F = 4096 (split 4) 7.6 and 8.7 /
+//   8.0, F = 8192 (split 2) 9.4 and 11.3 / 9.1, K = 2048, F = 16384 16.8 and 19.0 / 18.6; NVFP4 K = 1024,
+//   F = 4096 6.5 and 7.4 / 7.0, K = 4096, F = 8192 (split 2) 12.2 and 13.6 / 12.7, F = 16384 18.1 and 18.2 / 19.4.
+// `idle`: the tiles leave SMs for a split.
+inline bool stream_takes(int kind, int64_t T, int k_tiles, int split, bool idle) {
+  const bool block = kind == kMXFP8 || kind == kNVFP4;
+  if (T <= 32) return true;
+  if (T <= 64) {
+    if (!block) return split >= 4 || k_tiles >= 16 || (split == 2 && k_tiles >= 4 && T <= 48);
+    const bool long_k = k_tiles >= (kind == kMXFP8 ? 16 : 8);   // K >= 2048
+    if (k_tiles >= 32) return true;
+    if (split == 1) return !idle && (kind == kNVFP4 || T <= 48);
+    return split == 2 ? long_k && T <= 48 : long_k || T <= 48;
+  }
+  const int enough = block ? 32 : 16;
+  if (split >= 4) return k_tiles >= enough || (2 * k_tiles >= enough && T <= 80);
+  return split == 2 && !block && k_tiles >= 32 && T <= 96;
+}
+
 // Once a device: the shared memory of the two forms of a kernel, and how many clusters of 2, 4 and 8 CTAs
 // of the shared form run at once.
 struct StreamSetup {
@@ -363,17 +404,27 @@ cudaError_t launch_dependent_clusters(void (*kernel)(Params...), int split, dim3
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
 }
 
+// *taken: whether the call runs here.
 template <int KIND, int NP>
-te_status launch_stream(const DecodeArgs& a, uint32_t xfmt, uint32_t wfmt, cudaStream_t st) {
+te_status launch_stream(const DecodeArgs& a, uint32_t xfmt, uint32_t wfmt, cudaStream_t st, bool* taken) {
   using C = StrCfg<NP>;
+  constexpr bool kSharedOnly = NP == 128;
+  *taken = true;
   static StreamSetup setup[64] = {};
   int dev_id = 0;
   cudaGetDevice(&dev_id);
   if (dev_id < 0 || dev_id >= 64) return TE_ERR_CUDA;
-  te_status s = setup[dev_id].set(gated_stream_kernel<KIND, NP, false>, gated_stream_kernel<KIND, NP, true>, kStrThreads,
-                                  C::kSmemTotal);
+  te_status s = setup[dev_id].set(gated_stream_kernel<KIND, NP, kSharedOnly>, gated_stream_kernel<KIND, NP, true>,
+                                  kStrThreads, C::kSmemTotal);
   if (s != TE_OK) return s;
   const uint64_t row_bytes = static_cast<uint64_t>(a.K) * (KIND == kBF16 ? 2 : 1);
+  const int tiles = (a.F + 63) / 64;
+  const int k_tiles = static_cast<int>((row_bytes + 127) / 128);
+  const int split = stream_split(tiles, k_tiles, setup[dev_id].most);
+  if (!stream_takes(KIND, a.T, k_tiles, split, tiles <= setup[dev_id].most[0])) {
+    *taken = false;
+    return TE_OK;
+  }
   CUtensorMap tw, tx;
   s = make_tmap_2d(&tw, a.w, row_bytes, 2 * static_cast<uint64_t>(a.F), 64);
   if (s != TE_OK) return s;
@@ -384,16 +435,13 @@ te_status launch_stream(const DecodeArgs& a, uint32_t xfmt, uint32_t wfmt, cudaS
   // the weights are operand A: M = 128, N = NP
   uint32_t idesc = make_idesc(KIND, wfmt, xfmt, 128);
   idesc = (idesc & ~(0x3Fu << 17)) | (static_cast<uint32_t>(NP >> 3) << 17);
-  const int tiles = (a.F + 63) / 64;
-  const int k_tiles = static_cast<int>((row_bytes + 127) / 128);
-  const int split = stream_split(tiles, k_tiles, setup[dev_id].most);
   const int grid = split > 1 ? split * tiles : (tiles < num_sms() ? tiles : num_sms());
   if (a.amax && (s = zero_amax(a.amax, st)) != TE_OK) return s;
   const dim3 g(static_cast<unsigned>(grid), 1, 1), block(kStrThreads, 1, 1);
   const cudaError_t e =
       split > 1 ? launch_dependent_clusters(gated_stream_kernel<KIND, NP, true>, split, g, block, C::kSmemTotal, st, tw,
                                             tx, a, idesc, k_tiles, err)
-                : launch_dependent(gated_stream_kernel<KIND, NP, false>, g, block, C::kSmemTotal, st, tw, tx, a, idesc,
+                : launch_dependent(gated_stream_kernel<KIND, NP, kSharedOnly>, g, block, C::kSmemTotal, st, tw, tx, a, idesc,
                                    k_tiles, err);
   if (e != cudaSuccess) return record_cuda(e);
   count_launch();
@@ -401,8 +449,10 @@ te_status launch_stream(const DecodeArgs& a, uint32_t xfmt, uint32_t wfmt, cudaS
 }
 
 template <int KIND>
-te_status launch_stream(const DecodeArgs& a, uint32_t xfmt, uint32_t wfmt, cudaStream_t st) {
-  return a.T <= 32 ? launch_stream<KIND, 32>(a, xfmt, wfmt, st) : launch_stream<KIND, 64>(a, xfmt, wfmt, st);
+te_status launch_stream(const DecodeArgs& a, uint32_t xfmt, uint32_t wfmt, cudaStream_t st, bool* taken) {
+  return a.T <= 32   ? launch_stream<KIND, 32>(a, xfmt, wfmt, st, taken)
+         : a.T <= 64 ? launch_stream<KIND, 64>(a, xfmt, wfmt, st, taken)
+                     : launch_stream<KIND, 128>(a, xfmt, wfmt, st, taken);
 }
 
 }  // namespace

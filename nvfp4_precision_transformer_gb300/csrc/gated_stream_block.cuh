@@ -1,4 +1,4 @@
-// The gated projections of up to 64 tokens with block-scaled operands (MXFP8, NVFP4): the kernel of
+// The gated projections of up to 128 tokens with block-scaled operands (MXFP8, NVFP4): the kernel of
 // gated_stream.cuh with the weights as the 128-row operand and the tokens as N, but a tile of 128
 // columns of h: a whole 128-row group of the gate's scales and one of the up projection's, each its own
 // MMA into its own accumulator, so that a thread finds g and u of its column in the same lane and
@@ -32,8 +32,9 @@ struct StbCfg {
   static constexpr int kSmemSf = kSmemB + kStages * kB;
   static constexpr int kSmemBar = kSmemSf + kStages * 3 * kSf;
   static constexpr int kSmemTotal = kSmemBar + 512 + 1024;
-  static constexpr int kSfBase = 128, kSfCols = 12 * kAtoms;    // TMEM columns of a stage's scales: g, u, x
+  static constexpr int kSfBase = NP == 128 ? 256 : 128, kSfCols = 12 * kAtoms;    // TMEM columns of a stage's scales: g, u, x
   static_assert(kSmemTotal <= 232448 && (3 * kStages + 3) * 8 + 16 <= 512, "shared memory");
+  static_assert(NP / 4 * 256 * 16 <= kSmemSf, "the shared accumulators' parts");
   static_assert(2 * NP <= kSfBase && kSfBase + kStages * kSfCols <= 512, "TMEM");
 };
 
@@ -317,16 +318,25 @@ __global__ void __launch_bounds__(kStbThreads, 1)
 }
 
 template <int KIND, int NP>
-te_status launch_stream_block(const DecodeArgs& a, uint32_t xfmt, uint32_t wfmt, cudaStream_t st) {
+te_status launch_stream_block(const DecodeArgs& a, uint32_t xfmt, uint32_t wfmt, cudaStream_t st, bool* taken) {
   using C = StbCfg<KIND, NP>;
+  constexpr bool kSharedOnly = NP == 128;
+  *taken = true;
   static StreamSetup setup[64] = {};
   int dev_id = 0;
   cudaGetDevice(&dev_id);
   if (dev_id < 0 || dev_id >= 64) return TE_ERR_CUDA;
-  te_status s = setup[dev_id].set(gated_stream_block_kernel<KIND, NP, false>, gated_stream_block_kernel<KIND, NP, true>,
-                                  kStbThreads, C::kSmemTotal);
+  te_status s = setup[dev_id].set(gated_stream_block_kernel<KIND, NP, kSharedOnly>,
+                                  gated_stream_block_kernel<KIND, NP, true>, kStbThreads, C::kSmemTotal);
   if (s != TE_OK) return s;
   const uint64_t row_bytes = static_cast<uint64_t>(a.K) / (KIND == kMXFP8 ? 1 : 2);
+  const int tiles = a.F / 128;
+  const int k_tiles = static_cast<int>((row_bytes + 127) / 128);
+  const int split = stream_split(tiles, k_tiles, setup[dev_id].most);
+  if (!stream_takes(KIND, a.T, k_tiles, split, tiles <= setup[dev_id].most[0])) {
+    *taken = false;
+    return TE_OK;
+  }
   CUtensorMap tw, tx;
   s = make_tmap_2d(&tw, a.w, row_bytes, 2 * static_cast<uint64_t>(a.F), 128);
   if (s != TE_OK) return s;
@@ -337,15 +347,12 @@ te_status launch_stream_block(const DecodeArgs& a, uint32_t xfmt, uint32_t wfmt,
   // the weights are operand A: M = 128, N = NP
   uint32_t idesc = make_idesc(KIND, wfmt, xfmt, 128);
   idesc = (idesc & ~(0x3Fu << 17)) | (static_cast<uint32_t>(NP >> 3) << 17);
-  const int tiles = a.F / 128;
-  const int k_tiles = static_cast<int>((row_bytes + 127) / 128);
-  const int split = stream_split(tiles, k_tiles, setup[dev_id].most);
   const int grid = split > 1 ? split * tiles : (tiles < num_sms() ? tiles : num_sms());
   const dim3 g(static_cast<unsigned>(grid), 1, 1), block(kStbThreads, 1, 1);
   const cudaError_t e =
       split > 1 ? launch_dependent_clusters(gated_stream_block_kernel<KIND, NP, true>, split, g, block, C::kSmemTotal,
                                             st, tw, tx, a, idesc, k_tiles, err)
-                : launch_dependent(gated_stream_block_kernel<KIND, NP, false>, g, block, C::kSmemTotal, st, tw, tx, a,
+                : launch_dependent(gated_stream_block_kernel<KIND, NP, kSharedOnly>, g, block, C::kSmemTotal, st, tw, tx, a,
                                    idesc, k_tiles, err);
   if (e != cudaSuccess) return record_cuda(e);
   count_launch();
@@ -353,8 +360,10 @@ te_status launch_stream_block(const DecodeArgs& a, uint32_t xfmt, uint32_t wfmt,
 }
 
 template <int KIND>
-te_status launch_stream_block(const DecodeArgs& a, uint32_t xfmt, uint32_t wfmt, cudaStream_t st) {
-  return a.T <= 32 ? launch_stream_block<KIND, 32>(a, xfmt, wfmt, st) : launch_stream_block<KIND, 64>(a, xfmt, wfmt, st);
+te_status launch_stream_block(const DecodeArgs& a, uint32_t xfmt, uint32_t wfmt, cudaStream_t st, bool* taken) {
+  return a.T <= 32   ? launch_stream_block<KIND, 32>(a, xfmt, wfmt, st, taken)
+         : a.T <= 64 ? launch_stream_block<KIND, 64>(a, xfmt, wfmt, st, taken)
+                     : launch_stream_block<KIND, 128>(a, xfmt, wfmt, st, taken);
 }
 
 }  // namespace

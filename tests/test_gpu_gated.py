@@ -625,7 +625,9 @@ def _twice(kind, T, K, Fc, actk, outs, fmt="e4m3"):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("T,K,Fc", [(9, 4112, 16), (13, 2064, 512), (33, 4112, 1040), (64, 2048, 2048), (27, 4096, 2576),
-                                    (62, 528, 4864), (63, 528, 4880), (1, 4608, 1536), (7, 8208, 1088), (12, 16400, 80)])
+                                    (62, 528, 4864), (63, 528, 4880), (1, 4608, 1536), (7, 8208, 1088), (12, 16400, 80),
+                                    (65, 4112, 1040), (128, 2048, 2576), (101, 8208, 80), (90, 4112, 4864),
+                                    (90, 4112, 4880)])
 @pytest.mark.parametrize("kind,actk,outs,fmt", [("bf16", "silu", ("h", "gu"), "e4m3"),
                                                 ("fp8", "gelu", ("h", "gu", "q"), "e5m2")])
 def test_few_tokens_shared_contraction(T, K, Fc, kind, actk, outs, fmt):
@@ -637,7 +639,8 @@ def test_few_tokens_shared_contraction(T, K, Fc, kind, actk, outs, fmt):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("T,K,Fc", [(1, 320, 128), (3, 1056, 256), (6, 2080, 1024), (30, 4128, 2048), (64, 2048, 4096),
-                                    (33, 8224, 128), (61, 800, 9728), (40, 800, 9856)])
+                                    (33, 8224, 128), (61, 800, 9728), (40, 800, 9856), (65, 4128, 1280), (128, 8224, 256),
+                                    (99, 4128, 384), (79, 4128, 640), (81, 2080, 640)])
 @pytest.mark.parametrize("kind,actk,outs", [("mxfp8", "silu", ("h", "gu", "q")), ("nvfp4", "gelu", ("h", "gu"))])
 def test_few_tokens_shared_contraction_block_scaled(T, K, Fc, kind, actk, outs):
     _check_forward(kind, T, K, Fc, actk, outs)
@@ -645,7 +648,7 @@ def test_few_tokens_shared_contraction_block_scaled(T, K, Fc, kind, actk, outs):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T", [10, 42])
+@pytest.mark.parametrize("T", [10, 42, 74])
 def test_shared_contraction_keeps_what_is_not_finite_in_its_row_and_column(T):
     a, b = _inputs(T, 4096, 256, 8)
     x, w = Operand(np.abs(a) + 0.1, "fp8"), Operand(b, "fp8", "e5m2")
