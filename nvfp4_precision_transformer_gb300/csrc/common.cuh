@@ -103,7 +103,9 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
 __device__ __forceinline__ void set_error(int* err, int code) { atomicCAS(err, 0, code); }
 
 // ---- programmatic dependent launch: wait for the kernel before this one in the stream to be complete,
-// let the one after it start
+// let the one after it start.  Behind the wait only ordinary loads: the read-only path (__ldg,
+// ld.global.nc, const __restrict__ parameters) is for data that nobody writes while the kernel lives,
+// and this one's life begins while the kernel before it still writes.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

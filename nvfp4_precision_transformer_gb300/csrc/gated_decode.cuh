@@ -45,9 +45,11 @@ struct DecodeArgs {
   uint8_t* s_h;
 };
 
+// (An ordinary load that leaves L1 alone: the read-only path is not for a kernel that is set up beside
+// the one before it, see pdl_wait.)
 __device__ __forceinline__ uint4 ld_stream(const uint8_t* p) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;
@@ -115,11 +117,11 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1) gated_decode_kernel(DecodeA
     const int n = i / pieces, p = i - n * pieces;
     uint4 v = make_uint4(0u, 0u, 0u, 0u);
     if (n < a.T && p * 16 < row_bytes)
-      v = __ldg(reinterpret_cast<const uint4*>(a.x + static_cast<int64_t>(n) * row_bytes + p * 16));
+      v = *reinterpret_cast<const uint4*>(a.x + static_cast<int64_t>(n) * row_bytes + p * 16);
     *reinterpret_cast<uint4*>(dec_smem + n * srow + p * 16) = v;
   }
-  const float alpha = (a.alpha_a ? __ldg(a.alpha_a) : 1.0f) * (a.alpha_b ? __ldg(a.alpha_b) : 1.0f);
-  const float qs = a.q ? __ldg(a.q_scale) : 1.0f;
+  const float alpha = (a.alpha_a ? *a.alpha_a : 1.0f) * (a.alpha_b ? *a.alpha_b : 1.0f);
+  const float qs = a.q ? *a.q_scale : 1.0f;
   unsigned int top = 0;
   __syncthreads();
 

@@ -196,8 +196,8 @@ __global__ void __launch_bounds__(kStrThreads, 1)
     const int quarter = warp & 3;
     const bool up = quarter >= 2;                 // lanes 64-127 of the accumulator: u
     const int fl = (quarter & 1) * 32 + lane;     // column of the tile
-    const float alpha = (a.alpha_a ? __ldg(a.alpha_a) : 1.0f) * (a.alpha_b ? __ldg(a.alpha_b) : 1.0f);
-    const float qs = a.q ? __ldg(a.q_scale) : 1.0f;
+    const float alpha = (a.alpha_a ? *a.alpha_a : 1.0f) * (a.alpha_b ? *a.alpha_b : 1.0f);
+    const float qs = a.q ? *a.q_scale : 1.0f;
     unsigned int top = 0;
     // g and u of tokens t0 and t0 + 1, column f
     auto emit = [&](float2 g, float2 u, int t0, int f) {

@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kStbThreads, 1)
   } else {
     const Walk<SPLIT> w(k_tiles);
     const int quarter = warp & 3;
-    const float alpha = (a.alpha_a ? __ldg(a.alpha_a) : 1.0f) * (a.alpha_b ? __ldg(a.alpha_b) : 1.0f);
+    const float alpha = (a.alpha_a ? *a.alpha_a : 1.0f) * (a.alpha_b ? *a.alpha_b : 1.0f);
     int it = 0;
     for (int tile = w.tile; tile < tiles; tile += w.step, ++it) {
       const bool ok = __all_sync(0xFFFFFFFFu, dev::mbar_wait(acc_full, static_cast<uint32_t>(it) & 1u, abort_flag, err));

@@ -143,7 +143,7 @@ struct GemmArgs {
   int sfb_row_atoms;    // 128-row groups present in B's scale tensor
   const float* alpha_a;
   const float* alpha_b;
-  const float* bias;
+  const float* bias;    // (read-only loads: never with pdl)
   void* D;
   int out_f32;
   int accumulate;       // 1: D (fp32) += result, by TMA reduce-add
@@ -544,7 +544,7 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, EPI>::kThreads, 1)
     const int quarter = warp & 3;
     const int half = (warp - 2) >> 2;
     uint8_t* stg = smem + C::kSmemStage + (warp - 2) * C::kStgBytes;
-    const float alpha = (args.alpha_a ? __ldg(args.alpha_a) : 1.0f) * (args.alpha_b ? __ldg(args.alpha_b) : 1.0f);
+    const float alpha = (args.alpha_a ? *args.alpha_a : 1.0f) * (args.alpha_b ? *args.alpha_b : 1.0f);
     typename EpiState<EPI>::type est;
     if constexpr (EPI == kGated) est.init(ep, stg, lane);
     if constexpr (EPI == kDgrad) est.init(stg, epi_bar + (warp - 2), lane);

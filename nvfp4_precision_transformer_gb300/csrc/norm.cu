@@ -69,8 +69,8 @@ __device__ __forceinline__ void store8(float* p, const float2 (&v)[4]) {
   *reinterpret_cast<float4*>(p) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
   *reinterpret_cast<float4*>(p + 4) = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
 }
-__device__ __forceinline__ void ldg8(const float* p, float2 (&v)[4]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+__device__ __forceinline__ void ld8(const float* p, float2 (&v)[4]) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
   v[0] = make_float2(a.x, a.y), v[1] = make_float2(a.z, a.w);
   v[2] = make_float2(b.x, b.y), v[3] = make_float2(b.z, b.w);
 }
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(32 * cta_warps(WPR), WPR <= 8 ? 2 : 1) rmsnorm
       const bool live = col < C;
       const int64_t at = row * C + col;
       float2 g[4] = {}, y[4];
-      if (live) ldg8(a.gamma + col, g);
+      if (live) ld8(a.gamma + col, g);
 #pragma unroll
       for (int i = 0; i < 4; ++i) y[i] = __fmul2_rn(__fmul2_rn(v[t][i], rs2), g[i]);
       if (live && a.res_out) store8(static_cast<T*>(a.res_out) + at, v[t]);
@@ -254,6 +254,7 @@ template <typename T, int WPR, int CH>
 __global__ void __launch_bounds__(32 * cta_warps(WPR), WPR <= 8 ? 2 : 1) rmsnorm_bwd_kernel(NormBwdArgs a) {
   constexpr int GR = cta_rows(WPR);
   constexpr bool kAhead = sizeof(T) == 2 && CH == 2;   // the next row's loads before this row is reduced
+  constexpr bool kHold = CH == 2;                      // gamma in registers
   __shared__ float red[GR][2][WPR];
   extern __shared__ __align__(16) float cols_sum[];   // [GR - 1][cols]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -290,6 +291,23 @@ __global__ void __launch_bounds__(32 * cta_warps(WPR), WPR <= 8 ? 2 : 1) rmsnorm
     }
   };
   dev::pdl_wait();
+  // a lane's columns are the same in every row: gamma once (four chunks of it would not fit), not behind
+  // each row's stores, which ordinary loads do not pass (15872 x 4096: 98.8 us
+  // so, 83.8 held; fp32 151, 142)
+  float2 gam[kHold ? CH : 1][4] = {};
+  if (kHold) {
+#pragma unroll
+    for (int t = 0; t < CH; ++t)
+      if (col0 + 256 * t < C) ld8(a.gamma + col0 + 256 * t, gam[kHold ? t : 0]);
+  }
+  auto gamma8 = [&](int t, float2 (&g)[4]) {
+    if (kHold) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) g[i] = gam[kHold ? t : 0][i];
+    } else {
+      ld8(a.gamma + col0 + 256 * t, g);
+    }
+  };
   RowRegs cur;
   int64_t row = static_cast<int64_t>(blockIdx.x) * GR + grp;
   if (kAhead) load(cur, row);
@@ -303,7 +321,7 @@ __global__ void __launch_bounds__(32 * cta_warps(WPR), WPR <= 8 ? 2 : 1) rmsnorm
     for (int t = 0; t < CH; ++t) {
       const int col = col0 + 256 * t;
       float2 g[4] = {};
-      if (col < C) ldg8(a.gamma + col, g);
+      if (col < C) gamma8(t, g);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float2 w = __fmul2_rn(cur.d[t].pair(i), __fmul2_rn(cur.x[t].pair(i), rs2));   // dy * xhat
@@ -319,7 +337,7 @@ __global__ void __launch_bounds__(32 * cta_warps(WPR), WPR <= 8 ? 2 : 1) rmsnorm
       const int col = col0 + 256 * t;
       if (col >= C) break;
       float2 g[4], o[4];
-      ldg8(a.gamma + col, g);
+      gamma8(t, g);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float2 p = __fmul2_rn(cur.d[t].pair(i), g[i]);
@@ -360,8 +378,7 @@ __global__ void __launch_bounds__(32 * cta_warps(WPR), WPR <= 8 ? 2 : 1) rmsnorm
 
 // dgamma[c] = the sum of the partial rows in a fixed order: 32 columns x 32 row lanes a CTA, every
 // load of a lane in flight at once (304 rows x 4096: with 8 lanes 8 us, as much as it hid).
-__global__ void __launch_bounds__(1024) dgamma_kernel(const float* __restrict__ partial, int n, int64_t C,
-                                                      float* __restrict__ dgamma) {
+__global__ void __launch_bounds__(1024) dgamma_kernel(const float* partial, int n, int64_t C, float* dgamma) {
   __shared__ float part[32][33];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   dev::pdl_wait();   // the partial sums are complete
