@@ -125,10 +125,11 @@ _bf16, _f32, _u8 = torch.bfloat16, torch.float32, torch.uint8
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream):
+def _stream(stream, dev=None):
     if stream is None:
         # the handle alone: building a Stream object takes 3 us, as long as a small kernel
-        return _raw_stream(torch.cuda.current_device()) if _raw_stream else torch.cuda.current_stream().cuda_stream
+        dev = torch.cuda.current_device() if dev is None else dev
+        return _raw_stream(dev) if _raw_stream else torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -200,14 +201,28 @@ def te_layernorm_fp8(x, gamma, beta, eps: float, fmt: int, scale, q_row, ln_out=
         _ptr(ln_out), _ptr(mu), _ptr(rsigma), _ptr(amax_out), _ptr(scale_inv_out), _stream(stream)))
 
 
-def _need(fn: str, name: str, t, dtype, shape, optional: bool = False):
-    """Refuses a tensor that the call would misread: not on the GPU, not contiguous, of another
+def _device() -> int:
+    """The current GPU, whose stream a call goes to; -2, where no tensor is, without one."""
+    try:
+        return torch.cuda.current_device()
+    except (RuntimeError, AssertionError):
+        return -2
+
+
+def _misplaced(fn: str, dev: int, name: str, t) -> ValueError:
+    if not t.is_cuda or dev < 0:
+        return ValueError(f"{fn}: {name} is not on the GPU")
+    return ValueError(f"{fn}: {name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+
+
+def _need(fn: str, dev: int, name: str, t, dtype, shape, optional: bool = False):
+    """Refuses a tensor that the call would misread: not on GPU ``dev``, not contiguous, of another
     dtype (one, or a tuple of them) or shape.  Returns its address."""
     if t is None:
         if optional:
             return None
         raise TypeError(f"{fn}: {name} is required")
-    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
         return t.data_ptr()
     if t.dtype is not dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
         raise TypeError(f"{fn}: {name} is {t.dtype}, expected {dtype}")
@@ -215,24 +230,26 @@ def _need(fn: str, name: str, t, dtype, shape, optional: bool = False):
         raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{fn}: {name} is not contiguous")
-    if not t.is_cuda:
-        raise ValueError(f"{fn}: {name} is not on the GPU")
+    if t.get_device() != dev:
+        raise _misplaced(fn, dev, name, t)
     return t.data_ptr()
 
 
-def _need_n(fn: str, name: str, t, dtype, n: int, optional: bool = False):
+def _need_n(fn: str, dev: int, name: str, t, dtype, n: int, optional: bool = False):
     """The same for a tensor of at least ``n`` elements whatever its shape (scalars, scale tensors)."""
     if t is None:
         if optional:
             return None
         raise TypeError(f"{fn}: {name} is required")
-    if t.dtype is dtype and t.numel() >= n and t.is_cuda and t.is_contiguous():
+    if t.dtype is dtype and t.numel() >= n and t.get_device() == dev and t.is_contiguous():
         return t.data_ptr()
     if t.dtype is not dtype:
         raise TypeError(f"{fn}: {name} is {t.dtype}, expected {dtype}")
     if t.numel() < n:
         raise ValueError(f"{fn}: {name} has {t.numel()} elements, needs {n}")
-    raise ValueError(f"{fn}: {name} is not {'contiguous' if t.is_cuda else 'on the GPU'}")
+    if t.get_device() != dev:
+        raise _misplaced(fn, dev, name, t)
+    raise ValueError(f"{fn}: {name} is not contiguous")
 
 
 def _mx_bytes(rows: int, cols: int) -> int:
@@ -245,36 +262,39 @@ def _nv_bytes(rows: int, cols: int) -> int:
     return -(-rows // 128) * 128 * (-(-cols // 256) * 16)
 
 
-def _norm_operands(fn, x, gamma, residual, res_out, y, rsigma):
+def _norm_operands(fn, dev, x, gamma, residual, res_out, y, rsigma):
     if x.dim() != 2:
         raise ValueError(f"{fn}: x has shape {tuple(x.shape)}, expected [rows, cols]")
     shape, dt = x.shape, x.dtype
     rows, cols = shape
-    px = _need(fn, "x", x, dt if dt is _bf16 or dt is _f32 else (_bf16, _f32), shape)
-    return (px, F32 if dt is _f32 else BF16, rows, cols, _need(fn, "residual", residual, dt, shape, True),
-            _need(fn, "gamma", gamma, _f32, (cols,)), _need(fn, "res_out", res_out, dt, shape, True),
-            _need(fn, "y", y, _bf16, shape, True), _need(fn, "rsigma", rsigma, _f32, (rows,), True))
+    px = _need(fn, dev, "x", x, dt if dt is _bf16 or dt is _f32 else (_bf16, _f32), shape)
+    return (px, F32 if dt is _f32 else BF16, rows, cols, _need(fn, dev, "residual", residual, dt, shape, True),
+            _need(fn, dev, "gamma", gamma, _f32, (cols,)), _need(fn, dev, "res_out", res_out, dt, shape, True),
+            _need(fn, dev, "y", y, _bf16, shape, True), _need(fn, dev, "rsigma", rsigma, _f32, (rows,), True))
 
 
 def te_rmsnorm_fp8(x, gamma, eps: float, fmt: int, scale=None, q_row=None, residual=None, res_out=None, y=None,
                    rsigma=None, amax_out=None, scale_inv_out=None, stream=None):
     """RMSNorm of x (+ residual), its output in FP8 with a per-tensor scale (and / or y in bf16)."""
     fn = "te_rmsnorm_fp8"
-    px, dt, r, c, pres, pg, pro, py, prs = _norm_operands(fn, x, gamma, residual, res_out, y, rsigma)
+    dev = _device()
+    px, dt, r, c, pres, pg, pro, py, prs = _norm_operands(fn, dev, x, gamma, residual, res_out, y, rsigma)
     _check(fn, lib().te_rmsnorm_fp8(
-        px, dt, r, c, pres, pg, float(eps), fmt, _need_n(fn, "scale", scale, _f32, 1, True),
-        _need(fn, "q_row", q_row, _u8, x.shape, True), py, pro, prs,
-        _need_n(fn, "amax_out", amax_out, _f32, 1, True), _need_n(fn, "scale_inv_out", scale_inv_out, _f32, 1, True),
-        _stream(stream)))
+        px, dt, r, c, pres, pg, float(eps), fmt, _need_n(fn, dev, "scale", scale, _f32, 1, True),
+        _need(fn, dev, "q_row", q_row, _u8, x.shape, True), py, pro, prs,
+        _need_n(fn, dev, "amax_out", amax_out, _f32, 1, True),
+        _need_n(fn, dev, "scale_inv_out", scale_inv_out, _f32, 1, True),
+        _stream(stream, dev)))
 
 
 def te_rmsnorm_mxfp8(x, gamma, eps: float, q_row, s_row, residual=None, res_out=None, y=None, rsigma=None, stream=None):
     """RMSNorm of x (+ residual), its output in MXFP8 (E4M3 codes, E8M0 scales in the tensor-core layout)."""
     fn = "te_rmsnorm_mxfp8"
-    px, dt, r, c, pres, pg, pro, py, prs = _norm_operands(fn, x, gamma, residual, res_out, y, rsigma)
+    dev = _device()
+    px, dt, r, c, pres, pg, pro, py, prs = _norm_operands(fn, dev, x, gamma, residual, res_out, y, rsigma)
     _check(fn, lib().te_rmsnorm_mxfp8(
-        px, dt, r, c, pres, pg, float(eps), _need(fn, "q_row", q_row, _u8, x.shape),
-        _need_n(fn, "s_row", s_row, _u8, _mx_bytes(r, c)), py, pro, prs, _stream(stream)))
+        px, dt, r, c, pres, pg, float(eps), _need(fn, dev, "q_row", q_row, _u8, x.shape),
+        _need_n(fn, dev, "s_row", s_row, _u8, _mx_bytes(r, c)), py, pro, prs, _stream(stream, dev)))
 
 
 def te_rmsnorm_bwd_workspace_bytes(rows: int, cols: int) -> int:
@@ -284,16 +304,17 @@ def te_rmsnorm_bwd_workspace_bytes(rows: int, cols: int) -> int:
 def te_rmsnorm_bwd(dy, s, gamma, rsigma, dx, dgamma, workspace, dres=None, stream=None):
     """Gradients of te_rmsnorm_*: dx (of x and of the residual) and dgamma."""
     fn = "te_rmsnorm_bwd"
+    dev = _device()
     if s.dim() != 2:
         raise ValueError(f"{fn}: s has shape {tuple(s.shape)}, expected [rows, cols]")
     shape, dt = s.shape, s.dtype
-    ps = _need(fn, "s", s, (_bf16, _f32), shape)
-    pw = _need_n(fn, "workspace", workspace, _f32, 0)
+    ps = _need(fn, dev, "s", s, (_bf16, _f32), shape)
+    pw = _need_n(fn, dev, "workspace", workspace, _f32, 0)
     _check(fn, lib().te_rmsnorm_bwd(
-        _need(fn, "dy", dy, _bf16, shape), ps, _in_dtype(s), shape[0], shape[1],
-        _need(fn, "gamma", gamma, _f32, shape[1:]), _need(fn, "rsigma", rsigma, _f32, shape[:1]),
-        _need(fn, "dres", dres, dt, shape, True), _need(fn, "dx", dx, dt, shape),
-        _need(fn, "dgamma", dgamma, _f32, shape[1:]), pw, workspace.numel() * 4, _stream(stream)))
+        _need(fn, dev, "dy", dy, _bf16, shape), ps, _in_dtype(s), shape[0], shape[1],
+        _need(fn, dev, "gamma", gamma, _f32, shape[1:]), _need(fn, dev, "rsigma", rsigma, _f32, shape[:1]),
+        _need(fn, dev, "dres", dres, dt, shape, True), _need(fn, dev, "dx", dx, dt, shape),
+        _need(fn, dev, "dgamma", dgamma, _f32, shape[1:]), pw, workspace.numel() * 4, _stream(stream, dev)))
 
 
 def te_quantize_mxfp8(x, q_row=None, s_row=None, q_col=None, s_col=None, stream=None):
@@ -366,104 +387,113 @@ def _gated_shape(fn, x, w, packed: int = 1):
 def te_gated_gemm_bf16(x, w, act: int, h=None, gu=None, stream=None):
     """h = act(x Wg^T) * (x Wu^T) in bf16 and / or the pre-activations gu = [g, u]."""
     fn = "te_gated_gemm_bf16"
+    dev = _device()
     T, K, F = _gated_shape(fn, x, w)
     _check(fn, lib().te_gated_gemm_bf16(
-        _need(fn, "x", x, _bf16, (T, K)), _need(fn, "w", w, _bf16, (2 * F, K)), act,
-        _need(fn, "h", h, _bf16, (T, F), True), _need(fn, "gu", gu, _bf16, (T, 2 * F), True), T, K, F,
-        _stream(stream)))
+        _need(fn, dev, "x", x, _bf16, (T, K)), _need(fn, dev, "w", w, _bf16, (2 * F, K)), act,
+        _need(fn, dev, "h", h, _bf16, (T, F), True), _need(fn, dev, "gu", gu, _bf16, (T, 2 * F), True), T, K, F,
+        _stream(stream, dev)))
 
 
 def te_gated_gemm_fp8(x, fx: int, w, fw: int, x_scale_inv, w_scale_inv, act: int, h=None, gu=None, q_h=None,
                       h_fmt: int = E4M3, h_scale=None, h_amax=None, h_scale_inv=None, stream=None):
     """te_gated_gemm_bf16 on per-tensor scaled FP8 operands; q_h is h in FP8 for the down projection."""
     fn = "te_gated_gemm_fp8"
+    dev = _device()
     T, K, F = _gated_shape(fn, x, w)
     _check(fn, lib().te_gated_gemm_fp8(
-        _need(fn, "x", x, _u8, (T, K)), fx, _need(fn, "w", w, _u8, (2 * F, K)), fw,
-        _need_n(fn, "x_scale_inv", x_scale_inv, _f32, 1), _need_n(fn, "w_scale_inv", w_scale_inv, _f32, 1), act,
-        _need(fn, "h", h, _bf16, (T, F), True), _need(fn, "gu", gu, _bf16, (T, 2 * F), True),
-        _need(fn, "q_h", q_h, _u8, (T, F), True), h_fmt, _need_n(fn, "h_scale", h_scale, _f32, 1, True),
-        _need_n(fn, "h_amax", h_amax, _f32, 1, True), _need_n(fn, "h_scale_inv", h_scale_inv, _f32, 1, True), T, K, F,
-        _stream(stream)))
+        _need(fn, dev, "x", x, _u8, (T, K)), fx, _need(fn, dev, "w", w, _u8, (2 * F, K)), fw,
+        _need_n(fn, dev, "x_scale_inv", x_scale_inv, _f32, 1), _need_n(fn, dev, "w_scale_inv", w_scale_inv, _f32, 1), act,
+        _need(fn, dev, "h", h, _bf16, (T, F), True), _need(fn, dev, "gu", gu, _bf16, (T, 2 * F), True),
+        _need(fn, dev, "q_h", q_h, _u8, (T, F), True), h_fmt, _need_n(fn, dev, "h_scale", h_scale, _f32, 1, True),
+        _need_n(fn, dev, "h_amax", h_amax, _f32, 1, True), _need_n(fn, dev, "h_scale_inv", h_scale_inv, _f32, 1, True),
+        T, K, F, _stream(stream, dev)))
 
 
 def te_gated_gemm_mxfp8(x, sx, w, sw, act: int, h=None, gu=None, q_h=None, s_h=None, fx: int = E4M3, fw: int = E4M3,
                         stream=None):
     """te_gated_gemm_bf16 on MXFP8 operands; q_h, s_h are h in MXFP8 for the down projection."""
     fn = "te_gated_gemm_mxfp8"
+    dev = _device()
     T, K, F = _gated_shape(fn, x, w)
     _check(fn, lib().te_gated_gemm_mxfp8(
-        _need(fn, "x", x, _u8, (T, K)), fx, _need_n(fn, "sx", sx, _u8, _mx_bytes(T, K)),
-        _need(fn, "w", w, _u8, (2 * F, K)), fw, _need_n(fn, "sw", sw, _u8, _mx_bytes(2 * F, K)), act,
-        _need(fn, "h", h, _bf16, (T, F), True), _need(fn, "gu", gu, _bf16, (T, 2 * F), True),
-        _need(fn, "q_h", q_h, _u8, (T, F), True), _need_n(fn, "s_h", s_h, _u8, _mx_bytes(T, F), True), T, K, F,
-        _stream(stream)))
+        _need(fn, dev, "x", x, _u8, (T, K)), fx, _need_n(fn, dev, "sx", sx, _u8, _mx_bytes(T, K)),
+        _need(fn, dev, "w", w, _u8, (2 * F, K)), fw, _need_n(fn, dev, "sw", sw, _u8, _mx_bytes(2 * F, K)), act,
+        _need(fn, dev, "h", h, _bf16, (T, F), True), _need(fn, dev, "gu", gu, _bf16, (T, 2 * F), True),
+        _need(fn, dev, "q_h", q_h, _u8, (T, F), True), _need_n(fn, dev, "s_h", s_h, _u8, _mx_bytes(T, F), True), T, K, F,
+        _stream(stream, dev)))
 
 
 def te_gated_gemm_nvfp4(x, sx, gx, w, sw, gw, act: int, h=None, gu=None, stream=None):
     """te_gated_gemm_bf16 on NVFP4 operands (packed codes, block scales, tensor scales)."""
     fn = "te_gated_gemm_nvfp4"
+    dev = _device()
     T, K, F = _gated_shape(fn, x, w, 2)
     _check(fn, lib().te_gated_gemm_nvfp4(
-        _need(fn, "x", x, _u8, (T, K // 2)), _need_n(fn, "sx", sx, _u8, _nv_bytes(T, K)),
-        _need_n(fn, "gx", gx, _f32, 1), _need(fn, "w", w, _u8, (2 * F, K // 2)),
-        _need_n(fn, "sw", sw, _u8, _nv_bytes(2 * F, K)), _need_n(fn, "gw", gw, _f32, 1), act,
-        _need(fn, "h", h, _bf16, (T, F), True), _need(fn, "gu", gu, _bf16, (T, 2 * F), True), T, K, F, _stream(stream)))
+        _need(fn, dev, "x", x, _u8, (T, K // 2)), _need_n(fn, dev, "sx", sx, _u8, _nv_bytes(T, K)),
+        _need_n(fn, dev, "gx", gx, _f32, 1), _need(fn, dev, "w", w, _u8, (2 * F, K // 2)),
+        _need_n(fn, dev, "sw", sw, _u8, _nv_bytes(2 * F, K)), _need_n(fn, dev, "gw", gw, _f32, 1), act,
+        _need(fn, dev, "h", h, _bf16, (T, F), True), _need(fn, dev, "gu", gu, _bf16, (T, 2 * F), True), T, K, F,
+        _stream(stream, dev)))
 
 
-def _dgrad_shape(fn, dy, w2, gu, dgu, packed: int = 1):
+def _dgrad_shape(fn, dev, dy, w2, gu, dgu, packed: int = 1):
     """(T, F, N) of dy [T, N / packed] and W2's col copy [F, N / packed], and the pointers of gu and dgu."""
     if dy.dim() != 2 or w2.dim() != 2 or dy.shape[1] != w2.shape[1]:
         raise ValueError(f"{fn}: dy {tuple(dy.shape)} and w2 {tuple(w2.shape)} are not [T, N] and [F, N]")
     T, F = dy.shape[0], w2.shape[0]
-    return (T, F, dy.shape[1] * packed, _need(fn, "gu", gu, _bf16, (T, 2 * F)),
-            _need(fn, "dgu", dgu, _bf16, (T, 2 * F)))
+    return (T, F, dy.shape[1] * packed, _need(fn, dev, "gu", gu, _bf16, (T, 2 * F)),
+            _need(fn, dev, "dgu", dgu, _bf16, (T, 2 * F)))
 
 
 def te_gated_dgrad_fp8(dy, fd: int, w2, fw: int, dy_scale_inv, w2_scale_inv, gu, act: int, dgu, stream=None):
     """Gradients of the pre-activations from dy's row copy [T, N] and W2's col copy [F, N] in FP8."""
     fn = "te_gated_dgrad_fp8"
-    T, F, N, pgu, pdgu = _dgrad_shape(fn, dy, w2, gu, dgu)
+    dev = _device()
+    T, F, N, pgu, pdgu = _dgrad_shape(fn, dev, dy, w2, gu, dgu)
     _check(fn, lib().te_gated_dgrad_fp8(
-        _need(fn, "dy", dy, _u8, (T, N)), fd, _need(fn, "w2", w2, _u8, (F, N)), fw,
-        _need_n(fn, "dy_scale_inv", dy_scale_inv, _f32, 1), _need_n(fn, "w2_scale_inv", w2_scale_inv, _f32, 1), pgu,
-        act, pdgu, T, F, N, _stream(stream)))
+        _need(fn, dev, "dy", dy, _u8, (T, N)), fd, _need(fn, dev, "w2", w2, _u8, (F, N)), fw,
+        _need_n(fn, dev, "dy_scale_inv", dy_scale_inv, _f32, 1), _need_n(fn, dev, "w2_scale_inv", w2_scale_inv, _f32, 1), pgu,
+        act, pdgu, T, F, N, _stream(stream, dev)))
 
 
 def te_gated_dgrad_mxfp8(dy, sd, w2, sw, gu, act: int, dgu, fd: int = E4M3, fw: int = E4M3, stream=None):
     """te_gated_dgrad_fp8 on MXFP8 copies."""
     fn = "te_gated_dgrad_mxfp8"
-    T, F, N, pgu, pdgu = _dgrad_shape(fn, dy, w2, gu, dgu)
+    dev = _device()
+    T, F, N, pgu, pdgu = _dgrad_shape(fn, dev, dy, w2, gu, dgu)
     _check(fn, lib().te_gated_dgrad_mxfp8(
-        _need(fn, "dy", dy, _u8, (T, N)), fd, _need_n(fn, "sd", sd, _u8, _mx_bytes(T, N)),
-        _need(fn, "w2", w2, _u8, (F, N)), fw, _need_n(fn, "sw", sw, _u8, _mx_bytes(F, N)), pgu, act, pdgu, T, F, N,
-        _stream(stream)))
+        _need(fn, dev, "dy", dy, _u8, (T, N)), fd, _need_n(fn, dev, "sd", sd, _u8, _mx_bytes(T, N)),
+        _need(fn, dev, "w2", w2, _u8, (F, N)), fw, _need_n(fn, dev, "sw", sw, _u8, _mx_bytes(F, N)), pgu, act, pdgu, T, F, N,
+        _stream(stream, dev)))
 
 
 def te_gated_dgrad_nvfp4(dy, sd, gd, w2, sw, gw, gu, act: int, dgu, stream=None):
     """te_gated_dgrad_fp8 on NVFP4 copies."""
     fn = "te_gated_dgrad_nvfp4"
-    T, F, N, pgu, pdgu = _dgrad_shape(fn, dy, w2, gu, dgu, 2)
+    dev = _device()
+    T, F, N, pgu, pdgu = _dgrad_shape(fn, dev, dy, w2, gu, dgu, 2)
     _check(fn, lib().te_gated_dgrad_nvfp4(
-        _need(fn, "dy", dy, _u8, (T, N // 2)), _need_n(fn, "sd", sd, _u8, _nv_bytes(T, N)),
-        _need_n(fn, "gd", gd, _f32, 1), _need(fn, "w2", w2, _u8, (F, N // 2)),
-        _need_n(fn, "sw", sw, _u8, _nv_bytes(F, N)), _need_n(fn, "gw", gw, _f32, 1), pgu, act, pdgu, T, F, N,
-        _stream(stream)))
+        _need(fn, dev, "dy", dy, _u8, (T, N // 2)), _need_n(fn, dev, "sd", sd, _u8, _nv_bytes(T, N)),
+        _need_n(fn, dev, "gd", gd, _f32, 1), _need(fn, dev, "w2", w2, _u8, (F, N // 2)),
+        _need_n(fn, dev, "sw", sw, _u8, _nv_bytes(F, N)), _need_n(fn, dev, "gw", gw, _f32, 1), pgu, act, pdgu, T, F, N,
+        _stream(stream, dev)))
 
 
 def te_gated_bwd_bf16(x, w, w2, dy, gu, act: int, dgu, dx=None, dw=None, accumulate: int = 0, stream=None):
     """The BF16 backward pass: dgu from dy [T, N] and w2 [N, F], then dx = dgu w and dw (+)= dgu^T x."""
     fn = "te_gated_bwd_bf16"
+    dev = _device()
     T, K, F = _gated_shape(fn, x, w)
     if dy.dim() != 2:
         raise ValueError(f"{fn}: dy has shape {tuple(dy.shape)}, expected [T, N]")
     N = dy.shape[1]
     _check(fn, lib().te_gated_bwd_bf16(
-        _need(fn, "x", x, _bf16, (T, K)), _need(fn, "w", w, _bf16, (2 * F, K)), _need(fn, "w2", w2, _bf16, (N, F)),
-        _need(fn, "dy", dy, _bf16, (T, N)), _need(fn, "gu", gu, _bf16, (T, 2 * F)), act,
-        _need(fn, "dgu", dgu, _bf16, (T, 2 * F)), _need(fn, "dx", dx, _bf16, (T, K), True),
-        _need(fn, "dw", dw, (_bf16, _f32), (2 * F, K), True), BF16 if dw is None else _out_dtype(dw),
-        int(accumulate), T, K, F, N, _stream(stream)))
+        _need(fn, dev, "x", x, _bf16, (T, K)), _need(fn, dev, "w", w, _bf16, (2 * F, K)), _need(fn, dev, "w2", w2, _bf16, (N, F)),
+        _need(fn, dev, "dy", dy, _bf16, (T, N)), _need(fn, dev, "gu", gu, _bf16, (T, 2 * F)), act,
+        _need(fn, dev, "dgu", dgu, _bf16, (T, 2 * F)), _need(fn, dev, "dx", dx, _bf16, (T, K), True),
+        _need(fn, dev, "dw", dw, (_bf16, _f32), (2 * F, K), True), BF16 if dw is None else _out_dtype(dw),
+        int(accumulate), T, K, F, N, _stream(stream, dev)))
 
 
 def te_scale_bytes(scale_fmt: int, rows: int, cols: int) -> int:

@@ -49,7 +49,7 @@ class GatedMLP:
                              "[K], [2 F, K] and [K, F]")
         self.gamma, self.w, self.w2 = gamma, w, w2
         self.T, self.K, self.F, self.recipe, self.act, self.eps = tokens, K, F, recipe, act, eps
-        self._check_weights("GatedMLP")
+        self._check_weights("GatedMLP", L._device())
         dev, T = w.device, tokens
         bf, u8, f32 = (dict(dtype=t, device=dev) for t in (torch.bfloat16, torch.uint8, torch.float32))
         self.r, self.y, self.h = torch.empty(T, K, **bf), torch.empty(T, K, **bf), torch.empty(T, F, **bf)
@@ -87,14 +87,14 @@ class GatedMLP:
         self.step_idx = int(sd["step"])
 
     # ---- checks: before the first launch of a pass, whose calls take addresses and sizes as they are ----
-    def _operand(self, fn: str, name: str, t: torch.Tensor, shape: tuple) -> None:
+    def _operand(self, fn: str, dev: int, name: str, t: torch.Tensor, shape: tuple) -> None:
         """A tensor that the BF16 GEMMs or the quantizers (which take fp32 too) read."""
-        L._need(fn, name, t, torch.bfloat16 if self.recipe == "bf16" else (torch.bfloat16, torch.float32), shape)
+        L._need(fn, dev, name, t, torch.bfloat16 if self.recipe == "bf16" else (torch.bfloat16, torch.float32), shape)
 
-    def _check_weights(self, fn: str) -> None:
-        L._need(fn, "gamma", self.gamma, torch.float32, (self.K,))
-        self._operand(fn, "w", self.w, (2 * self.F, self.K))
-        self._operand(fn, "w2", self.w2, (self.K, self.F))
+    def _check_weights(self, fn: str, dev: int) -> None:
+        L._need(fn, dev, "gamma", self.gamma, torch.float32, (self.K,))
+        self._operand(fn, dev, "w", self.w, (2 * self.F, self.K))
+        self._operand(fn, dev, "w2", self.w2, (self.K, self.F))
 
     # ---- quantization of one tensor under the recipe --------------------------------------------
     def _quantize(self, name: str, t: torch.Tensor, fmt: int, row: bool = True) -> None:
@@ -117,9 +117,10 @@ class GatedMLP:
     # ---- passes ----------------------------------------------------------------------------------
     def forward(self, x: torch.Tensor, residual: torch.Tensor):
         E4, tokens = L.E4M3, (self.T, self.K)
-        self._check_weights("GatedMLP.forward")
-        L._need("GatedMLP.forward", "x", x, torch.bfloat16, tokens)
-        L._need("GatedMLP.forward", "residual", residual, torch.bfloat16, tokens, True)
+        fn, dev = "GatedMLP.forward", L._device()
+        self._check_weights(fn, dev)
+        L._need(fn, dev, "x", x, torch.bfloat16, tokens)
+        L._need(fn, dev, "residual", residual, torch.bfloat16, tokens, True)
         if self.recipe == "bf16":
             L.te_rmsnorm_fp8(x, self.gamma, self.eps, E4, residual=residual, res_out=self.r, y=self.y, rsigma=self.rsigma)
             L.te_gated_gemm_bf16(self.y, self.w, self.act, h=self.h, gu=self.gu)
@@ -143,9 +144,10 @@ class GatedMLP:
 
     def backward(self, dout: torch.Tensor, dr: torch.Tensor | None = None) -> None:
         E4, E5, MN = L.E4M3, L.E5M2, L.MN_MAJOR
-        self._check_weights("GatedMLP.backward")
-        self._operand("GatedMLP.backward", "dout", dout, (self.T, self.K))
-        L._need("GatedMLP.backward", "dr", dr, torch.bfloat16, (self.T, self.K), True)
+        fn, dev = "GatedMLP.backward", L._device()
+        self._check_weights(fn, dev)
+        self._operand(fn, dev, "dout", dout, (self.T, self.K))
+        L._need(fn, dev, "dr", dr, torch.bfloat16, (self.T, self.K), True)
         if self.recipe == "bf16":
             L.te_gemm_bf16(dout, self.h, self.dw2, None, MN, MN)
             L.te_gated_bwd_bf16(self.y, self.w, self.w2, dout, self.gu, self.act, self.dgu, dx=self.dy, dw=self.dw)
