@@ -21,6 +21,7 @@
 #pragma once
 
 #include "gated_decode.cuh"
+#include "launch_setup.cuh"
 
 namespace te {
 namespace {
@@ -357,34 +358,6 @@ inline bool stream_takes(int kind, int64_t T, int k_tiles, int split, bool idle)
   return split == 2 && !block && k_tiles >= 32 && T <= 96;
 }
 
-// Once a device: the shared memory of the two forms of a kernel, and how many clusters of 2, 4 and 8 CTAs
-// of the shared form run at once.
-struct StreamSetup {
-  bool done;
-  int most[3];
-  template <typename... P>
-  te_status set(void (*single)(P...), void (*shared)(P...), int threads, int smem) {
-    if (done) return TE_OK;
-    if (cudaFuncSetAttribute(single, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
-        cudaFuncSetAttribute(shared, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-      return record_cuda(cudaGetLastError());
-    for (int i = 0; i < 3; ++i) {
-      cudaLaunchAttribute attr[1];
-      attr[0].id = cudaLaunchAttributeClusterDimension;
-      attr[0].val.clusterDim = {2u << i, 1u, 1u};
-      cudaLaunchConfig_t cfg = {};
-      cfg.gridDim = dim3(2u << i, 1, 1);
-      cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
-      cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-      cfg.attrs = attr;
-      cfg.numAttrs = 1;
-      if (cudaOccupancyMaxActiveClusters(&most[i], shared, &cfg) != cudaSuccess) return record_cuda(cudaGetLastError());
-    }
-    done = true;
-    return TE_OK;
-  }
-};
-
 // launch_dependent of clusters of `split` CTAs.
 template <typename... Params, typename... Args>
 cudaError_t launch_dependent_clusters(void (*kernel)(Params...), int split, dim3 grid, dim3 block, size_t smem,
@@ -414,8 +387,8 @@ te_status launch_stream(const DecodeArgs& a, uint32_t xfmt, uint32_t wfmt, cudaS
   int dev_id = 0;
   cudaGetDevice(&dev_id);
   if (dev_id < 0 || dev_id >= 64) return TE_ERR_CUDA;
-  te_status s = setup[dev_id].set(gated_stream_kernel<KIND, NP, kSharedOnly>, gated_stream_kernel<KIND, NP, true>,
-                                  kStrThreads, C::kSmemTotal);
+  te_status s = setup[dev_id].set(kernel_address(gated_stream_kernel<KIND, NP, kSharedOnly>),
+                                  kernel_address(gated_stream_kernel<KIND, NP, true>), kStrThreads, C::kSmemTotal);
   if (s != TE_OK) return s;
   const uint64_t row_bytes = static_cast<uint64_t>(a.K) * (KIND == kBF16 ? 2 : 1);
   const int tiles = (a.F + 63) / 64;

@@ -326,8 +326,8 @@ te_status launch_stream_block(const DecodeArgs& a, uint32_t xfmt, uint32_t wfmt,
   int dev_id = 0;
   cudaGetDevice(&dev_id);
   if (dev_id < 0 || dev_id >= 64) return TE_ERR_CUDA;
-  te_status s = setup[dev_id].set(gated_stream_block_kernel<KIND, NP, kSharedOnly>,
-                                  gated_stream_block_kernel<KIND, NP, true>, kStbThreads, C::kSmemTotal);
+  te_status s = setup[dev_id].set(kernel_address(gated_stream_block_kernel<KIND, NP, kSharedOnly>),
+                                  kernel_address(gated_stream_block_kernel<KIND, NP, true>), kStbThreads, C::kSmemTotal);
   if (s != TE_OK) return s;
   const uint64_t row_bytes = static_cast<uint64_t>(a.K) / (KIND == kMXFP8 ? 1 : 2);
   const int tiles = a.F / 128;
