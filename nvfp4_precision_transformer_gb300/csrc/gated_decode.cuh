@@ -191,22 +191,18 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1) gated_decode_kernel(DecodeA
 
 template <int W, int X, int NT>
 te_status launch_decode(const DecodeArgs& a, cudaStream_t st) {
-  static bool attr_set[64] = {false};
-  int dev_id = 0;
-  cudaGetDevice(&dev_id);
-  if (dev_id < 0 || dev_id >= 64) return TE_ERR_CUDA;
-  if (!attr_set[dev_id]) {
-    if (cudaFuncSetAttribute(gated_decode_kernel<W, X, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448) !=
-        cudaSuccess)
-      return record_cuda(cudaGetLastError());
-    attr_set[dev_id] = true;
-  }
+  static PerDevice<SharedMemory> ready;
+  te_status s = TE_OK;
+  if (!ready.get(&s, [](SharedMemory* m) {
+        return allow_shared_memory(m, kernel_address(gated_decode_kernel<W, X, NT>), 232448);
+      }))
+    return s;
   const int units = a.F / 8;
   const int grid = units < num_sms() ? units : num_sms();
   const size_t smem = decode_smem(a.T, a.K, W == kDecBF16 ? 2 : 1);
   const dim3 g(static_cast<unsigned>(grid), 1, 1), block(32 * kDecWarps, 1, 1);
   if (a.amax) {
-    const te_status s = zero_amax(a.amax, st);
+    s = zero_amax(a.amax, st);
     if (s != TE_OK) return s;
   }
   const cudaError_t e = launch_dependent(gated_decode_kernel<W, X, NT>, g, block, smem, st, a);

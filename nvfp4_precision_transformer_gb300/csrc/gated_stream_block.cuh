@@ -322,18 +322,18 @@ te_status launch_stream_block(const DecodeArgs& a, uint32_t xfmt, uint32_t wfmt,
   using C = StbCfg<KIND, NP>;
   constexpr bool kSharedOnly = NP == 128;
   *taken = true;
-  static StreamSetup setup[64] = {};
-  int dev_id = 0;
-  cudaGetDevice(&dev_id);
-  if (dev_id < 0 || dev_id >= 64) return TE_ERR_CUDA;
-  te_status s = setup[dev_id].set(kernel_address(gated_stream_block_kernel<KIND, NP, kSharedOnly>),
-                                  kernel_address(gated_stream_block_kernel<KIND, NP, true>), kStbThreads, C::kSmemTotal);
-  if (s != TE_OK) return s;
+  static PerDevice<StreamSetup> setups;
+  te_status s = TE_OK;
+  const StreamSetup* setup = setups.get(&s, [](StreamSetup* m) {
+    return m->set(kernel_address(gated_stream_block_kernel<KIND, NP, kSharedOnly>),
+                  kernel_address(gated_stream_block_kernel<KIND, NP, true>), kStbThreads, C::kSmemTotal);
+  });
+  if (setup == nullptr) return s;
   const uint64_t row_bytes = static_cast<uint64_t>(a.K) / (KIND == kMXFP8 ? 1 : 2);
   const int tiles = a.F / 128;
   const int k_tiles = static_cast<int>((row_bytes + 127) / 128);
-  const int split = stream_split(tiles, k_tiles, setup[dev_id].most);
-  if (!stream_takes(KIND, a.T, k_tiles, split, tiles <= setup[dev_id].most[0])) {
+  const int split = stream_split(tiles, k_tiles, setup->most);
+  if (!stream_takes(KIND, a.T, k_tiles, split, tiles <= setup->most[0])) {
     *taken = false;
     return TE_OK;
   }

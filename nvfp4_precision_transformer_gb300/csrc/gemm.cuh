@@ -51,6 +51,7 @@
 
 #include "common.cuh"
 #include "convert.cuh"
+#include "launch_setup.cuh"
 
 namespace te {
 namespace {
@@ -766,6 +767,11 @@ uint32_t make_idesc(int kind, uint32_t afmt, uint32_t bfmt, int m) {
   return d;
 }
 
+// CTA pairs (CG = 1: CTAs) that run at once; SPLIT: clusters of two and of four pairs.
+struct GemmSetup {
+  int units, fours;
+};
+
 template <int KIND, int CG = 1, int EPI = kPlain, bool SPLIT = false>
 te_status launch_gemm(const void* A, const void* B, int64_t row_bytes, const uint8_t* sfa, const uint8_t* sfb,
                       int64_t sf_katoms, const float* alpha_a, const float* alpha_b, const float* bias, void* D,
@@ -775,12 +781,7 @@ te_status launch_gemm(const void* A, const void* B, int64_t row_bytes, const uin
                       int max_split = 4) {
   using C = Cfg<KIND, CG, EPI>;
   static_assert(!SPLIT || (CG == 2 && !C::kBlockScaled), "split K: pairs, BF16 and FP8");
-  static bool attr_set[64] = {false};
-  static int max_clusters[64] = {0};      // CTA pairs at once; SPLIT: clusters of two and of four pairs
-  static int max_clusters4[64] = {0};
-  int dev_id = 0;
-  cudaGetDevice(&dev_id);
-  if (dev_id < 0 || dev_id >= 64) return TE_ERR_CUDA;
+  static PerDevice<GemmSetup> setups;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -794,7 +795,8 @@ te_status launch_gemm(const void* A, const void* B, int64_t row_bytes, const uin
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (!attr_set[dev_id]) {
+  te_status s = TE_OK;
+  const GemmSetup* setup = setups.get(&s, [&](GemmSetup* m) {
     if (cudaFuncSetAttribute(gemm_kernel<KIND, CG, EPI, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemTotal) !=
         cudaSuccess)
       return record_cuda(cudaGetLastError());
@@ -808,9 +810,8 @@ te_status launch_gemm(const void* A, const void* B, int64_t row_bytes, const uin
           cudaGetLastError();   // no such cluster: not taken
           mc = 0;
         }
-        (pairs == 4 ? max_clusters4 : max_clusters)[dev_id] = mc;
+        (pairs == 4 ? m->fours : n) = mc;
       }
-      n = max_clusters[dev_id];
     } else if (CG > 1) {
       // clusters that can be resident at once (a GPC may leave an SM unpaired)
       cfg.gridDim = dim3(CG * n, 1, 1);
@@ -819,12 +820,14 @@ te_status launch_gemm(const void* A, const void* B, int64_t row_bytes, const uin
         return record_cuda(cudaGetLastError());
       n = mc < n ? mc : n;
     }
-    max_clusters[dev_id] = n;
-    attr_set[dev_id] = true;
-  }
+    m->units = n;
+    return TE_OK;
+  });
+  if (setup == nullptr) return s;
+  attr[0].val.clusterDim.x = CG;
   CUtensorMap ta, tb;
-  te_status s = a_mn ? make_tmap_2d(&ta, A, static_cast<uint64_t>(M) * 2, static_cast<uint64_t>(K), 64)
-                     : make_tmap_2d(&ta, A, static_cast<uint64_t>(row_bytes), static_cast<uint64_t>(M), BM);
+  s = a_mn ? make_tmap_2d(&ta, A, static_cast<uint64_t>(M) * 2, static_cast<uint64_t>(K), 64)
+           : make_tmap_2d(&ta, A, static_cast<uint64_t>(row_bytes), static_cast<uint64_t>(M), BM);
   if (s != TE_OK) return s;
   s = b_mn ? make_tmap_2d(&tb, B, static_cast<uint64_t>(N) * 2, static_cast<uint64_t>(K), 64)
            : make_tmap_2d(&tb, B, static_cast<uint64_t>(row_bytes), static_cast<uint64_t>(N), C::kBRows);
@@ -881,8 +884,8 @@ te_status launch_gemm(const void* A, const void* B, int64_t row_bytes, const uin
     // outweigh the exchange (3 us).  One pair / shared: gated BF16 128 tokens, K = 1024, F = 1024 (8 tiles
     // of 16 k-tiles) 10.1 / 11.1 us, K = 1536 12.2 / 11.6, K = 2048 14.5 / 12.4; in two, 32 tiles of 32
     // k-tiles 14.9 / 15.4, of 64 23.3 / 19.0, of 128 41.7 / 32.9.
-    if (max_split >= 4 && tiles <= max_clusters4[dev_id] && g.k_tiles >= 24) g.split = 4;
-    else if (max_split >= 2 && tiles <= max_clusters[dev_id] && g.k_tiles >= 48) g.split = 2;
+    if (max_split >= 4 && tiles <= setup->fours && g.k_tiles >= 24) g.split = 4;
+    else if (max_split >= 2 && tiles <= setup->units && g.k_tiles >= 48) g.split = 2;
     if (g.split == 1)
       return launch_gemm<KIND, CG, EPI, false>(A, B, row_bytes, sfa, sfb, sf_katoms, alpha_a, alpha_b, bias, D, out,
                                                accumulate, M, N, K, afmt, bfmt, st, a_mn, b_mn, ep, pdl);
@@ -891,7 +894,7 @@ te_status launch_gemm(const void* A, const void* B, int64_t row_bytes, const uin
   // The fewest CTA pairs that keep the number of waves: every pair runs the same number of
   // tiles (within one), and the SMs left idle leave their share of the power budget to the
   // busy ones (FP8 / MXFP8 layer GEMMs 1.4-1.7 % faster than with one pair per two SMs).
-  int units = tiles < max_clusters[dev_id] ? tiles : max_clusters[dev_id];
+  int units = tiles < setup->units ? tiles : setup->units;
   if (units > 0) {
     const int waves = (tiles + units - 1) / units;
     units = (tiles + waves - 1) / waves;

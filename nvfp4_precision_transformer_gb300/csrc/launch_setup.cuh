@@ -1,23 +1,69 @@
 // What launchers look up once (host code alone).
 #pragma once
 
+#include <atomic>
+#include <mutex>
+
 #include "common.cuh"
 
 namespace te {
 namespace {
+
+// State of each device that is looked up on the first call there.  Host threads may make that call together:
+// one looks up, under the lock, and the flag that it sets last (release) is what the others go by (acquire).
+template <typename T>
+class PerDevice {
+ public:
+  // The current device's state, filled by make(T*) the first time.  Where that fails: nullptr, its status in
+  // *status, and the next call tries again.
+  template <typename Make>
+  const T* get(te_status* status, Make make) {
+    int d = -1;
+    cudaGetDevice(&d);
+    if (d < 0 || d >= kDevices) {
+      *status = TE_ERR_CUDA;
+      return nullptr;
+    }
+    Slot& slot = slots_[d];
+    if (!slot.ready.load(std::memory_order_acquire)) {
+      std::lock_guard<std::mutex> lock(mutex_);
+      if (!slot.ready.load(std::memory_order_relaxed)) {
+        *status = make(&slot.value);
+        if (*status != TE_OK) return nullptr;
+        slot.ready.store(true, std::memory_order_release);
+      }
+    }
+    return &slot.value;
+  }
+
+ private:
+  static constexpr int kDevices = 64;
+  struct Slot {
+    std::atomic<bool> ready{false};
+    T value{};
+  };
+  std::mutex mutex_;
+  Slot slots_[kDevices];
+};
 
 template <typename... P>
 [[maybe_unused]] const void* kernel_address(void (*kernel)(P...)) {
   return reinterpret_cast<const void*>(kernel);
 }
 
-// Once a device: the shared memory of the two forms of a kernel, and how many clusters of 2, 4 and 8 CTAs
-// of the shared form run at once.
+// A kernel's shared memory beyond 48 KB.
+struct SharedMemory {};
+[[maybe_unused]] inline te_status allow_shared_memory(SharedMemory*, const void* kernel, int bytes) {
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+    return record_cuda(cudaGetLastError());
+  return TE_OK;
+}
+
+// The shared memory of the two forms of a stream kernel, and how many clusters of 2, 4 and 8 CTAs of the shared
+// form run at once.
 struct StreamSetup {
-  bool done;
   int most[3];
   te_status set(const void* single, const void* shared, int threads, int smem) {
-    if (done) return TE_OK;
     if (cudaFuncSetAttribute(single, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
         cudaFuncSetAttribute(shared, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
       return record_cuda(cudaGetLastError());
@@ -36,7 +82,6 @@ struct StreamSetup {
         most[i] = 0;
       }
     }
-    done = true;
     return TE_OK;
   }
 };

@@ -18,6 +18,7 @@
 
 #include "common.cuh"
 #include "convert.cuh"
+#include "launch_setup.cuh"
 
 namespace te {
 namespace {
@@ -1327,15 +1328,12 @@ template <typename T, int FMT, bool SR>
 te_status launch_qtile(const void* x, int64_t R, int64_t C, uint8_t* q_row, uint8_t* q_col, TileArgs a,
                        cudaStream_t st) {
   using G = QGeom<T, FMT>;
-  static bool attr_set[64] = {false};
-  int dev_id = 0;
-  cudaGetDevice(&dev_id);
-  if (dev_id >= 0 && dev_id < 64 && !attr_set[dev_id]) {
-    if (cudaFuncSetAttribute(qtile_kernel<T, FMT, SR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             QSmem<T, FMT, SR>::kTotalMax) != cudaSuccess)
-      return record_cuda(cudaGetLastError());
-    attr_set[dev_id] = true;
-  }
+  static PerDevice<SharedMemory> ready;
+  te_status s = TE_OK;
+  if (!ready.get(&s, [](SharedMemory* m) {
+        return allow_shared_memory(m, kernel_address(qtile_kernel<T, FMT, SR>), QSmem<T, FMT, SR>::kTotalMax);
+      }))
+    return s;
   CUtensorMap tin, trow, tcol;
   memset(&tin, 0, sizeof(tin));
   memset(&trow, 0, sizeof(trow));
@@ -1343,7 +1341,7 @@ te_status launch_qtile(const void* x, int64_t R, int64_t C, uint8_t* q_row, uint
   a.do_row = q_row != nullptr;
   a.do_col = q_col != nullptr;
   if (R * C > 0) {
-    te_status s = make_tmap_2d(&tin, x, static_cast<uint64_t>(C) * sizeof(T), static_cast<uint64_t>(R), 64);
+    s = make_tmap_2d(&tin, x, static_cast<uint64_t>(C) * sizeof(T), static_cast<uint64_t>(R), 64);
     if (s == TE_OK && q_row)
       s = make_tmap_2d_boxswz(&trow, q_row, static_cast<uint64_t>(FMT == kQNV ? C / 2 : C), static_cast<uint64_t>(R),
                               G::ROW_W, 64);
@@ -1526,15 +1524,11 @@ te_status te_layernorm_fp8(const void* x, te_dtype in_dtype, int64_t rows, int64
     const int64_t fit = (224 * 1024 - 8 * cols) / (4 * cols);
     const int nw = static_cast<int>(fit < kLnWarps ? fit : kLnWarps);
     const size_t smem = static_cast<size_t>(8 * cols) + static_cast<size_t>(2 * nw) * static_cast<size_t>(cols) * 2;
-    static bool attr_set[64] = {false};
-    int dev_id = 0;
-    cudaGetDevice(&dev_id);
-    if (dev_id >= 0 && dev_id < 64 && !attr_set[dev_id]) {
-      if (cudaFuncSetAttribute(layernorm_fp8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 224 * 1024) !=
-          cudaSuccess)
-        return record_cuda(cudaGetLastError());
-      attr_set[dev_id] = true;
-    }
+    static PerDevice<SharedMemory> ready;
+    if (!ready.get(&s, [](SharedMemory* m) {
+          return allow_shared_memory(m, kernel_address(layernorm_fp8_kernel), 224 * 1024);
+        }))
+      return s;
     int* err = device_error_word();
     if (err == nullptr) return record_cuda(cudaErrorInvalidDevice);
     const int64_t want = (rows + nw - 1) / nw;

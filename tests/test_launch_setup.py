@@ -75,3 +75,58 @@ int main() {
   CHECK(s.set(&s, &s, 192, 200000) == TE_OK && s.most[2] == 19);
   return 0;
 }""")
+
+
+THREADS = r"""
+#include <thread>
+#include <vector>
+struct State { int a, b; };
+int main() {
+  for (int round = 0; round < 200; ++round) {
+    te::PerDevice<State>* p = new te::PerDevice<State>;
+    std::atomic<int> made{0}, wrong{0};
+    std::vector<std::thread> t;
+    for (int i = 0; i < 8; ++i)
+      t.emplace_back([&] {
+        te_status s = TE_OK;
+        const State* v = p->get(&s, [&](State* m) { made++; m->a = round; m->b = ~round; return TE_OK; });
+        if (v == nullptr || s != TE_OK || v->a != round || v->b != ~round) wrong++;
+      });
+    for (auto& x : t) x.join();
+    CHECK(made == 1 && wrong == 0);
+    delete p;
+  }
+  return 0;
+}"""
+
+
+def test_first_call_state_is_published_whole(tmp_path):
+    """Eight threads make the first call at once: one looks up, all see its state complete; under the thread
+    sanitizer where the compiler has one."""
+    run(tmp_path, THREADS)
+    probe = tmp_path / "p.cpp"
+    probe.write_text("int main() { return 0; }")
+    r = subprocess.run([shutil.which("g++"), "-fsanitize=thread", str(probe), "-o", str(tmp_path / "p")], capture_output=True)
+    if r.returncode == 0 and subprocess.run([str(tmp_path / "p")], capture_output=True).returncode == 0:
+        run(tmp_path, THREADS, "-fsanitize=thread")
+
+
+def test_a_failed_look_up_is_tried_again(tmp_path):
+    run(tmp_path, r"""
+int main() {
+  static te::PerDevice<int> p;
+  te_status s = TE_OK;
+  CHECK(p.get(&s, [](int* v) { *v = 3; return TE_ERR_CUDA; }) == nullptr && s == TE_ERR_CUDA);
+  const int* v = p.get(&s, [](int* v) { *v = 4; return TE_OK; });
+  CHECK(v != nullptr && *v == 4 && p.get(&s, [](int*) { return TE_ERR_CUDA; }) == v);
+  return 0;
+}""")
+
+
+def test_no_launcher_has_a_plain_flag():
+    """First-call state is reached through PerDevice (or under the lock of host.cu), never by an unguarded static."""
+    for name in sorted(os.listdir(CSRC)):
+        lines = [line.split("//")[0] for line in open(os.path.join(CSRC, name))]
+        bad = [line.strip() for line in lines if line.lstrip().startswith("static ") and ("[64]" in line or " bool " in line)
+               and "PerDevice" not in line and "constexpr" not in line and "(" not in line]
+        assert not bad, (name, bad)
