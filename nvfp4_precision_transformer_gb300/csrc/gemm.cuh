@@ -767,11 +767,6 @@ uint32_t make_idesc(int kind, uint32_t afmt, uint32_t bfmt, int m) {
   return d;
 }
 
-// CTA pairs (CG = 1: CTAs) that run at once; SPLIT: clusters of two and of four pairs.
-struct GemmSetup {
-  int units, fours;
-};
-
 template <int KIND, int CG = 1, int EPI = kPlain, bool SPLIT = false>
 te_status launch_gemm(const void* A, const void* B, int64_t row_bytes, const uint8_t* sfa, const uint8_t* sfb,
                       int64_t sf_katoms, const float* alpha_a, const float* alpha_b, const float* bias, void* D,
@@ -797,34 +792,9 @@ te_status launch_gemm(const void* A, const void* B, int64_t row_bytes, const uin
   cfg.numAttrs = 1;
   te_status s = TE_OK;
   const GemmSetup* setup = setups.get(&s, [&](GemmSetup* m) {
-    if (cudaFuncSetAttribute(gemm_kernel<KIND, CG, EPI, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemTotal) !=
-        cudaSuccess)
-      return record_cuda(cudaGetLastError());
-    int n = num_sms() / CG;
-    if (SPLIT) {
-      for (int pairs = 4; pairs >= 2; pairs -= 2) {
-        attr[0].val.clusterDim.x = static_cast<unsigned>(2 * pairs);
-        cfg.gridDim = dim3(static_cast<unsigned>(num_sms() / (2 * pairs) * 2 * pairs), 1, 1);
-        int mc = 0;
-        if (cudaOccupancyMaxActiveClusters(&mc, gemm_kernel<KIND, CG, EPI, SPLIT>, &cfg) != cudaSuccess) {
-          cudaGetLastError();   // no such cluster: not taken
-          mc = 0;
-        }
-        (pairs == 4 ? m->fours : n) = mc;
-      }
-    } else if (CG > 1) {
-      // clusters that can be resident at once (a GPC may leave an SM unpaired)
-      cfg.gridDim = dim3(CG * n, 1, 1);
-      int mc = 0;
-      if (cudaOccupancyMaxActiveClusters(&mc, gemm_kernel<KIND, CG, EPI, SPLIT>, &cfg) != cudaSuccess || mc <= 0)
-        return record_cuda(cudaGetLastError());
-      n = mc < n ? mc : n;
-    }
-    m->units = n;
-    return TE_OK;
+    return m->set(kernel_address(gemm_kernel<KIND, CG, EPI, SPLIT>), CG, SPLIT, C::kSmemTotal, cfg);
   });
   if (setup == nullptr) return s;
-  attr[0].val.clusterDim.x = CG;
   CUtensorMap ta, tb;
   s = a_mn ? make_tmap_2d(&ta, A, static_cast<uint64_t>(M) * 2, static_cast<uint64_t>(K), 64)
            : make_tmap_2d(&ta, A, static_cast<uint64_t>(row_bytes), static_cast<uint64_t>(M), BM);

@@ -59,6 +59,47 @@ struct SharedMemory {};
   return TE_OK;
 }
 
+// The shared memory of a GEMM kernel, and the CTA pairs (pair size 1: CTAs) that run at once or, where several
+// pairs share a tile, the clusters of two and of four pairs.
+struct GemmSetup {
+  int units, fours;
+  // cfg: the launch's block, shared memory and attributes, the first of them its cluster.
+  te_status set(const void* kernel, int pair, bool shared, int smem, cudaLaunchConfig_t cfg) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+      return record_cuda(cudaGetLastError());
+    cudaLaunchAttribute attr[1] = {cfg.attrs[0]};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const int sms = num_sms();
+    if (shared) {
+      for (int pairs = 4; pairs >= 2; pairs -= 2) {
+        attr[0].val.clusterDim.x = static_cast<unsigned>(2 * pairs);
+        cfg.gridDim = dim3(static_cast<unsigned>(sms / (2 * pairs) * 2 * pairs), 1, 1);
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+          cudaGetLastError();   // no such cluster: not taken
+          n = 0;
+        }
+        (pairs == 4 ? fours : units) = n;
+      }
+      return TE_OK;
+    }
+    units = sms / pair;
+    if (pair > 1) {
+      // pairs that can be resident at once (a GPC may leave an SM unpaired)
+      cfg.gridDim = dim3(static_cast<unsigned>(pair * units), 1, 1);
+      int n = 0;
+      const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+      if (e != cudaSuccess || n <= 0) {
+        cudaGetLastError();
+        return record_cuda(e != cudaSuccess ? e : cudaErrorInvalidConfiguration);
+      }
+      units = n < units ? n : units;
+    }
+    return TE_OK;
+  }
+};
+
 // The shared memory of the two forms of a stream kernel, and how many clusters of 2, 4 and 8 CTAs of the shared
 // form run at once.
 struct StreamSetup {

@@ -15,7 +15,7 @@ STUBS = r"""
 #include <string.h>
 #include "launch_setup.cuh"
 
-static int fail_cluster = 0, pending = 0, recorded = 0, attributes = 0, fail_attribute = 0;
+static int fail_cluster = 0, pending = 0, recorded = 0, attributes = 0, no_room = 0, fail_attribute = 0;
 extern "C" {
 cudaError_t cudaGetDevice(int* d) { *d = 0; return cudaSuccess; }
 cudaError_t cudaGetLastError(void) { int p = pending; pending = 0; return static_cast<cudaError_t>(p); }
@@ -27,11 +27,13 @@ cudaError_t cudaFuncSetAttribute(const void*, cudaFuncAttribute, int) {
 cudaError_t cudaOccupancyMaxActiveClusters(int* n, const void*, const cudaLaunchConfig_t* cfg) {
   const int size = static_cast<int>(cfg->attrs[0].val.clusterDim.x);
   if (size == fail_cluster) return static_cast<cudaError_t>(pending = cudaErrorInvalidClusterSize);
+  if (no_room) return *n = 0, cudaSuccess;
   *n = 152 / size;
   return cudaSuccess;
 }
 }
 namespace te {
+int num_sms() { return 152; }
 te_status record_cuda(cudaError_t e) { if (e != cudaSuccess) ++recorded; return e == cudaSuccess ? TE_OK : TE_ERR_CUDA; }
 }
 #define CHECK(c) do { if (!(c)) { printf("line %d: %s\n", __LINE__, #c); return 1; } } while (0)
@@ -130,3 +132,27 @@ def test_no_launcher_has_a_plain_flag():
         bad = [line.strip() for line in lines if line.lstrip().startswith("static ") and ("[64]" in line or " bool " in line)
                and "PerDevice" not in line and "constexpr" not in line and "(" not in line]
         assert not bad, (name, bad)
+
+
+def test_gemm_pairs_that_cannot_run_are_an_error(tmp_path):
+    """No CTA pair fits, and the query itself says nothing: the call must not return as if it had been made."""
+    run(tmp_path, r"""
+int main() {
+  cudaLaunchAttribute attr[2] = {};
+  cudaLaunchConfig_t cfg = {};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  te::GemmSetup g = {};
+  attr[0].val.clusterDim = {2, 1, 1};
+  CHECK(g.set(&g, 2, false, 200000, cfg) == TE_OK && g.units == 76);
+  no_room = 1;
+  CHECK(g.set(&g, 2, false, 200000, cfg) == TE_ERR_CUDA && recorded == 1);
+  no_room = 0, fail_cluster = 2;
+  CHECK(g.set(&g, 2, false, 200000, cfg) == TE_ERR_CUDA && recorded == 2 && pending == 0);
+  // shared tiles: sizes that cannot run are only not taken
+  fail_cluster = 8;
+  CHECK(g.set(&g, 2, true, 200000, cfg) == TE_OK && g.units == 38 && g.fours == 0 && pending == 0);
+  fail_cluster = 0, no_room = 1;
+  CHECK(g.set(&g, 2, true, 200000, cfg) == TE_OK && g.units == 0 && g.fours == 0);
+  return 0;
+}""")
