@@ -341,8 +341,10 @@ te_status te_gemm_nvfp4(const uint8_t* A, const uint8_t* sA, const float* gA, co
  * two halves of w start at whole 128-row groups of the scale layout).  T = 0 is a no-op but
  * for the amax and 1 / scale.  Which kernel a call takes goes by its sizes alone (few tokens
  * have kernels of their own), and sums run in a fixed order, so the same call gives the same
- * bits every time.  The first call on a device looks up attributes and addresses: make it
- * before any stream capture. */
+ * bits every time.  The first call of the library on a device looks up addresses: make one, of
+ * any form, before a stream capture.  The attributes of a kernel (one each for the operand
+ * kind and formats, up to 8, 16, 24, 32, 64, 128 or more tokens, a shared contraction) are looked
+ * up on the first call that takes it, which may itself be captured. */
 enum { TE_ACT_SILU = 0, TE_ACT_GELU = 1 };
 
 te_status te_gated_gemm_bf16(const void* x, const void* w, int act, void* h, void* gu, int64_t T, int64_t K, int64_t F,
