@@ -48,6 +48,7 @@
 #pragma once
 
 #include <cuda_bf16.h>
+#include <float.h>
 
 #include "common.cuh"
 #include "convert.cuh"
