@@ -7,17 +7,18 @@
 //             dgamma = sum over the rows of dy * xhat
 //
 // Both are bound by HBM (15872 x 4096 bf16 on 6.8 TB/s: forward with every output and MXFP8 88 us in the
-// kernel, 6.65 TB/s; backward 77 us, 6.75 TB/s, and 4 us for dgamma's sums).  A row belongs to WPR warps
+// kernel, 6.65 TB/s; backward with dgamma's sums 82 us a call, 6.3 TB/s).  A row belongs to WPR warps
 // (1 to 16), each lane holding up to four (backward: two) chunks of eight columns in registers, so
 // every tensor is read once; the row's sum is a butterfly over the lanes and one exchange through
 // shared memory between the row's warps.  Groups walk the rows with the grid's stride, the next row's
-// loads in flight while one is reduced and written, and gamma comes from L1.  All sums are fp32 in a
-// fixed order, so results do not depend on timing.
+// loads in flight while one is reduced and written; gamma comes from L1 (backward: shared memory).  All
+// sums are fp32 in a fixed order, so results do not depend on timing.
 #include <cuda_bf16.h>
 #include <math.h>
 
 #include "common.cuh"
 #include "convert.cuh"
+#include "launch_setup.cuh"
 
 namespace te {
 namespace {
@@ -246,17 +247,16 @@ struct NormBwdArgs {
   float* partial;   // [gridDim.x, cols]
 };
 
-// Two chunks a lane and two CTAs per SM, with the next row in flight in bf16 (15872 x 4096: 87.7 us;
-// without it 105.1, four chunks 96.7, three CTAs 94.2 and, with it, spilled, 132.5).  In fp32 the
-// second row would take the registers of the second CTA's warps: 151 us without, 152 with it
-// (30000 x 768: 59.9 / 74.7), four chunks 217.
+// Two chunks a lane and two CTAs per SM, with the next row in flight in bf16 (15872 x 4096, of one early build,
+// 87.7 us; without it 105.1, four chunks 96.7, three CTAs 94.2 and, with it, spilled, 132.5).  In fp32
+// the second row would take the registers of the second CTA's warps: 151 us without, 152 with it
+// (30000 x 768: 59.9 / 74.7), four chunks 217.  Now: fp32 143 us and 54.
 template <typename T, int WPR, int CH>
 __global__ void __launch_bounds__(32 * cta_warps(WPR), WPR <= 8 ? 2 : 1) rmsnorm_bwd_kernel(NormBwdArgs a) {
   constexpr int GR = cta_rows(WPR);
   constexpr bool kAhead = sizeof(T) == 2 && CH == 2;   // the next row's loads before this row is reduced
-  constexpr bool kHold = CH == 2;                      // gamma in registers
   __shared__ float red[GR][2][WPR];
-  extern __shared__ __align__(16) float cols_sum[];   // [GR - 1][cols]
+  extern __shared__ __align__(16) float cols_sum[];   // [GR - 1][cols], then gamma
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int grp = warp / WPR, wr = warp % WPR;
   const int64_t C = a.cols;
@@ -291,26 +291,22 @@ __global__ void __launch_bounds__(32 * cta_warps(WPR), WPR <= 8 ? 2 : 1) rmsnorm
     }
   };
   dev::pdl_wait();
-  // a lane's columns are the same in every row: gamma once (four chunks of it would not fit), not behind
-  // each row's stores, which ordinary loads do not pass (15872 x 4096: 98.8 us
-  // so, 83.8 held; fp32 151, 142)
-  float2 gam[kHold ? CH : 1][4] = {};
-  if (kHold) {
-#pragma unroll
-    for (int t = 0; t < CH; ++t)
-      if (col0 + 256 * t < C) ld8(a.gamma + col0 + 256 * t, gam[kHold ? t : 0]);
-  }
-  auto gamma8 = [&](int t, float2 (&g)[4]) {
-    if (kHold) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) g[i] = gam[kHold ? t : 0][i];
-    } else {
-      ld8(a.gamma + col0 + 256 * t, g);
-    }
+  // gamma once into shared memory, the two halves of its chunks of eight apart (reads without bank conflicts):
+  // loaded from L1 in every row it waits behind the stores, which ordinary loads do not pass (15872 x 4096 bf16
+  // 98.8 us a call, in registers 84.8, so 82.2-82.9; 4000 x 16384 fp32, four chunks a lane, 229 from L1, so 165)
+  float4* sgam = reinterpret_cast<float4*>(cols_sum + (GR - 1) * C);
+  const int chunks = static_cast<int>(C >> 3);
+  for (int i = threadIdx.x; i < 2 * chunks; i += blockDim.x)
+    sgam[(i & 1) * chunks + (i >> 1)] = reinterpret_cast<const float4*>(a.gamma)[i];
+  auto gamma8 = [&](int col, float2 (&g)[4]) {
+    const float4 u = sgam[col >> 3], v = sgam[chunks + (col >> 3)];
+    g[0] = make_float2(u.x, u.y), g[1] = make_float2(u.z, u.w);
+    g[2] = make_float2(v.x, v.y), g[3] = make_float2(v.z, v.w);
   };
   RowRegs cur;
   int64_t row = static_cast<int64_t>(blockIdx.x) * GR + grp;
   if (kAhead) load(cur, row);
+  __syncthreads();
   for (int turn = 0; row < a.rows; row += step, turn ^= 1) {
     RowRegs nxt;
     if (kAhead) load(nxt, row + step);
@@ -321,7 +317,7 @@ __global__ void __launch_bounds__(32 * cta_warps(WPR), WPR <= 8 ? 2 : 1) rmsnorm
     for (int t = 0; t < CH; ++t) {
       const int col = col0 + 256 * t;
       float2 g[4] = {};
-      if (col < C) gamma8(t, g);
+      if (col < C) gamma8(col, g);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float2 w = __fmul2_rn(cur.d[t].pair(i), __fmul2_rn(cur.x[t].pair(i), rs2));   // dy * xhat
@@ -337,7 +333,7 @@ __global__ void __launch_bounds__(32 * cta_warps(WPR), WPR <= 8 ? 2 : 1) rmsnorm
       const int col = col0 + 256 * t;
       if (col >= C) break;
       float2 g[4], o[4];
-      gamma8(t, g);
+      gamma8(col, g);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float2 p = __fmul2_rn(cur.d[t].pair(i), g[i]);
@@ -445,16 +441,24 @@ te_status launch_norm(NormArgs& a, cudaStream_t st) {
 }
 
 template <typename T>
-cudaError_t launch_norm_bwd(const NormBwdArgs& a, int wpr, int grid, cudaStream_t st) {
+te_status launch_norm_bwd(const NormBwdArgs& a, int wpr, int grid, cudaStream_t st) {
   void (*kernel)(NormBwdArgs) = wpr == 1                    ? rmsnorm_bwd_kernel<T, 1, 2>
                                 : wpr == 2                  ? rmsnorm_bwd_kernel<T, 2, 2>
                                 : wpr == 4                  ? rmsnorm_bwd_kernel<T, 4, 2>
                                 : wpr == 8                  ? rmsnorm_bwd_kernel<T, 8, 2>
                                 : a.cols <= 16 * 32 * 8 * 2 ? rmsnorm_bwd_kernel<T, 16, 2>
                                                             : rmsnorm_bwd_kernel<T, 16, 4>;
-  const size_t smem = static_cast<size_t>(cta_rows(wpr) - 1) * static_cast<size_t>(a.cols) * sizeof(float);
-  return launch_dependent(kernel, dim3(static_cast<unsigned>(grid), 1, 1),
-                          dim3(static_cast<unsigned>(32 * cta_warps(wpr)), 1, 1), smem, st, a);
+  const size_t smem = static_cast<size_t>(cta_rows(wpr)) * static_cast<size_t>(a.cols) * sizeof(float);
+  if (a.cols > 16 * 32 * 8 * 2) {   // up to 64 KB of gamma
+    static PerDevice<SharedMemory> ready;
+    te_status s = TE_OK;
+    if (!ready.get(&s, [](SharedMemory* m) {
+          return allow_shared_memory(m, kernel_address(rmsnorm_bwd_kernel<T, 16, 4>), kMaxCols * sizeof(float));
+        }))
+      return s;
+  }
+  return record_cuda(launch_dependent(kernel, dim3(static_cast<unsigned>(grid), 1, 1),
+                                      dim3(static_cast<unsigned>(32 * cta_warps(wpr)), 1, 1), smem, st, a));
 }
 
 te_status check_norm(const void* x, te_dtype in, int64_t rows, int64_t cols, const float* gamma, float eps,
@@ -552,12 +556,12 @@ te_status te_rmsnorm_bwd(const void* dy, const void* s, te_dtype in_dtype, int64
   NormBwdArgs a = {static_cast<const __nv_bfloat16*>(dy), s, dres, gamma, rsigma, rows, cols, dx, workspace};
   const int wpr = warps_per_row(cols, 2);
   const int grid = walk_grid(rows, wpr);
-  cudaError_t e = in_dtype == TE_BF16 ? launch_norm_bwd<__nv_bfloat16>(a, wpr, grid, st)
-                                      : launch_norm_bwd<float>(a, wpr, grid, st);
-  if (e != cudaSuccess) return record_cuda(e);
+  const te_status launched = in_dtype == TE_BF16 ? launch_norm_bwd<__nv_bfloat16>(a, wpr, grid, st)
+                                                 : launch_norm_bwd<float>(a, wpr, grid, st);
+  if (launched != TE_OK) return launched;
   count_launch();
   // the sums' launch overlaps the end of the first kernel
-  e = launch_dependent(dgamma_kernel, dim3(static_cast<unsigned>((cols + 31) / 32), 1, 1),
+  const cudaError_t e = launch_dependent(dgamma_kernel, dim3(static_cast<unsigned>((cols + 31) / 32), 1, 1),
                                          dim3(1024, 1, 1), 0, st, static_cast<const float*>(workspace), grid, cols,
                                          dgamma);
   if (e != cudaSuccess) return record_cuda(e);
