@@ -117,3 +117,11 @@ def test_another_current_device(library, name, monkeypatch):
             value.index = 1
     fn(**args)
     assert len(library.calls) == 1
+
+
+def test_scale_sizes_are_the_librarys():
+    """The checks' own arithmetic of scale tensors' sizes, which spares them a call."""
+    for rows in (0, 1, 16, 127, 128, 129, 4096):
+        for cols in (32, 64, 96, 128, 256, 288, 4096, 4128):
+            assert L._mx_bytes(rows, cols) == te.te_scale_bytes(te.E8M0, rows, cols)
+            assert L._nv_bytes(rows, cols) == te.te_scale_bytes(te.UE4M3, rows, cols)
