@@ -276,7 +276,9 @@ te_status te_gated_bwd_bf16(const void* x, const void* w, const void* w2, const 
   // (1001 tokens, K = N = 768, F = 2048: dX has 12 tiles for 76 pairs).
   s = launch_gemm<kBF16, 2, kDgrad, true>(dy, w2, N * 2, nullptr, nullptr, 0, nullptr, nullptr, nullptr, nullptr,
                                           TE_BF16, 0, T, F, N, 1u, 1u, st, 0, 1, ep, kPdlChain);
-  // dX = dGU W (W [2 F, K] MN-major);  dW = dGU^T X (both MN-major).  dX's tiles are shared between CTA
+  // dX = dGU W (W [2 F, K] MN-major);  dW = dGU^T X (both MN-major).  They contract dg and du as stored, rounded
+  // to bf16: the tensor cores take no wider operand, and a second one for what the rounding drops would double
+  // their work.  Their outputs are then 0.0023 off (relative Frobenius), two roundings, where one leaves 0.0017.  dX's tiles are shared between CTA
   // pairs only as far as dW's fit beside them, where they fit at all.
   int share = 4;
   if (dx && dw) {

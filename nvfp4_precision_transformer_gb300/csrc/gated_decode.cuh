@@ -9,8 +9,8 @@
 // blocks ahead and across units, so the loads never wait for the arithmetic.  Each unit ends with the
 // warps' partial sums added in warp order through shared memory.
 //
-// One token, K = 4096, F = 16384: BF16 42.7 us (6.28 TB/s; gemm_kernel, whose SMs all read the one line
-// of x at the same time, 84.0), FP8 23.9 us (5.61 TB/s; 43.4).
+// One token, K = 4096, F = 16384: BF16 42.4 us (6.33 TB/s; gemm_kernel, whose SMs all read the one line
+// of x at the same time, 84.0), FP8 24.3 us (5.52 TB/s; 43.4).
 #pragma once
 
 #include "gemm.cuh"
@@ -222,12 +222,16 @@ te_status launch_decode(const DecodeArgs& a, cudaStream_t st) {
 }
 
 // Whether this kernel takes the call, or the one of gated_stream.cuh (us, this / that):
-//   T = 1, BF16: K = 4096, F = 1024 6.0 / 7.4, F = 4096 14.2 / 14.8, F = 16384 42.4 / 47.9; K = 5120,
-//   F = 1024 7.6 / 8.4, F = 4096 18.1 / 16.6; K = 8192, F = 1024 9.8 / 11.1, F = 4096 25.9 / 24.3;
-//   K = 2048, F = 16384 23.0 / 26.1; K = 1024, F = 4096 6.2 / 6.6, F = 16384 15.2 / 14.9; K = 512,
+//   T = 1, BF16: K = 4096, F = 1024 6.0 / 7.5, F = 4096 14.2 / 14.9, F = 16384 42.4 / 47.2; K = 5120,
+//   F = 1024 7.6 / 8.5, F = 4096 18.1 / 16.6; K = 8192, F = 1024 9.9 / 11.0, F = 4096 25.9 / 24.1;
+//   K = 2048, F = 16384 22.9 / 25.5; K = 1024, F = 4096 6.2 / 6.6, F = 16384 15.2 / 15.0; K = 512,
 //   F = 4096 4.9 / 5.2, F = 16384 12.2 / 9.7;
-//   T = 1, FP8: K = 4096, F = 1024 4.4 / 5.5, F = 16384 24.4 / 25.3; K = 2048, F = 4096 6.7 / 6.6, F = 16384
-//   16.5 / 15.0; K = 512, F = 4096 4.8 / 4.3, F = 16384 11.8 / 7.3;
+//   T = 1, FP8: K = 4096, F = 1024 4.3 / 5.6, F = 16384 24.3 / 25.2; K = 2048, F = 4096 6.7 / 6.6, F = 16384
+//   16.5 / 14.9; K = 512, F = 4096 4.8 / 4.4, F = 16384 11.8 / 7.3;
+//   T = 2 to 8 as one token: T = 2 and 8, BF16 K = 4096, F = 1024 6.0 and 6.2 / 7.5 and 7.6, F = 16384 42.7 and
+//   43.4 / 47.3 and 44.0, K = 2048, F = 16384 23.1 and 23.5 / 24.8 and 24.7, K = 8192, F = 1024 10.0 and 10.3 /
+//   11.0 and 11.1, K = 512, F = 4096 5.0 and 5.0 / 5.3 and 5.3; FP8 K = 4096, F = 1024 4.3 and 4.4 / 5.6 and
+//   5.7, F = 16384 24.4 and 24.5 / 25.3 and 24.7, K = 8192, F = 1024 6.6 and 6.8 / 7.5 and 7.6;
 //   T = 16: BF16 K = 768, F = 2048 4.3 / 5.5, K = 1024, F = 4096 6.8 / 6.9, F = 8192 9.7 / 9.2, K = 2048,
 //   F = 1024 5.7 / 5.8; FP8 K = 768, F = 2048 3.7 / 5.1, K = 1024, F = 2048 4.1 / 5.0, F = 4096 5.9 / 5.5;
 //   T = 24: BF16 K = 1024, F = 2048 5.5 / 5.8, K = 2048, F = 1024 6.8 / 6.2; FP8 K = 2048, F = 1024 4.9 / 5.2.

@@ -15,8 +15,8 @@
 // leave more SMs idle at smaller F: 24 tokens, K = F = 4096 BF16 18.7 us here, 25.3 so, with one CTA a
 // tile.)  Where the tiles leave SMs idle, clusters of 2, 4 or 8 CTAs share a tile's K (below).
 //
-// 24 tokens, K = 4096, F = 16384: BF16 45.1 us (5.96 TB/s; gemm_kernel 51.5), FP8 25.6 us (5.25 TB/s;
-// 33.2); 64 tokens 48.2 / 52.5 and 28.0 / 30.1.  gemm_kernel's six stages turn round in about 1.7 us
+// 24 tokens, K = 4096, F = 16384: BF16 44.1 us (6.09 TB/s; gemm_kernel 51.5), FP8 24.8 us (5.41 TB/s;
+// 33.2); 64 tokens 46.9 / 49.6 and 27.2 / 27.6.  gemm_kernel's six stages turn round in about 1.7 us
 // (load, MMA, commit), which bounds what an SM can have in flight; these turn round in less and are more.
 #pragma once
 
@@ -341,7 +341,13 @@ inline int stream_split(int tiles, int k_tiles, const int (&most)[3]) {
 //   33 and 64 tokens, few k-tiles: BF16 K = 512, F = 4096 (split 2) 7.0 and 8.1 / 7.6, F = 16384 13.6 and
 //   14.2 / 12.2; FP8 K = 1024, F = 16384 13.5 and 14.2 / 11.9; MXFP8 K = 1024, F = 4096 (split 4) 7.6 and 8.7 /
 //   8.0, F = 8192 (split 2) 9.4 and 11.3 / 9.1, K = 2048, F = 16384 16.8 and 19.0 / 18.6; NVFP4 K = 1024,
-//   F = 4096 6.5 and 7.4 / 7.0, K = 4096, F = 8192 (split 2) 12.2 and 13.6 / 12.7, F = 16384 18.1 and 18.2 / 19.4.
+//   F = 4096 6.5 and 7.4 / 7.0, K = 4096, F = 8192 (split 2) 12.2 and 13.6 / 12.7, F = 16384 18.1 and 18.2 / 19.4;
+//   where the tokens cut, 48 and 49: BF16 K = 512, F = 4096 7.3 and 7.6 / 7.7; MXFP8 K = 1024, F = 4096 8.0 and
+//   8.3 / 8.1, K = 2048, F = 8192 (split 2) 12.5 and 12.8 / 13.0, F = 16384 17.9 and 18.2 / 20.3 and 21.0 (64: 19.1 /
+//   18.5); NVFP4 K = 1024, F = 4096 6.8 and 7.2 / 6.9, K = 4096, F = 8192 (split 2) 12.9 and 13.1 / 13.2;
+//   80 and 81 (few k-tiles): MXFP8 K = F = 2048 9.9 and 10.2 / 10.2, NVFP4 K = 4096, F = 2048 9.7 and 10.1 / 10.9,
+//   FP8 K = F = 2048 (16 k-tiles: all) 7.7 and 8.0 / 9.3; 96 and 97 (split 2): BF16 K = F = 4096 19.0 and 19.3 /
+//   20.1, FP8 K = F = 4096 13.5 and 13.8 / 14.1.
 // `idle`: the tiles leave SMs for a split.
 inline bool stream_takes(int kind, int64_t T, int k_tiles, int split, bool idle) {
   const bool block = kind == kMXFP8 || kind == kNVFP4;

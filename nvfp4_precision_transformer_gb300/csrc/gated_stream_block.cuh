@@ -8,8 +8,8 @@
 // warp 0 producer, warp 1 MMA issuer, warps 2-5 epilogue (lane = column of h; a warp's 32 columns are
 // one MXFP8 block of h), warp 6 scale copier.
 //
-// One token, K = 4096, F = 16384: MXFP8 24.2 us (5.72 TB/s; gemm_kernel 43.2), NVFP4 16.0 us (4.72 TB/s;
-// 27.1); 32 tokens 26.9 / 32.7 and 16.6 / 21.3.  128 tiles leave 24 SMs idle; what is left beside that is
+// One token, K = 4096, F = 16384: MXFP8 23.9 us (5.79 TB/s; gemm_kernel 43.2), NVFP4 15.6 us (4.84 TB/s;
+// 27.1); 32 tokens 26.4 / 32.7 and 15.9 / 21.3.  128 tiles leave 24 SMs idle; what is left beside that is
 // set-up and the first loads' latency (about 4 us).
 #pragma once
 
