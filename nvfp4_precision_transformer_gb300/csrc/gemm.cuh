@@ -132,7 +132,8 @@ struct Cfg {
 // Programmatic dependent launch (bits of pdl): the kernel waits for the one before it after its set-up;
 // it lets the next one be set up once it has itself begun (after that wait); it waits for the one
 // before it only at its end, being independent of its results, so that what follows in the stream
-// finds both complete.
+// finds both complete.  (What it reads was complete before the other kernel let it start, after that one's own
+// wait; and it reads by TMA alone, past L1.)
 constexpr int kPdlWait = 1, kPdlTrigger = 2, kPdlWaitAtEnd = 4;
 constexpr int kPdlChain = kPdlWait | kPdlTrigger;
 
