@@ -6,7 +6,8 @@
  *   saturating FP8 cast / MXFP8 / NVFP4 block quantizers (row-wise and
  *   column-wise copies from one read) -> tensor-core GEMMs (tcgen05 + TMEM,
  *   TMA-fed) with the dequantization scale and bias applied in the epilogue;
- *   beside them RMSNorm with 8-bit outputs and the gated feed-forward projections.
+ *   beside them RMSNorm and LayerNorm with 8-bit outputs, the gated feed-forward projections and the
+ *   linear with bias, activation and residual in its epilogue.
  *
  * Conventions shared by every entry point
  *  - All tensor pointers are DEVICE pointers owned by the caller (for example
@@ -286,6 +287,37 @@ te_status te_rmsnorm_bwd(const void* dy, const void* s, te_dtype in_dtype, int64
                          const float* gamma, const float* rsigma, const void* dres, void* dx, float* dgamma,
                          float* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- LayerNorm with residual -------------------------------------------------------
+ * The same place in a layer with LayerNorm (te_layernorm_fp8 is the form without residual that
+ * casts its bf16 output):
+ *   s = x + residual (residual NULL: s = x);  mu = mean(s);  rsigma = 1 / sqrt(mean((s - mu)^2) + eps);
+ *   y = ((s - mu) * rsigma) * gamma + beta, in fp32.
+ * Types, sizes (any number of rows; cols % 16 == 0, MXFP8 % 32, cols <= 16384; eps >= 0), outputs
+ * and their roundings as for te_rmsnorm_fp8 / te_rmsnorm_mxfp8 above: y in bf16 and y in 8 bits are
+ * separate roundings of the same fp32 value, res_out may be x or residual itself.  gamma, beta
+ * device fp32 [cols]; mu, rsigma (each nullable) fp32 [rows], kept with s for the backward pass. */
+te_status te_add_layernorm_fp8(const void* x, te_dtype in_dtype, int64_t rows, int64_t cols, const void* residual,
+                               const float* gamma, const float* beta, float eps, te_dtype fmt, const float* scale,
+                               uint8_t* q_row, void* y, void* res_out, float* mu, float* rsigma, float* amax_out,
+                               float* scale_inv_out, void* stream);
+te_status te_add_layernorm_mxfp8(const void* x, te_dtype in_dtype, int64_t rows, int64_t cols, const void* residual,
+                                 const float* gamma, const float* beta, float eps, uint8_t* q_row, uint8_t* s_row,
+                                 void* y, void* res_out, float* mu, float* rsigma, void* stream);
+
+/* Its backward pass (and te_layernorm_fp8's, from its x, mu and rsigma).  dy bf16 [rows, cols] (the
+ * gradient of y); s (the forward pass's res_out, or x where there was no residual), dres and dx
+ * in_dtype; mu, rsigma fp32 [rows].  With xhat = (s - mu) * rsigma and p = dy * gamma (fp32):
+ *   dx = rsigma * (p - mean(p) - xhat * mean(p * xhat)) + dres   (dres nullable: the gradient that
+ *        arrives on res_out) -- the gradient of x and of residual alike; dx may be dres or s;
+ *   dgamma, dbeta fp32 [cols] = sums over the rows of dy * xhat and of dy (overwritten; 0 for no rows).
+ * workspace: device memory of at least te_layernorm_bwd_workspace_bytes(rows, cols) bytes (at most 512
+ * rows of two fp32 partial sums a column), 16-byte aligned, no initial contents needed.  The partial
+ * sums are added in a fixed order, so the result does not depend on timing. */
+size_t te_layernorm_bwd_workspace_bytes(int64_t rows, int64_t cols);
+te_status te_layernorm_bwd(const void* dy, const void* s, te_dtype in_dtype, int64_t rows, int64_t cols,
+                           const float* gamma, const float* mu, const float* rsigma, const void* dres, void* dx,
+                           float* dgamma, float* dbeta, float* workspace, size_t workspace_bytes, void* stream);
+
 /* ---- GEMMs ----------------------------------------------------------------------
  * Common: A [M, K], B [N, K] contraction-major; D [M, N] row-major of out_dtype
  * (TE_BF16, round-to-nearest-even, or TE_F32); bias (nullable) device fp32 [N];
@@ -392,6 +424,74 @@ te_status te_gated_dgrad_nvfp4(const uint8_t* dy, const uint8_t* sd, const float
 te_status te_gated_bwd_bf16(const void* x, const void* w, const void* w2, const void* dy, const void* gu, int act,
                             void* dgu, void* dx, void* dw, te_dtype dw_dtype, int accumulate, int64_t T, int64_t K,
                             int64_t F, int64_t N, void* stream);
+
+/* ---- linear with bias, activation and residual ---------------------------------------
+ * One kernel for a linear and what stands around it:
+ *   z = x W^T + bias;  y = act(z) + residual
+ * x [T, K] (T tokens, any number), w [N, K], both contraction-major; bias (nullable) device fp32 [N].
+ * act: TE_ACT_NONE (z itself), TE_ACT_RELU (max(z, 0), a NaN stays one), or one of the two above.
+ * fp32 accumulation; z and act(z) stay fp32 until each output is rounded once.  Outputs, each
+ * nullable, one at least:
+ *   z  bf16 [T, N], what the backward pass keeps (act'(z));
+ *   y  [T, N] of y_dtype (TE_BF16 or TE_F32); residual (nullable, with y only) is of the same type, and
+ *      y may be residual itself;
+ *   q  (FP8, MXFP8) act(z) in 8 bits, the operand of the linear after it; not with a residual
+ *      (TE_ERR_UNSUPPORTED).
+ * N % 16 == 0 (N % 32 where an MXFP8 q is asked for); K % 16 == 0 (BF16, FP8) or K % 32 == 0 (MXFP8,
+ * NVFP4).  T = 0 is a no-op but for the amax and 1 / scale.  Which kernel a call takes goes by its
+ * sizes alone, and sums run in a fixed order, so the same call gives the same bits every time.  First
+ * calls and stream captures as for the gated projections above. */
+enum { TE_ACT_NONE = 2, TE_ACT_RELU = 3 };
+
+te_status te_act_gemm_bf16(const void* x, const void* w, const float* bias, int act, const void* residual, void* z,
+                           void* y, te_dtype y_dtype, int64_t T, int64_t K, int64_t N, void* stream);
+
+/* x, w per-tensor scaled FP8, as te_gemm_fp8.  q (nullable) [T, N] = q_fmt(fl32(act(z) * *q_scale)),
+ * saturating, under DelayedScaling; with it q_amax (nullable) = max |act(z)| in fp32 (NaN if one is
+ * NaN) and q_scale_inv (nullable) = fl32(1 / *q_scale). */
+te_status te_act_gemm_fp8(const uint8_t* x, te_dtype fx, const uint8_t* w, te_dtype fw, const float* x_scale_inv,
+                          const float* w_scale_inv, const float* bias, int act, const void* residual, void* z, void* y,
+                          te_dtype y_dtype, uint8_t* q, te_dtype q_fmt, const float* q_scale, float* q_amax,
+                          float* q_scale_inv, int64_t T, int64_t K, int64_t N, void* stream);
+
+/* MXFP8 operands, as te_gemm_mxfp8.  q [T, N], s_q (nullable as a pair): act(z) as te_quantize_mxfp8
+ * writes a row copy, padding zero. */
+te_status te_act_gemm_mxfp8(const uint8_t* x, te_dtype fx, const uint8_t* sx, const uint8_t* w, te_dtype fw,
+                            const uint8_t* sw, const float* bias, int act, const void* residual, void* z, void* y,
+                            te_dtype y_dtype, uint8_t* q, uint8_t* s_q, int64_t T, int64_t K, int64_t N, void* stream);
+
+/* NVFP4 operands, as te_gemm_nvfp4. */
+te_status te_act_gemm_nvfp4(const uint8_t* x, const uint8_t* sx, const float* gx, const uint8_t* w, const uint8_t* sw,
+                            const float* gw, const float* bias, int act, const void* residual, void* z, void* y,
+                            te_dtype y_dtype, int64_t T, int64_t K, int64_t N, void* stream);
+
+/* Backward: from dy [T, N], the gradient of act(z) W2^T (W2 [N, F], the linear after it), and the forward
+ * pass's z [T, F], in one kernel:
+ *   dh = dy W2;  dz = dh act'(z) (bf16 [T, F]);  dbias fp32 [F] = sum over the tokens of dz (nullable)
+ * dh, and dz as it is added up, stay fp32.  act'(0) = 0 for ReLU.  z may be NULL with TE_ACT_NONE (dz =
+ * dh); dz may be z itself.  The 8- and 4-bit forms take dy's row copy [T, N] and W2's col copy [F, N] with
+ * their scales (N % 16 == 0 for FP8, % 32 for MXFP8 and NVFP4; F % 16 == 0); dx and dw follow by te_gemm_*
+ * on dz's quantized copies.  workspace (with dbias): device memory of at least
+ * te_act_dbias_workspace_bytes(T, F) bytes (a row of fp32 sums for each 32 tokens), 16-byte aligned, no
+ * initial contents needed; the rows are added in a fixed order.  T = 0: dbias = 0. */
+size_t te_act_dbias_workspace_bytes(int64_t T, int64_t F);
+te_status te_act_dgrad_fp8(const uint8_t* dy, te_dtype fd, const uint8_t* w2, te_dtype fw, const float* dy_scale_inv,
+                           const float* w2_scale_inv, const void* z, int act, void* dz, float* dbias, float* workspace,
+                           size_t workspace_bytes, int64_t T, int64_t F, int64_t N, void* stream);
+te_status te_act_dgrad_mxfp8(const uint8_t* dy, te_dtype fd, const uint8_t* sd, const uint8_t* w2, te_dtype fw,
+                             const uint8_t* sw, const void* z, int act, void* dz, float* dbias, float* workspace,
+                             size_t workspace_bytes, int64_t T, int64_t F, int64_t N, void* stream);
+te_status te_act_dgrad_nvfp4(const uint8_t* dy, const uint8_t* sd, const float* gd, const uint8_t* w2, const uint8_t* sw,
+                             const float* gw, const void* z, int act, void* dz, float* dbias, float* workspace,
+                             size_t workspace_bytes, int64_t T, int64_t F, int64_t N, void* stream);
+
+/* The whole backward pass in BF16, for any number of tokens: dz and dbias as above from dy [T, N] and
+ * w2 [N, F], then (each nullable) dx bf16 [T, K] = dz w and dw [F, K] = dz^T x (dw_dtype TE_BF16 or
+ * TE_F32; accumulate = 1 with TE_F32: dw += dz^T x; dbias is overwritten all the same).  w [F, K] is
+ * read for dx, x for dw.  K, F, N multiples of 16.  T = 0: dw = 0 (kept with accumulate), dbias = 0. */
+te_status te_act_bwd_bf16(const void* x, const void* w, const void* w2, const void* dy, const void* z, int act, void* dz,
+                          float* dbias, float* workspace, size_t workspace_bytes, void* dx, void* dw, te_dtype dw_dtype,
+                          int accumulate, int64_t T, int64_t K, int64_t F, int64_t N, void* stream);
 
 /* ---- host helpers ------------------------------------------------------------------ */
 

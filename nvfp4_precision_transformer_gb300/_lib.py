@@ -22,8 +22,8 @@ F32, BF16, E4M3, E5M2, E2M1, E8M0, UE4M3 = range(7)
 # NVFP4 flags
 NVFP4_2D, NVFP4_RHT_COL, NVFP4_SR = 1, 2, 4
 ALGO_MAX, ALGO_MOST_RECENT = 0, 1
-# gated activations
-ACT_SILU, ACT_GELU = 0, 1
+# activations (gated projections: the first two)
+ACT_SILU, ACT_GELU, ACT_NONE, ACT_RELU = 0, 1, 2, 3
 # te_layout
 K_MAJOR, MN_MAJOR = 0, 1
 
@@ -56,6 +56,12 @@ SIGNATURES = {
     "te_rmsnorm_mxfp8": (_st, [_vp, _int, _i64, _i64, _vp, _vp, ctypes.c_float, _vp, _vp, _vp, _vp, _vp, _vp]),
     "te_rmsnorm_bwd_workspace_bytes": (ctypes.c_size_t, [_i64, _i64]),
     "te_rmsnorm_bwd": (_st, [_vp, _vp, _int, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
+    "te_add_layernorm_fp8": (_st, [_vp, _int, _i64, _i64, _vp, _vp, _vp, ctypes.c_float, _int, _vp, _vp, _vp, _vp, _vp,
+                                   _vp, _vp, _vp, _vp]),
+    "te_add_layernorm_mxfp8": (_st, [_vp, _int, _i64, _i64, _vp, _vp, _vp, ctypes.c_float, _vp, _vp, _vp, _vp, _vp, _vp,
+                                     _vp]),
+    "te_layernorm_bwd_workspace_bytes": (ctypes.c_size_t, [_i64, _i64]),
+    "te_layernorm_bwd": (_st, [_vp, _vp, _int, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
     "te_quantize_nvfp4": (_st, [_vp, _int, _i64, _i64, _u32, _u32, _u64, _u64, _vp, _vp,
                                 _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "te_gemm_bf16": (_st, [_vp, _int, _vp, _int, _vp, _vp, _int, _int, _i64, _i64, _i64, _vp]),
@@ -72,6 +78,21 @@ SIGNATURES = {
     "te_gated_dgrad_nvfp4": (_st, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _int, _vp, _i64, _i64, _i64, _vp]),
     "te_gated_bwd_bf16": (_st, [_vp, _vp, _vp, _vp, _vp, _int, _vp, _vp, _vp, _int, _int, _i64, _i64, _i64, _i64,
                                 _vp]),
+    "te_act_gemm_bf16": (_st, [_vp, _vp, _vp, _int, _vp, _vp, _vp, _int, _i64, _i64, _i64, _vp]),
+    "te_act_gemm_fp8": (_st, [_vp, _int, _vp, _int, _vp, _vp, _vp, _int, _vp, _vp, _vp, _int, _vp, _int, _vp, _vp, _vp,
+                              _i64, _i64, _i64, _vp]),
+    "te_act_gemm_mxfp8": (_st, [_vp, _int, _vp, _vp, _int, _vp, _vp, _int, _vp, _vp, _vp, _int, _vp, _vp, _i64, _i64,
+                                _i64, _vp]),
+    "te_act_gemm_nvfp4": (_st, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _int, _vp, _vp, _vp, _int, _i64, _i64, _i64, _vp]),
+    "te_act_dbias_workspace_bytes": (ctypes.c_size_t, [_i64, _i64]),
+    "te_act_dgrad_fp8": (_st, [_vp, _int, _vp, _int, _vp, _vp, _vp, _int, _vp, _vp, _vp, ctypes.c_size_t, _i64, _i64, _i64,
+                               _vp]),
+    "te_act_dgrad_mxfp8": (_st, [_vp, _int, _vp, _vp, _int, _vp, _vp, _int, _vp, _vp, _vp, ctypes.c_size_t, _i64, _i64,
+                                 _i64, _vp]),
+    "te_act_dgrad_nvfp4": (_st, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _int, _vp, _vp, _vp, ctypes.c_size_t, _i64, _i64,
+                                 _i64, _vp]),
+    "te_act_bwd_bf16": (_st, [_vp, _vp, _vp, _vp, _vp, _int, _vp, _vp, _vp, ctypes.c_size_t, _vp, _vp, _int, _int, _i64,
+                              _i64, _i64, _i64, _vp]),
     "te_scale_bytes": (ctypes.c_size_t, [_int, _i64, _i64]),
     "te_scale_unswizzle": (_st, [_int, _i64, _i64, _vp, _vp]),
     "te_status_str": (ctypes.c_char_p, [_int]),
@@ -317,6 +338,52 @@ def te_rmsnorm_bwd(dy, s, gamma, rsigma, dx, dgamma, workspace, dres=None, strea
         _need(fn, dev, "dgamma", dgamma, _f32, shape[1:]), pw, workspace.numel() * 4, _stream(stream, dev)))
 
 
+def te_add_layernorm_fp8(x, gamma, beta, eps: float, fmt: int, scale=None, q_row=None, residual=None, res_out=None, y=None,
+                         mu=None, rsigma=None, amax_out=None, scale_inv_out=None, stream=None):
+    """LayerNorm of x (+ residual), its output in FP8 with a per-tensor scale (and / or y in bf16)."""
+    fn = "te_add_layernorm_fp8"
+    dev = _device()
+    px, dt, r, c, pres, pg, pro, py, prs = _norm_operands(fn, dev, x, gamma, residual, res_out, y, rsigma)
+    _check(fn, lib().te_add_layernorm_fp8(
+        px, dt, r, c, pres, pg, _need(fn, dev, "beta", beta, _f32, (c,)), float(eps), fmt,
+        _need_n(fn, dev, "scale", scale, _f32, 1, True), _need(fn, dev, "q_row", q_row, _u8, x.shape, True), py, pro,
+        _need(fn, dev, "mu", mu, _f32, (r,), True), prs, _need_n(fn, dev, "amax_out", amax_out, _f32, 1, True),
+        _need_n(fn, dev, "scale_inv_out", scale_inv_out, _f32, 1, True), _stream(stream, dev)))
+
+
+def te_add_layernorm_mxfp8(x, gamma, beta, eps: float, q_row, s_row, residual=None, res_out=None, y=None, mu=None,
+                           rsigma=None, stream=None):
+    """LayerNorm of x (+ residual), its output in MXFP8 (E4M3 codes, E8M0 scales in the tensor-core layout)."""
+    fn = "te_add_layernorm_mxfp8"
+    dev = _device()
+    px, dt, r, c, pres, pg, pro, py, prs = _norm_operands(fn, dev, x, gamma, residual, res_out, y, rsigma)
+    _check(fn, lib().te_add_layernorm_mxfp8(
+        px, dt, r, c, pres, pg, _need(fn, dev, "beta", beta, _f32, (c,)), float(eps),
+        _need(fn, dev, "q_row", q_row, _u8, x.shape), _need_n(fn, dev, "s_row", s_row, _u8, _mx_bytes(r, c)), py, pro,
+        _need(fn, dev, "mu", mu, _f32, (r,), True), prs, _stream(stream, dev)))
+
+
+def te_layernorm_bwd_workspace_bytes(rows: int, cols: int) -> int:
+    return int(lib().te_layernorm_bwd_workspace_bytes(rows, cols))
+
+
+def te_layernorm_bwd(dy, s, gamma, mu, rsigma, dx, dgamma, dbeta, workspace, dres=None, stream=None):
+    """Gradients of te_add_layernorm_* (and te_layernorm_fp8): dx (of x and of the residual), dgamma and dbeta."""
+    fn = "te_layernorm_bwd"
+    dev = _device()
+    if s.dim() != 2:
+        raise ValueError(f"{fn}: s has shape {tuple(s.shape)}, expected [rows, cols]")
+    shape, dt = s.shape, s.dtype
+    ps = _need(fn, dev, "s", s, (_bf16, _f32), shape)
+    pw = _need_n(fn, dev, "workspace", workspace, _f32, 0)
+    _check(fn, lib().te_layernorm_bwd(
+        _need(fn, dev, "dy", dy, _bf16, shape), ps, _in_dtype(s), shape[0], shape[1],
+        _need(fn, dev, "gamma", gamma, _f32, shape[1:]), _need(fn, dev, "mu", mu, _f32, shape[:1]),
+        _need(fn, dev, "rsigma", rsigma, _f32, shape[:1]), _need(fn, dev, "dres", dres, dt, shape, True),
+        _need(fn, dev, "dx", dx, dt, shape), _need(fn, dev, "dgamma", dgamma, _f32, shape[1:]),
+        _need(fn, dev, "dbeta", dbeta, _f32, shape[1:]), pw, workspace.numel() * 4, _stream(stream, dev)))
+
+
 def te_quantize_mxfp8(x, q_row=None, s_row=None, q_col=None, s_col=None, stream=None):
     r, c = _rc(x)
     _check("te_quantize_mxfp8", lib().te_quantize_mxfp8(_ptr(x), _in_dtype(x), r, c, _ptr(q_row), _ptr(s_row),
@@ -494,6 +561,148 @@ def te_gated_bwd_bf16(x, w, w2, dy, gu, act: int, dgu, dx=None, dw=None, accumul
         _need(fn, dev, "dgu", dgu, _bf16, (T, 2 * F)), _need(fn, dev, "dx", dx, _bf16, (T, K), True),
         _need(fn, dev, "dw", dw, (_bf16, _f32), (2 * F, K), True), BF16 if dw is None else _out_dtype(dw),
         int(accumulate), T, K, F, N, _stream(stream, dev)))
+
+
+# ---- linear with bias, activation and residual: y = act(x w^T + bias) + residual ----------------------
+
+def _act_shape(fn, x, w, packed: int = 1):
+    """(T, K, N) of x [T, K / packed] and w [N, K / packed]."""
+    if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1]:
+        raise ValueError(f"{fn}: x {tuple(x.shape)} and w {tuple(w.shape)} are not [T, K] and [N, K]")
+    return x.shape[0], x.shape[1] * packed, w.shape[0]
+
+
+def _act_outputs(fn, dev, T, N, y, z, bias, residual):
+    """Pointers of bias, residual, z and y, and y's type."""
+    dt = _bf16 if y is None else y.dtype
+    if dt is not _bf16 and dt is not _f32:
+        raise TypeError(f"{fn}: y is {dt}, expected {(_bf16, _f32)}")
+    return (_need(fn, dev, "bias", bias, _f32, (N,), True), _need(fn, dev, "residual", residual, dt, (T, N), True),
+            _need(fn, dev, "z", z, _bf16, (T, N), True), _need(fn, dev, "y", y, dt, (T, N), True),
+            F32 if dt is _f32 else BF16)
+
+
+def te_act_gemm_bf16(x, w, act: int, y=None, z=None, bias=None, residual=None, stream=None):
+    """y = act(x w^T + bias) + residual in bf16 or fp32 and / or z = x w^T + bias in bf16."""
+    fn = "te_act_gemm_bf16"
+    dev = _device()
+    T, K, N = _act_shape(fn, x, w)
+    pb, pr, pz, py, dt = _act_outputs(fn, dev, T, N, y, z, bias, residual)
+    _check(fn, lib().te_act_gemm_bf16(_need(fn, dev, "x", x, _bf16, (T, K)), _need(fn, dev, "w", w, _bf16, (N, K)), pb, act,
+                                      pr, pz, py, dt, T, K, N, _stream(stream, dev)))
+
+
+def te_act_gemm_fp8(x, fx: int, w, fw: int, x_scale_inv, w_scale_inv, act: int, y=None, z=None, bias=None, residual=None,
+                    q=None, q_fmt: int = E4M3, q_scale=None, q_amax=None, q_scale_inv=None, stream=None):
+    """te_act_gemm_bf16 on per-tensor scaled FP8 operands; q is act(z) in FP8 for the linear after it."""
+    fn = "te_act_gemm_fp8"
+    dev = _device()
+    T, K, N = _act_shape(fn, x, w)
+    pb, pr, pz, py, dt = _act_outputs(fn, dev, T, N, y, z, bias, residual)
+    _check(fn, lib().te_act_gemm_fp8(
+        _need(fn, dev, "x", x, _u8, (T, K)), fx, _need(fn, dev, "w", w, _u8, (N, K)), fw,
+        _need_n(fn, dev, "x_scale_inv", x_scale_inv, _f32, 1), _need_n(fn, dev, "w_scale_inv", w_scale_inv, _f32, 1), pb, act,
+        pr, pz, py, dt, _need(fn, dev, "q", q, _u8, (T, N), True), q_fmt, _need_n(fn, dev, "q_scale", q_scale, _f32, 1, True),
+        _need_n(fn, dev, "q_amax", q_amax, _f32, 1, True), _need_n(fn, dev, "q_scale_inv", q_scale_inv, _f32, 1, True),
+        T, K, N, _stream(stream, dev)))
+
+
+def te_act_gemm_mxfp8(x, sx, w, sw, act: int, y=None, z=None, bias=None, residual=None, q=None, s_q=None, fx: int = E4M3,
+                      fw: int = E4M3, stream=None):
+    """te_act_gemm_bf16 on MXFP8 operands; q, s_q are act(z) in MXFP8 for the linear after it."""
+    fn = "te_act_gemm_mxfp8"
+    dev = _device()
+    T, K, N = _act_shape(fn, x, w)
+    pb, pr, pz, py, dt = _act_outputs(fn, dev, T, N, y, z, bias, residual)
+    _check(fn, lib().te_act_gemm_mxfp8(
+        _need(fn, dev, "x", x, _u8, (T, K)), fx, _need_n(fn, dev, "sx", sx, _u8, _mx_bytes(T, K)),
+        _need(fn, dev, "w", w, _u8, (N, K)), fw, _need_n(fn, dev, "sw", sw, _u8, _mx_bytes(N, K)), pb, act, pr, pz, py, dt,
+        _need(fn, dev, "q", q, _u8, (T, N), True), _need_n(fn, dev, "s_q", s_q, _u8, _mx_bytes(T, N), True), T, K, N,
+        _stream(stream, dev)))
+
+
+def te_act_gemm_nvfp4(x, sx, gx, w, sw, gw, act: int, y=None, z=None, bias=None, residual=None, stream=None):
+    """te_act_gemm_bf16 on NVFP4 operands (packed codes, block scales, tensor scales)."""
+    fn = "te_act_gemm_nvfp4"
+    dev = _device()
+    T, K, N = _act_shape(fn, x, w, 2)
+    pb, pr, pz, py, dt = _act_outputs(fn, dev, T, N, y, z, bias, residual)
+    _check(fn, lib().te_act_gemm_nvfp4(
+        _need(fn, dev, "x", x, _u8, (T, K // 2)), _need_n(fn, dev, "sx", sx, _u8, _nv_bytes(T, K)),
+        _need_n(fn, dev, "gx", gx, _f32, 1), _need(fn, dev, "w", w, _u8, (N, K // 2)),
+        _need_n(fn, dev, "sw", sw, _u8, _nv_bytes(N, K)), _need_n(fn, dev, "gw", gw, _f32, 1), pb, act, pr, pz, py, dt, T, K, N,
+        _stream(stream, dev)))
+
+
+def te_act_dbias_workspace_bytes(T: int, F: int) -> int:
+    return int(lib().te_act_dbias_workspace_bytes(T, F))
+
+
+def _act_dgrad(fn, dev, dy, w2, z, act, dz, dbias, workspace, packed: int = 1):
+    """(T, F, N) of dy [T, N / packed] and W2's col copy [F, N / packed], and the arguments from z to the workspace."""
+    if dy.dim() != 2 or w2.dim() != 2 or dy.shape[1] != w2.shape[1]:
+        raise ValueError(f"{fn}: dy {tuple(dy.shape)} and w2 {tuple(w2.shape)} are not [T, N] and [F, N]")
+    T, F = dy.shape[0], w2.shape[0]
+    return (T, F, dy.shape[1] * packed), _act_dz(fn, dev, T, F, z, act, dz, dbias, workspace)
+
+
+def _act_dz(fn, dev, T, F, z, act, dz, dbias, workspace):
+    return (_need(fn, dev, "z", z, _bf16, (T, F), act == ACT_NONE), act, _need(fn, dev, "dz", dz, _bf16, (T, F)),
+            _need(fn, dev, "dbias", dbias, _f32, (F,), True), _need_n(fn, dev, "workspace", workspace, _f32, 0, True),
+            0 if workspace is None else workspace.numel() * 4)
+
+
+def te_act_dgrad_fp8(dy, fd: int, w2, fw: int, dy_scale_inv, w2_scale_inv, z, act: int, dz, dbias=None, workspace=None,
+                     stream=None):
+    """dz and dbias from dy's row copy [T, N] and W2's col copy [F, N] in FP8 and the forward pass's z."""
+    fn = "te_act_dgrad_fp8"
+    dev = _device()
+    (T, F, N), own = _act_dgrad(fn, dev, dy, w2, z, act, dz, dbias, workspace)
+    _check(fn, lib().te_act_dgrad_fp8(
+        _need(fn, dev, "dy", dy, _u8, (T, N)), fd, _need(fn, dev, "w2", w2, _u8, (F, N)), fw,
+        _need_n(fn, dev, "dy_scale_inv", dy_scale_inv, _f32, 1), _need_n(fn, dev, "w2_scale_inv", w2_scale_inv, _f32, 1),
+        *own, T, F, N, _stream(stream, dev)))
+
+
+def te_act_dgrad_mxfp8(dy, sd, w2, sw, z, act: int, dz, dbias=None, workspace=None, fd: int = E4M3, fw: int = E4M3,
+                       stream=None):
+    """te_act_dgrad_fp8 on MXFP8 copies."""
+    fn = "te_act_dgrad_mxfp8"
+    dev = _device()
+    (T, F, N), own = _act_dgrad(fn, dev, dy, w2, z, act, dz, dbias, workspace)
+    _check(fn, lib().te_act_dgrad_mxfp8(
+        _need(fn, dev, "dy", dy, _u8, (T, N)), fd, _need_n(fn, dev, "sd", sd, _u8, _mx_bytes(T, N)),
+        _need(fn, dev, "w2", w2, _u8, (F, N)), fw, _need_n(fn, dev, "sw", sw, _u8, _mx_bytes(F, N)), *own, T, F, N,
+        _stream(stream, dev)))
+
+
+def te_act_dgrad_nvfp4(dy, sd, gd, w2, sw, gw, z, act: int, dz, dbias=None, workspace=None, stream=None):
+    """te_act_dgrad_fp8 on NVFP4 copies."""
+    fn = "te_act_dgrad_nvfp4"
+    dev = _device()
+    (T, F, N), own = _act_dgrad(fn, dev, dy, w2, z, act, dz, dbias, workspace, 2)
+    _check(fn, lib().te_act_dgrad_nvfp4(
+        _need(fn, dev, "dy", dy, _u8, (T, N // 2)), _need_n(fn, dev, "sd", sd, _u8, _nv_bytes(T, N)),
+        _need_n(fn, dev, "gd", gd, _f32, 1), _need(fn, dev, "w2", w2, _u8, (F, N // 2)),
+        _need_n(fn, dev, "sw", sw, _u8, _nv_bytes(F, N)), _need_n(fn, dev, "gw", gw, _f32, 1), *own, T, F, N,
+        _stream(stream, dev)))
+
+
+def te_act_bwd_bf16(x, w, w2, dy, z, act: int, dz, dbias=None, workspace=None, dx=None, dw=None, accumulate: int = 0,
+                    stream=None):
+    """The BF16 backward pass: dz and dbias from dy [T, N] and w2 [N, F], then dx = dz w and dw (+)= dz^T x."""
+    fn = "te_act_bwd_bf16"
+    dev = _device()
+    T, K, F = _act_shape(fn, x, w)
+    if dy.dim() != 2:
+        raise ValueError(f"{fn}: dy has shape {tuple(dy.shape)}, expected [T, N]")
+    N = dy.shape[1]
+    own = _act_dz(fn, dev, T, F, z, act, dz, dbias, workspace)
+    _check(fn, lib().te_act_bwd_bf16(
+        _need(fn, dev, "x", x, _bf16, (T, K)), _need(fn, dev, "w", w, _bf16, (F, K)), _need(fn, dev, "w2", w2, _bf16, (N, F)),
+        _need(fn, dev, "dy", dy, _bf16, (T, N)), *own, _need(fn, dev, "dx", dx, _bf16, (T, K), True),
+        _need(fn, dev, "dw", dw, (_bf16, _f32), (F, K), True), BF16 if dw is None else _out_dtype(dw), int(accumulate), T, K, F,
+        N, _stream(stream, dev)))
 
 
 def te_scale_bytes(scale_fmt: int, rows: int, cols: int) -> int:

@@ -16,7 +16,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libte_gb300.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--cudart", "shared"]
-UNITS = {"host.cu": [], "quant.cu": ["-fmad=false"], "norm.cu": [], "gemm.cu": [], "gated.cu": []}
+UNITS = {"host.cu": [], "quant.cu": ["-fmad=false"], "norm.cu": [], "layernorm.cu": [], "gemm.cu": [], "gated.cu": [],
+         "act.cu": []}
 
 
 def _nvcc() -> str:

@@ -67,7 +67,11 @@ enum Kind { kBF16 = 0, kFP8 = 1, kMXFP8 = 2, kNVFP4 = 3 };
 //            columns 0-127 and u columns 128-255, and each epilogue thread holds both of its elements.
 //   kDgrad   acc is dh = dY W2; with g and u (loaded by TMA while the tile's MMAs run) the epilogue
 //            writes dg = dh u act'(g) and du = dh act(g).
-enum Epi { kPlain = 0, kGated = 1, kDgrad = 2 };
+//   kAct     y = act(alpha * acc + bias) (+ residual, loaded by TMA while the tile's MMAs run), z before the
+//            activation, act(z) in 8 bits.
+//   kActGrad acc is dh = dY W2; with z (loaded like g and u) the epilogue writes dz = dh act'(z) and the sums of
+//            dz over each 32 rows.
+enum Epi { kPlain = 0, kGated = 1, kDgrad = 2, kAct = 3, kActGrad = 4 };
 
 constexpr int BM = 128;
 constexpr int BN = 256;
@@ -120,8 +124,9 @@ struct Cfg {
   static constexpr int kSmemSfb = kSmemSfa + kStages * kSfaBytes;
   static constexpr int kSmemStage = kSmemSfb + kStages * kSfbBytes;      // epilogue staging
   static constexpr int kSmemBar = kSmemStage + kEpiWarps * kStgBytes;
-  static constexpr int kEpiBars = EPI == kDgrad ? kEpiWarps : 0;          // a barrier per warp for its g and u
-  static constexpr int kBarBytes = EPI == kDgrad ? 384 : 256;
+  // barriers for the boxes that an epilogue warp reads: one for its g and u, two for residual's or z's
+  static constexpr int kEpiBars = EPI == kDgrad ? kEpiWarps : (EPI == kAct || EPI == kActGrad ? 2 * kEpiWarps : 0);
+  static constexpr int kBarBytes = kEpiBars > 0 ? 384 : 256;
   static constexpr int kSmemTotal = kSmemBar + kBarBytes + 1024;  // barriers + alignment slack
   static_assert((4 * kStages + 5 + kEpiBars) * 8 + 8 <= kBarBytes, "barrier area");
   static_assert(EPI == kPlain || kPair, "the gated epilogues take CTA pairs");
@@ -173,17 +178,44 @@ struct GatedArgs {
   int64_t s_kpad;
   int s_rows;
 };
+// Operands of the activation's epilogues.
+struct ActArgs {
+  CUtensorMap y, z, res, q;   // kAct: y, z, residual and the 8-bit act(z); kActGrad: dz (y) and z
+  CUtensorMap q32;            // kAct: the 8-bit act(z) in boxes of 32 columns, for slices of one chunk
+  int N;                      // columns of y
+  int act;
+  int has_y, has_z, has_res, has_q;
+  int y_f32;                  // y and residual in fp32
+  const float* bias;
+  const float* q_scale;       // FP8: the scale, the amax (float bits), 1 / scale
+  int q_e5m2;
+  unsigned int* amax;
+  float* scale_inv;
+  uint8_t* s_q;               // MXFP8: the scales, scale columns and padded rows
+  int64_t s_kpad;
+  int s_rows;
+  float* partial;             // kActGrad: [rows / 32, N] sums of dz (nullable)
+};
 struct NoEpiArgs {};
 template <int EPI>
 struct EpiParam {
-  using type = GatedArgs;
+  using type = ActArgs;
 };
 template <>
 struct EpiParam<kPlain> {
   using type = NoEpiArgs;
 };
+template <>
+struct EpiParam<kGated> {
+  using type = GatedArgs;
+};
+template <>
+struct EpiParam<kDgrad> {
+  using type = GatedArgs;
+};
 
 #include "gated_epilogue.inc"
+#include "act_epilogue.inc"
 
 // Tile `tile` of the persistent walk -> (M tile, N tile).  Grouped raster: 16 pair M-tiles at
 // a time, M fastest.  raster = 1 (8-bit kinds on long contractions): the smaller operand's tiles
@@ -235,7 +267,7 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, EPI>::kThreads, 1)
   uint64_t* drain = acc_empty + 2;
   uint64_t* sf_ready = drain + 1;  // [kStages]: the stage's scale factors are in TMEM
   uint64_t* sf_full = sf_ready + kStages;   // [kStages]: the stage's scale atoms have landed (block-scaled kinds)
-  uint64_t* epi_bar = sf_full + kStages;    // kDgrad: [kEpiWarps], the warp's g and u boxes have landed
+  uint64_t* epi_bar = sf_full + kStages;    // [kEpiBars]: boxes that the epilogue reads have landed
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(epi_bar + C::kEpiBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -551,6 +583,8 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, EPI>::kThreads, 1)
     typename EpiState<EPI>::type est;
     if constexpr (EPI == kGated) est.init(ep, stg, lane);
     if constexpr (EPI == kDgrad) est.init(stg, epi_bar + (warp - 2), lane);
+    if constexpr (EPI == kAct) est.init(ep, stg, epi_bar + 2 * (warp - 2), lane);
+    if constexpr (EPI == kActGrad) est.init(stg, epi_bar + 2 * (warp - 2), lane);
     int it = 0;
     for (int tile = unit; tile < num_tiles; tile += units, ++it) {
       int mt, nt;
@@ -573,7 +607,7 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, EPI>::kThreads, 1)
         chunks /= by_half ? 2 : args.split;
         n0 += 32 * chunks * sub;
       }
-      if constexpr (EPI == kDgrad)
+      if constexpr (EPI == kDgrad || EPI == kAct || EPI == kActGrad)
         if (mine) est.begin(ep, (mt * CG + static_cast<int>(rank)) * BM + quarter * 32, n0, chunks, args.M);
       const bool acc_ok = dev::mbar_wait<kPair>(&acc_full[as], aphase, abort_flag, args.err);
       if (!SPLIT && !acc_ok) break;
@@ -667,6 +701,14 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, EPI>::kThreads, 1)
         if (!est.tile(ep, acc, alpha, abort_flag, args.err)) break;
         continue;
       }
+      if constexpr (EPI == kAct) {
+        if (!est.template tile<KIND == kMXFP8>(ep, acc, alpha, chunks, args.M, abort_flag, args.err)) break;
+        continue;
+      }
+      if constexpr (EPI == kActGrad) {
+        if (!est.tile(ep, acc, alpha, args.M, abort_flag, args.err)) break;
+        continue;
+      }
 
       // Stage 32 rows x 64 bytes at a time in this warp's shared-memory box and write it
       // with a TMA store (the store clips rows >= M and columns >= N).
@@ -729,7 +771,8 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, EPI>::kThreads, 1)
       }
     }
     if constexpr (EPI == kGated) est.finish(ep);
-    if constexpr (EPI == kDgrad) est.finish(args.err);
+    if constexpr (EPI == kDgrad || EPI == kActGrad) est.finish(args.err);
+    if constexpr (EPI == kAct) est.finish(ep, args.err);
     if (lane == 0) dev::bulk_wait0();
   }
 

@@ -24,3 +24,23 @@ def layernorm(x, gamma, beta, eps: float):
     y = (x - mu[:, None]) * rsigma[:, None] * np.asarray(gamma, np.float64)[None, :] + \
         np.asarray(beta, np.float64)[None, :]
     return y, mu, rsigma
+
+
+def add_layernorm(x, gamma, beta, eps: float, residual=None):
+    """(s [R, C], y [R, C], mu [R], rsigma [R]) in fp64, s = x + residual normalised."""
+    s = np.asarray(x, np.float64)
+    if residual is not None:
+        s = s + np.asarray(residual, np.float64)
+    return (s, *layernorm(s, gamma, beta, eps))
+
+
+def layernorm_bwd(dy, s, gamma, mu, rsigma, dres=None):
+    """(ds [R, C], dgamma [C], dbeta [C]) in fp64, for L(y) with dy = dL/dy and a gradient dres that reaches s
+    beside it:  ds = rsigma (p - mean(p) - xhat mean(p xhat)) + dres,  p = dy gamma, xhat = (s - mu) rsigma."""
+    dy, s = np.asarray(dy, np.float64), np.asarray(s, np.float64)
+    rs = np.asarray(rsigma, np.float64)[:, None]
+    xhat, p = (s - np.asarray(mu, np.float64)[:, None]) * rs, dy * np.asarray(gamma, np.float64)
+    ds = rs * (p - p.mean(axis=1, keepdims=True) - xhat * (p * xhat).mean(axis=1, keepdims=True))
+    if dres is not None:
+        ds = ds + np.asarray(dres, np.float64)
+    return ds, (dy * xhat).sum(axis=0), dy.sum(axis=0)
