@@ -1,6 +1,7 @@
 // Entry points of the linear with bias, activation and residual in its epilogue, y = act(x W^T + b) + residual,
-// and of its backward pass.  The kernels are gemm_kernel with the epilogues of act_epilogue.inc.
-#include "gemm.cuh"
+// and of its backward pass.  The kernels are gemm_kernel with the epilogues of act_epilogue.inc, and those of
+// act_decode.cuh and act_stream.cuh for few tokens.
+#include "act_stream.cuh"
 
 namespace te {
 namespace {
@@ -71,6 +72,24 @@ te_status act_args(ActArgs* ep, const Outputs& o, int64_t T, int64_t N) {
     s = make_tmap_2d_plain(&ep->q32, o.q, static_cast<uint64_t>(N), static_cast<uint64_t>(T), 32u, 32u);
   }
   return s;
+}
+
+// The same for the kernels of few tokens.
+FewArgs few_args(const void* x, const void* w, const Outputs& o, int64_t T, int64_t K, int64_t N) {
+  FewArgs a = {};
+  a.x = static_cast<const uint8_t*>(x);
+  a.w = static_cast<const uint8_t*>(w);
+  a.T = static_cast<int>(T);
+  a.K = static_cast<int>(K);
+  a.N = static_cast<int>(N);
+  a.act = o.act;
+  a.bias = o.bias;
+  a.res = o.residual;
+  a.z = static_cast<__nv_bfloat16*>(o.z);
+  a.y = o.y;
+  a.y_f32 = o.y != nullptr && o.y_dtype == TE_F32;
+  a.q = o.q;
+  return a;
 }
 
 // dbias[c] = the sum of the partial rows (one for each 32 tokens) in a fixed order: 32 columns x 32 row lanes a
@@ -172,6 +191,13 @@ te_status te_act_gemm_bf16(const void* x, const void* w, const float* bias, int 
   const Outputs o = {bias, act, residual, z, y, y_dtype, nullptr};
   if ((s = check_outputs(o)) != TE_OK) return s;
   if ((s = check_operands(x, w)) != TE_OK) return s;
+  if (T <= kAstMaxTokens) {
+    const FewArgs a = few_args(x, w, o, T, K, N);
+    if (act_decodes(T, K, N, 2)) return launch_act_decode<kDecBF16, kDecBF16>(a, static_cast<cudaStream_t>(stream));
+    bool taken;
+    s = launch_act_stream<kBF16>(a, 1u, 1u, static_cast<cudaStream_t>(stream), &taken);
+    if (taken || s != TE_OK) return s;
+  }
   ActArgs ep = {};
   if ((s = act_args(&ep, o, T, N)) != TE_OK) return s;
   return launch_gemm<kBF16, 2, kAct, true>(x, w, K * 2, nullptr, nullptr, 0, nullptr, nullptr, nullptr, nullptr, TE_BF16,
@@ -198,6 +224,23 @@ te_status te_act_gemm_fp8(const uint8_t* x, te_dtype fx, const uint8_t* w, te_dt
   if (q ? !q_scale : (q_amax || q_scale_inv)) return TE_ERR_NULL;   // the amax and 1 / scale go with q
   if (!x_scale_inv || !w_scale_inv) return TE_ERR_NULL;
   if ((s = check_operands(x, w)) != TE_OK) return s;
+  if (T <= kAstMaxTokens) {
+    FewArgs a = few_args(x, w, o, T, K, N);
+    a.alpha_a = x_scale_inv;
+    a.alpha_b = w_scale_inv;
+    a.q_scale = q_scale;
+    a.q_e5m2 = q_fmt == TE_E5M2;
+    a.amax = reinterpret_cast<unsigned int*>(q_amax);
+    a.scale_inv = q_scale_inv;
+    if (act_decodes(T, K, N, 1)) {
+      if (fw == TE_E4M3)
+        return fx == TE_E4M3 ? launch_act_decode<kDecE4M3, kDecE4M3>(a, st) : launch_act_decode<kDecE4M3, kDecE5M2>(a, st);
+      return fx == TE_E4M3 ? launch_act_decode<kDecE5M2, kDecE4M3>(a, st) : launch_act_decode<kDecE5M2, kDecE5M2>(a, st);
+    }
+    bool taken;
+    s = launch_act_stream<kFP8>(a, fp8_code(fx), fp8_code(fw), st, &taken);
+    if (taken || s != TE_OK) return s;
+  }
   ActArgs ep = {};
   if ((s = act_args(&ep, o, T, N)) != TE_OK) return s;
   if (q) {
@@ -223,6 +266,17 @@ te_status te_act_gemm_mxfp8(const uint8_t* x, te_dtype fx, const uint8_t* sx, co
   if ((s = check_operands(x, w)) != TE_OK) return s;
   if ((s = check_operands(sx, sw)) != TE_OK) return s;
   if (!aligned16(s_q)) return TE_ERR_ALIGN;
+  if (T <= kAstMaxTokens) {
+    FewArgs a = few_args(x, w, o, T, K, N);
+    a.sx = sx;
+    a.sw = sw;
+    a.s_kpad = (K / 32 + 3) / 4 * 4;
+    a.s_q = s_q;
+    a.q_kpad = (N / 32 + 3) / 4 * 4;
+    bool taken;
+    s = launch_act_stream<kMXFP8>(a, fp8_code(fx), fp8_code(fw), static_cast<cudaStream_t>(stream), &taken);
+    if (taken || s != TE_OK) return s;
+  }
   ActArgs ep = {};
   if ((s = act_args(&ep, o, T, N)) != TE_OK) return s;
   ep.s_q = s_q;
@@ -243,6 +297,17 @@ te_status te_act_gemm_nvfp4(const uint8_t* x, const uint8_t* sx, const float* gx
   if (!gx || !gw) return TE_ERR_NULL;
   if ((s = check_operands(x, w)) != TE_OK) return s;
   if ((s = check_operands(sx, sw)) != TE_OK) return s;
+  if (T <= kAstMaxTokens) {
+    FewArgs a = few_args(x, w, o, T, K, N);
+    a.alpha_a = gx;
+    a.alpha_b = gw;
+    a.sx = sx;
+    a.sw = sw;
+    a.s_kpad = (K / 16 + 15) / 16 * 16;
+    bool taken;
+    s = launch_act_stream<kNVFP4>(a, 1u, 1u, static_cast<cudaStream_t>(stream), &taken);
+    if (taken || s != TE_OK) return s;
+  }
   ActArgs ep = {};
   if ((s = act_args(&ep, o, T, N)) != TE_OK) return s;
   return launch_gemm<kNVFP4, 2, kAct>(x, w, K / 2, sx, sw, (K / 16 + 15) / 16 * 4, gx, gw, nullptr, nullptr, TE_BF16, 0,

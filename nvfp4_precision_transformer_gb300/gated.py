@@ -28,7 +28,67 @@ FWD_SLOTS = ("y", "w", "h", "w2")
 BWD_SLOTS = ("dout", "dgu")
 
 
-class GatedMLP:
+class _Block:
+    """What the feed-forward blocks share: the quantized copies of their tensors by name, the DelayedScaling state and
+    its checkpoint, and the GEMMs on the copies."""
+
+    def _allocate(self, shapes: dict, fwd: tuple, bwd: tuple, history_len: int, dev) -> None:
+        """Copies of the tensors (name -> [rows, cols]) and the state of the recipe."""
+        u8 = dict(dtype=torch.uint8, device=dev)
+        # quantized copies: name -> (row copy, col copy), and for MXFP8 their scales
+        if self.recipe != "bf16":
+            self.row = {n: torch.empty(r, c, **u8) for n, (r, c) in shapes.items()}
+            self.col = {n: torch.empty(c, r, **u8) for n, (r, c) in shapes.items()}
+        if self.recipe == "mxfp8":
+            self.srow = {n: torch.empty(L.te_scale_bytes(L.E8M0, r, c), **u8) for n, (r, c) in shapes.items()}
+            self.scol = {n: torch.empty(L.te_scale_bytes(L.E8M0, c, r), **u8) for n, (r, c) in shapes.items()}
+        if self.recipe == "fp8_delayed":
+            self.fwd = DelayedState(len(fwd), history_len, dev)
+            self.bwd = DelayedState(len(bwd), history_len, dev)
+            self.slots = {n: self.fwd.slot(i) for i, n in enumerate(fwd)}
+            self.slots.update({n: self.bwd.slot(i) for i, n in enumerate(bwd)})
+            self.te_recipe = L.te_recipe(L.E4M3, L.E5M2, history_len, L.ALGO_MAX, 0, 1)
+        self.step_idx = 0
+
+    def _end_step(self) -> None:
+        """The scales of the next step."""
+        if self.recipe == "fp8_delayed":
+            for i, st in enumerate((self.fwd, self.bwd)):
+                L.te_scale_update(self.te_recipe, i, st.hist, st.amax, st.scale, st.scale_inv, self.step_idx)
+        self.step_idx += 1
+
+    def state_dict(self) -> dict:
+        """DelayedScaling state of the block (both directions) and its step counter, on the host."""
+        if self.recipe != "fp8_delayed":
+            return {"step": self.step_idx}
+        return {"fwd": self.fwd.state_dict(), "bwd": self.bwd.state_dict(), "step": self.step_idx}
+
+    def load_state_dict(self, sd: dict) -> None:
+        if self.recipe == "fp8_delayed":
+            self.fwd.load_state_dict(sd["fwd"])
+            self.bwd.load_state_dict(sd["bwd"])
+        self.step_idx = int(sd["step"])
+
+    # ---- quantization of one tensor under the recipe --------------------------------------------
+    def _quantize(self, name: str, t: torch.Tensor, fmt: int, row: bool = True) -> None:
+        """Both copies of ``t``; only the col copy where a kernel has written the row copy already."""
+        if self.recipe == "mxfp8":
+            L.te_quantize_mxfp8(t, self.row[name] if row else None, self.srow[name] if row else None, self.col[name],
+                                self.scol[name])
+        else:
+            scale, _, amax = self.slots[name]
+            L.te_quantize_fp8(t, fmt, scale, 0, self.row[name] if row else None, self.col[name], amax if row else None)
+
+    def _gemm(self, a: str, a_col: bool, fa: int, b: str, b_col: bool, fb: int, out: torch.Tensor) -> None:
+        """out = A B^T from the named copies."""
+        A, B = (self.col if a_col else self.row)[a], (self.col if b_col else self.row)[b]
+        if self.recipe == "mxfp8":
+            L.te_gemm_mxfp8(A, (self.scol if a_col else self.srow)[a], B, (self.scol if b_col else self.srow)[b], out)
+        else:
+            L.te_gemm_fp8(A, fa, B, fb, self.slots[a][1], self.slots[b][1], out)
+
+
+class GatedMLP(_Block):
     """Device buffers of one gated feed-forward block for ``tokens`` tokens, its forward and backward pass.
 
     ``forward(x, residual)`` returns (out, r): the block's output and the next residual, whose sum is
@@ -51,40 +111,15 @@ class GatedMLP:
         self.T, self.K, self.F, self.recipe, self.act, self.eps = tokens, K, F, recipe, act, eps
         self._check_weights("GatedMLP", L._device())
         dev, T = w.device, tokens
-        bf, u8, f32 = (dict(dtype=t, device=dev) for t in (torch.bfloat16, torch.uint8, torch.float32))
+        bf, f32 = (dict(dtype=t, device=dev) for t in (torch.bfloat16, torch.float32))
         self.r, self.y, self.h = torch.empty(T, K, **bf), torch.empty(T, K, **bf), torch.empty(T, F, **bf)
         self.gu, self.dgu = torch.empty(T, 2 * F, **bf), torch.empty(T, 2 * F, **bf)
         self.out, self.dy, self.dx = (torch.empty(T, K, **bf) for _ in range(3))
         self.dw, self.dw2 = torch.empty(2 * F, K, **bf), torch.empty(K, F, **bf)
         self.rsigma, self.dgamma = torch.empty(T, **f32), torch.empty(K, **f32)
         self.workspace = torch.empty(L.te_rmsnorm_bwd_workspace_bytes(T, K) // 4, **f32)
-        # quantized copies: name -> (row copy, col copy), and for MXFP8 their scales
-        if recipe != "bf16":
-            shapes = {"y": (T, K), "w": (2 * F, K), "h": (T, F), "w2": (K, F), "dout": (T, K), "dgu": (T, 2 * F)}
-            self.row = {n: torch.empty(r, c, **u8) for n, (r, c) in shapes.items()}
-            self.col = {n: torch.empty(c, r, **u8) for n, (r, c) in shapes.items()}
-        if recipe == "mxfp8":
-            self.srow = {n: torch.empty(L.te_scale_bytes(L.E8M0, r, c), **u8) for n, (r, c) in shapes.items()}
-            self.scol = {n: torch.empty(L.te_scale_bytes(L.E8M0, c, r), **u8) for n, (r, c) in shapes.items()}
-        if recipe == "fp8_delayed":
-            self.fwd = DelayedState(len(FWD_SLOTS), history_len, dev)
-            self.bwd = DelayedState(len(BWD_SLOTS), history_len, dev)
-            self.slots = {n: self.fwd.slot(i) for i, n in enumerate(FWD_SLOTS)}
-            self.slots.update({n: self.bwd.slot(i) for i, n in enumerate(BWD_SLOTS)})
-            self.te_recipe = L.te_recipe(L.E4M3, L.E5M2, history_len, L.ALGO_MAX, 0, 1)
-        self.step_idx = 0
-
-    def state_dict(self) -> dict:
-        """DelayedScaling state of the block (both directions) and its step counter, on the host."""
-        if self.recipe != "fp8_delayed":
-            return {"step": self.step_idx}
-        return {"fwd": self.fwd.state_dict(), "bwd": self.bwd.state_dict(), "step": self.step_idx}
-
-    def load_state_dict(self, sd: dict) -> None:
-        if self.recipe == "fp8_delayed":
-            self.fwd.load_state_dict(sd["fwd"])
-            self.bwd.load_state_dict(sd["bwd"])
-        self.step_idx = int(sd["step"])
+        self._allocate({"y": (T, K), "w": (2 * F, K), "h": (T, F), "w2": (K, F), "dout": (T, K), "dgu": (T, 2 * F)},
+                       FWD_SLOTS, BWD_SLOTS, history_len, dev)
 
     # ---- checks: before the first launch of a pass, whose calls take addresses and sizes as they are ----
     def _operand(self, fn: str, dev: int, name: str, t: torch.Tensor, shape: tuple) -> None:
@@ -95,24 +130,6 @@ class GatedMLP:
         L._need(fn, dev, "gamma", self.gamma, torch.float32, (self.K,))
         self._operand(fn, dev, "w", self.w, (2 * self.F, self.K))
         self._operand(fn, dev, "w2", self.w2, (self.K, self.F))
-
-    # ---- quantization of one tensor under the recipe --------------------------------------------
-    def _quantize(self, name: str, t: torch.Tensor, fmt: int, row: bool = True) -> None:
-        """Both copies of ``t``; only the col copy where a kernel has written the row copy already."""
-        if self.recipe == "mxfp8":
-            L.te_quantize_mxfp8(t, self.row[name] if row else None, self.srow[name] if row else None, self.col[name],
-                                self.scol[name])
-        else:
-            scale, _, amax = self.slots[name]
-            L.te_quantize_fp8(t, fmt, scale, 0, self.row[name] if row else None, self.col[name], amax if row else None)
-
-    def _gemm(self, a: str, a_col: bool, fa: int, b: str, b_col: bool, fb: int, out: torch.Tensor) -> None:
-        """out = A B^T from the named copies."""
-        A, B = (self.col if a_col else self.row)[a], (self.col if b_col else self.row)[b]
-        if self.recipe == "mxfp8":
-            L.te_gemm_mxfp8(A, (self.scol if a_col else self.srow)[a], B, (self.scol if b_col else self.srow)[b], out)
-        else:
-            L.te_gemm_fp8(A, fa, B, fb, self.slots[a][1], self.slots[b][1], out)
 
     # ---- passes ----------------------------------------------------------------------------------
     def forward(self, x: torch.Tensor, residual: torch.Tensor):
@@ -167,7 +184,4 @@ class GatedMLP:
             self._gemm("dgu", False, E5, "w", True, E4, self.dy)
             self._gemm("dgu", True, E5, "y", True, E4, self.dw)
         L.te_rmsnorm_bwd(self.dy, self.r, self.gamma, self.rsigma, self.dx, self.dgamma, self.workspace, dres=dr)
-        if self.recipe == "fp8_delayed":
-            for i, st in enumerate((self.fwd, self.bwd)):
-                L.te_scale_update(self.te_recipe, i, st.hist, st.amax, st.scale, st.scale_inv, self.step_idx)
-        self.step_idx += 1
+        self._end_step()
