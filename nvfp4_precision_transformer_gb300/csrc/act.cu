@@ -163,11 +163,10 @@ te_status check_grads(const Grads& g, int64_t T, int64_t F) {
 te_status grads_args(ActArgs* ep, const Grads& g, int64_t T, int64_t F) {
   ep->N = static_cast<int>(F);
   ep->act = g.act;
-  ep->has_z = g.act != TE_ACT_NONE;
   ep->partial = g.dbias ? g.workspace : nullptr;
-  te_status s = boxes(&ep->y, g.dz, T, F, 2);
-  if (s == TE_OK && ep->has_z) s = boxes(&ep->z, g.z, T, F, 2);
-  return s;
+  ep->has_z = g.act != TE_ACT_NONE;
+  const te_status s = boxes(&ep->y, g.dz, T, F, 2);
+  return s == TE_OK && g.act != TE_ACT_NONE ? boxes(&ep->z, g.z, T, F, 2) : s;
 }
 
 // No tokens: dbias = 0.
@@ -201,7 +200,7 @@ te_status te_act_gemm_bf16(const void* x, const void* w, const float* bias, int 
   ActArgs ep = {};
   if ((s = act_args(&ep, o, T, N)) != TE_OK) return s;
   return launch_gemm<kBF16, 2, kAct, true>(x, w, K * 2, nullptr, nullptr, 0, nullptr, nullptr, nullptr, nullptr, TE_BF16,
-                                           0, T, N, K, 1u, 1u, static_cast<cudaStream_t>(stream), 0, 0, ep, kPdlChain);
+                                           0, T, N, K, 1u, 1u, static_cast<cudaStream_t>(stream), 0, 0, ep, kPdlChain, 4, ep.y_f32 ? kSegment<kBF16> : 0);
 }
 
 te_status te_act_gemm_fp8(const uint8_t* x, te_dtype fx, const uint8_t* w, te_dtype fw, const float* x_scale_inv,
@@ -251,7 +250,7 @@ te_status te_act_gemm_fp8(const uint8_t* x, te_dtype fx, const uint8_t* w, te_dt
   }
   if (q_amax && (s = zero_amax(q_amax, st)) != TE_OK) return s;
   return launch_gemm<kFP8, 2, kAct, true>(x, w, K, nullptr, nullptr, 0, x_scale_inv, w_scale_inv, nullptr, nullptr,
-                                          TE_BF16, 0, T, N, K, fp8_code(fx), fp8_code(fw), st, 0, 0, ep, kPdlChain);
+                                          TE_BF16, 0, T, N, K, fp8_code(fx), fp8_code(fw), st, 0, 0, ep, kPdlChain, 4, ep.y_f32 ? kSegment<kFP8> : 0);
 }
 
 te_status te_act_gemm_mxfp8(const uint8_t* x, te_dtype fx, const uint8_t* sx, const uint8_t* w, te_dtype fw,
@@ -284,7 +283,7 @@ te_status te_act_gemm_mxfp8(const uint8_t* x, te_dtype fx, const uint8_t* sx, co
   ep.s_rows = static_cast<int>((T + 127) / 128 * 128);
   return launch_gemm<kMXFP8, 2, kAct>(x, w, K, sx, sw, (K / 32 + 3) / 4, nullptr, nullptr, nullptr, nullptr, TE_BF16, 0,
                                       T, N, K, fp8_code(fx), fp8_code(fw), static_cast<cudaStream_t>(stream), 0, 0, ep,
-                                      kPdlChain);
+                                      kPdlChain, 4, ep.y_f32 ? kSegment<kMXFP8> : 0);
 }
 
 te_status te_act_gemm_nvfp4(const uint8_t* x, const uint8_t* sx, const float* gx, const uint8_t* w, const uint8_t* sw,
@@ -331,7 +330,7 @@ te_status te_act_dgrad_fp8(const uint8_t* dy, te_dtype fd, const uint8_t* w2, te
   ActArgs ep = {};
   if ((s = grads_args(&ep, g, T, F)) != TE_OK) return s;
   s = launch_gemm<kFP8, 2, kActGrad, true>(dy, w2, N, nullptr, nullptr, 0, dy_scale_inv, w2_scale_inv, nullptr, nullptr,
-                                           TE_BF16, 0, T, F, N, fp8_code(fd), fp8_code(fw), st, 0, 0, ep, kPdlChain);
+                                           TE_BF16, 0, T, F, N, fp8_code(fd), fp8_code(fw), st, 0, 0, ep, kPdlChain, 4, kSegment<kFP8>);
   return s != TE_OK || !dbias ? s : reduce_dbias(workspace, T, F, dbias, 0, st);
 }
 
@@ -350,7 +349,7 @@ te_status te_act_dgrad_mxfp8(const uint8_t* dy, te_dtype fd, const uint8_t* sd, 
   ActArgs ep = {};
   if ((s = grads_args(&ep, g, T, F)) != TE_OK) return s;
   s = launch_gemm<kMXFP8, 2, kActGrad>(dy, w2, N, sd, sw, (N / 32 + 3) / 4, nullptr, nullptr, nullptr, nullptr, TE_BF16,
-                                       0, T, F, N, fp8_code(fd), fp8_code(fw), st, 0, 0, ep, kPdlChain);
+                                       0, T, F, N, fp8_code(fd), fp8_code(fw), st, 0, 0, ep, kPdlChain, 4, kSegment<kMXFP8>);
   return s != TE_OK || !dbias ? s : reduce_dbias(workspace, T, F, dbias, 0, st);
 }
 
@@ -399,7 +398,7 @@ te_status te_act_bwd_bf16(const void* x, const void* w, const void* w2, const vo
   // dh = dY W2 (W2 [N, F] read MN-major), dz in its epilogue.  The kernels after it read dz and the partial sums
   // and nothing of one another, so dbias and dW run beside dX wherever that leaves SMs idle.
   s = launch_gemm<kBF16, 2, kActGrad, true>(dy, w2, N * 2, nullptr, nullptr, 0, nullptr, nullptr, nullptr, nullptr,
-                                            TE_BF16, 0, T, F, N, 1u, 1u, st, 0, 1, ep, kPdlChain);
+                                            TE_BF16, 0, T, F, N, 1u, 1u, st, 0, 1, ep, kPdlChain, 4, kSegment<kBF16>);
   // dX = dZ W (W [F, K] MN-major);  dW = dZ^T X (both MN-major), on dz as stored, rounded to bf16: the tensor cores
   // take no wider operand.  dX's tiles are shared between CTA pairs only as far as dW's fit beside them, where they
   // fit at all.

@@ -56,12 +56,15 @@ __device__ __forceinline__ uint8_t few_code(const FewArgs& a, float v, float sca
   return static_cast<uint8_t>(a.q_e5m2 ? cvt_e5m2x2(v * scale, 0.0f) : cvt_e4m3x2(v * scale, 0.0f));
 }
 
-// x's T rows, then the partial sums of two units: [turn][warp][tile][lane].
+constexpr int kActDecTokens = 8;
+constexpr int kActDecX = 32 * 1024;   // bytes of x
+
+// x's T rows, then the partial sums of two units: [turn][warp][lane].
 __host__ inline size_t act_decode_smem(int T, int K, int elem) {
-  return static_cast<size_t>(T) * decode_row_bytes(K, elem) + 2 * static_cast<size_t>(kDecWarps) * ((T + 7) / 8) * 512;
+  return static_cast<size_t>(T) * decode_row_bytes(K, elem) + 2 * kDecWarps * 512;
 }
 
-template <int W, int X, int NT>
+template <int W, int X>
 __global__ void __launch_bounds__(32 * kDecWarps, 1) act_decode_kernel(FewArgs a) {
   constexpr int EB = W == kDecBF16 ? 2 : 1;
   extern __shared__ __align__(128) uint8_t dec_smem[];
@@ -114,41 +117,37 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1) act_decode_kernel(FewArgs a
 
   const uint8_t* xrow = dec_smem + r * srow + t * 16;
   for (int unit = 0; unit < units; ++unit) {
-    float4 acc[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) acc[n] = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int step = 0; step < steps; ++step) {
       uint4 ca[kDecAhead], cb[kDecAhead];
 #pragma unroll
       for (int i = 0; i < kDecAhead; ++i) ca[i] = wa[i], cb[i] = wb[i];
       const bool last = step + 1 == steps;
       fetch(last ? unit + 1 : unit, last ? 0 : step + 1);
+      // (the tensor cores round their sums towards zero: only eight instructions' worth before they are added up here)
+      float4 part = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < kDecAhead; ++i) {
         const int block = (step * kDecAhead + i) * kDecWarps + warp;
         if (block >= blocks) break;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          uint4 b = make_uint4(0u, 0u, 0u, 0u);   // tokens past the last
-          if (n * 8 + r < a.T) b = *reinterpret_cast<const uint4*>(xrow + n * 8 * srow + block * 64);
-          mma_dec<W, X>(acc[n], ca[i].x, cb[i].x, ca[i].y, cb[i].y, b.x, b.y);
-          mma_dec<W, X>(acc[n], ca[i].z, cb[i].z, ca[i].w, cb[i].w, b.z, b.w);
-        }
+        uint4 b = make_uint4(0u, 0u, 0u, 0u);   // tokens past the last
+        if (r < a.T) b = *reinterpret_cast<const uint4*>(xrow + block * 64);
+        mma_dec<W, X>(part, ca[i].x, cb[i].x, ca[i].y, cb[i].y, b.x, b.y);
+        mma_dec<W, X>(part, ca[i].z, cb[i].z, ca[i].w, cb[i].w, b.z, b.w);
       }
+      acc.x += part.x, acc.y += part.y, acc.z += part.z, acc.w += part.w;
     }
     // (the units' sums take turns in two buffers, so that one barrier a unit is enough)
-    float4* mine = red + (unit & 1) * kDecWarps * NT * 32;
-#pragma unroll
-    for (int n = 0; n < NT; ++n) mine[(warp * NT + n) * 32 + lane] = acc[n];
+    float4* mine = red + (unit & 1) * kDecWarps * 32;
+    mine[warp * 32 + lane] = acc;
     __syncthreads();
-    // tile n of tokens: lane (r, t) has tokens 2 t and 2 t + 1 of rows r (warp 2 n) and r + 8 (warp 2 n + 1)
-    if (warp < 2 * NT) {
-      const int n = warp >> 1, hi = warp & 1;
-      const float2* p = reinterpret_cast<const float2*>(mine + n * 32 + lane) + hi;
+    // lane (r, t) has tokens 2 t and 2 t + 1 of rows r (warp 0) and r + 8 (warp 1)
+    if (warp < 2) {
+      const float2* p = reinterpret_cast<const float2*>(mine + lane) + warp;
       float2 s = p[0];
 #pragma unroll
-      for (int k = 1; k < kDecWarps; ++k) s = __fadd2_rn(s, p[k * NT * 64]);
-      const int u0 = unit_lo(unit), row = r + 8 * hi;
+      for (int k = 1; k < kDecWarps; ++k) s = __fadd2_rn(s, p[k * 64]);
+      const int u0 = unit_lo(unit), row = r + 8 * warp;
       if (row < unit_lo(unit + 1) - u0) {
         const int col = u0 + row;
         const float b = a.bias ? a.bias[col] : 0.0f;
@@ -156,7 +155,7 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1) act_decode_kernel(FewArgs a
         const float2 v2 = act_value(z2, a.act);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const int tok = n * 8 + 2 * t + j;
+          const int tok = 2 * t + j;
           if (tok < a.T) {
             const int64_t at = static_cast<int64_t>(tok) * a.N + col;
             const float v = j ? v2.y : v2.x;
@@ -170,19 +169,19 @@ __global__ void __launch_bounds__(32 * kDecWarps, 1) act_decode_kernel(FewArgs a
       }
     }
   }
-  if (a.amax && warp < 2 * NT) {
+  if (a.amax && warp < 2) {
     top = __reduce_max_sync(0xFFFFFFFFu, top);
     if (lane == 0) atomicMax(a.amax, top);
   }
   if (a.scale_inv && blockIdx.x == 0 && threadIdx.x == 0) *a.scale_inv = __fdiv_rn(1.0f, qs);
 }
 
-template <int W, int X, int NT>
+template <int W, int X>
 te_status launch_act_decode(const FewArgs& a, cudaStream_t st) {
   static PerDevice<SharedMemory> ready;
   te_status s = TE_OK;
   if (!ready.get(&s, [](SharedMemory* m) {
-        return allow_shared_memory(m, kernel_address(act_decode_kernel<W, X, NT>), 232448);
+        return allow_shared_memory(m, kernel_address(act_decode_kernel<W, X>), 64 * 1024);
       }))
     return s;
   // a CTA for every eight rows where there are few
@@ -193,27 +192,25 @@ te_status launch_act_decode(const FewArgs& a, cudaStream_t st) {
     s = zero_amax(a.amax, st);
     if (s != TE_OK) return s;
   }
-  const cudaError_t e = launch_dependent(act_decode_kernel<W, X, NT>, dim3(static_cast<unsigned>(grid), 1, 1),
+  const cudaError_t e = launch_dependent(act_decode_kernel<W, X>, dim3(static_cast<unsigned>(grid), 1, 1),
                                          dim3(32 * kDecWarps, 1, 1), smem, st, a);
   if (e != cudaSuccess) return record_cuda(e);
   count_launch();
   return launch_status();
 }
 
-template <int W, int X>
-te_status launch_act_decode(const FewArgs& a, cudaStream_t st) {
-  switch ((a.T + 7) / 8) {
-    case 1: return launch_act_decode<W, X, 1>(a, st);
-    case 2: return launch_act_decode<W, X, 2>(a, st);
-    case 3: return launch_act_decode<W, X, 3>(a, st);
-    default: return launch_act_decode<W, X, 4>(a, st);
-  }
-}
-
-// Whether this kernel takes the call, or the one of act_stream.cuh.
+// Whether this kernel takes the call, or the one of act_stream.cuh (us, this / that):
+//   T = 1, BF16: K = 512, N = 512 2.4 / 3.7, K = 768, N = 2048 2.7 / 4.1, K = N = 2048 3.1 / 5.1, K = 1024, N = 4096 3.9 /
+//   4.6, K = 2048, N = 4096 (16 MB) 5.3 / 5.4, K = N = 4096 8.6 / 8.6, K = 4096, N = 16384 24.9 / 24.3; FP8 K = 768,
+//   N = 2048 2.7 / 3.9, K = N = 2048 2.9 / 4.3, K = 1024, N = 4096 3.9 / 4.0, K = N = 4096 6.5 / 5.4;
+//   short rows, many of them: K = 256, N = 8192 BF16 5.6 / 4.0, FP8 5.8 / 2.9;
+//   T = 2, 4 and 8 of a long row: BF16 K = 8192, N = 256 6.0, 7.0 and 9.0 / 6.7, K = 3200, N = 1600 4.0, 4.5 and 5.3 / 5.0;
+//   FP8 K = 8192, N = 256 4.8, 5.3 and 6.2 / 5.1.
+// No tensor memory to set up and loads that go out at once make it the faster one where w is small; a unit of 16 rows
+// costs as much for a short row, and what x takes of shared memory and of the loads is felt beside few rows.
 inline bool act_decodes(int64_t T, int64_t K, int64_t N, int elem) {
-  if (T > 8 || K > (1 << 17)) return false;
-  return act_decode_smem(static_cast<int>(T), static_cast<int>(K), elem) <= 232448;
+  const int64_t row = K * elem;
+  return T <= kActDecTokens && N * row <= (12 << 20) && N <= 4 * row && T * row <= kActDecX;
 }
 
 }  // namespace

@@ -88,7 +88,8 @@ struct Cfg {
   static constexpr bool kPair = CG == 2;
   static constexpr int kBRows = BN / CG;                      // B rows staged by one CTA
   static constexpr bool kBlockScaled = KIND >= kMXFP8;
-  // Staging of the epilogue per warp: 2 KB boxes of 32 rows x 64 bytes.  kGated writes up to seven
+  // Staging of the epilogue per warp: 2 KB boxes of 32 rows x 64 bytes.  kAct and kActGrad have two (act_epilogue.inc).
+  // kGated writes up to seven
   // boxes a tile through two of them; kDgrad holds a g box and a u box (twice, with a stage less, was
   // slower where it matters: 15872 tokens, N = 4096, F = 16384 FP8 841 / 740 us, BF16 1296 / 1270; N = 768,
   // F = 2048 73 / 79).
@@ -104,7 +105,13 @@ struct Cfg {
   // k-tile from one thread outlast the k-tile's MMAs: two copier warps, each issuing the
   // copies of half the k-steps (+29 %).  BF16 and FP8 have no scales and no copier warp.
   static constexpr int kSfCopiers = KIND == kNVFP4 ? 2 : (kBlockScaled ? 1 : 0);
-  static constexpr int kThreads = 32 * (2 + kEpiWarps + kSfCopiers);
+  // kAct gives its epilogue warps the registers that the other warps do not need (setmaxnreg), which goes by groups of
+  // four warps: its copiers are warps 2 and 3 and the epilogue is warps 4 to 11.  FP8 15872 x 4096 x 16384 with z, y and
+  // q 676 -> 655 us, NVFP4 15872 x 16384 x 4096 336 -> 326, BF16 4096 x 4096 x 16384 293 -> 286.
+  static constexpr bool kSplitRegs = EPI == kAct;
+  static constexpr int kEpiFirst = kSplitRegs ? 4 : 2;
+  static constexpr int kCopyFirst = kSplitRegs ? 2 : kCopyWarp;
+  static constexpr int kThreads = kSplitRegs ? 384 : 32 * (2 + kEpiWarps + kSfCopiers);
   static constexpr uint32_t kTmemCols = 512u;
   static constexpr int kABytes = BM * 128;
   static constexpr int kBBytes = kBRows * 128;
@@ -134,6 +141,10 @@ struct Cfg {
   static_assert(kSmemTotal <= 232448, "shared memory budget");
 };
 
+// Registers of a thread at launch and after the split, for kAct.
+constexpr int kLaunchRegs = 168, kFewRegs = 72, kManyRegs = 216;
+static_assert(kFewRegs + 2 * kManyRegs == 3 * kLaunchRegs, "what the block was launched with");
+
 // Programmatic dependent launch (bits of pdl): the kernel waits for the one before it after its set-up;
 // it lets the next one be set up once it has itself begun (after that wait); it waits for the one
 // before it only at its end, being independent of its results, so that what follows in the stream
@@ -158,6 +169,7 @@ struct GemmArgs {
   uint32_t idesc;
   int a_mn, b_mn;       // BF16 only: operand stored [K, M] / [K, N]
   int split;            // SPLIT: CTA pairs that share a tile's K
+  int seg;              // kAct, kActGrad: k-tiles that are added up in tensor memory (0: all; see kSegments)
   int pdl;              // programmatic dependent launch: see kPdl*
   int raster;           // 1: the smaller operand's tiles vary fastest (see tile_coords)
   int* err;
@@ -243,6 +255,19 @@ __device__ __forceinline__ void tile_coords(int tile, int m_tiles, int n_tiles, 
 // it, which adds the parts in the pairs' order after its own, so the result does not depend on timing.
 // The received parts lie where the operands' ring was.
 // dX of 256 tokens, K = 1024, 2 F = 8192 (4 tiles on 76 pairs): 39 -> 19 us.
+// Segments (kAct, kActGrad; args.seg > 0).  The tensor cores round each addition to an accumulator towards zero, so
+// that a long sum shrinks by about 1.7e-8 of itself with every 16 terms in BF16 (relative error of fp32 outputs
+// 1.0e-6 at K = 1024, 4.4e-6 at 4096, 1.9e-5 at 16384; FP8 and MXFP8, whose products are short, 1.2e-6 at 16384; NVFP4
+// below 5e-8).  Where an output is fp32 (y, the sums of dz) a contraction is therefore cut into segments, each added
+// up in an accumulator of its own, which the epilogue warps take over and add to the sum of those before it in fp32
+// registers, rounding to nearest.  BF16 and FP8 have a second accumulator that is filled meanwhile.
+// K = 832 in BF16 (fp32 outputs within 8.1e-7; dZ of 15872 tokens, F = 16384, N = 4096 takes 1249 us, uncut 1207, with
+// K = 768 1289), 8192 in 8 bits (5.0e-7).
+template <int KIND>
+constexpr int kSegment = KIND == kBF16 ? 13 : (KIND == kNVFP4 ? 0 : 64);   // k-tiles
+template <int KIND, int EPI>
+constexpr bool kSegments = (EPI == kAct || EPI == kActGrad) && KIND != kNVFP4;
+
 template <int KIND, int CG, int EPI, bool SPLIT>
 __global__ void __launch_bounds__(Cfg<KIND, CG, EPI>::kThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -288,6 +313,9 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, EPI>::kThreads, 1)
   const int k_lo = SPLIT ? static_cast<int>(static_cast<int64_t>(args.k_tiles) * part / args.split) : 0;
   const int k_num =
       SPLIT ? static_cast<int>(static_cast<int64_t>(args.k_tiles) * (part + 1) / args.split) - k_lo : args.k_tiles;
+  int segs = 1;
+  if constexpr (kSegments<KIND, EPI>)
+    if (args.seg > 0) segs = (k_num + args.seg - 1) / args.seg;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -358,6 +386,8 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, EPI>::kThreads, 1)
   if constexpr (EPI == kGated) gate_rows = ep.F;
   auto b_group = [&](int nt, int h) { return EPI == kGated ? nt + h * (gate_rows >> 7) : nt * 2 + h; };
 
+  if (C::kSplitRegs ? warp < C::kEpiFirst : (warp < 2 || warp >= kCopyWarp)) {
+  if constexpr (C::kSplitRegs) dev::registers_down<kFewRegs>();
   if (warp == 0) {
     // ------------------------------------------------ TMA producer
     if (lane == 0) {
@@ -474,7 +504,10 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, EPI>::kThreads, 1)
       auto sf_slot = [&](int st) {
         return tmem_base + C::kSfTmemBase + static_cast<uint32_t>(st * (C::kSfaCols + C::kSfbCols));
       };
-      for (int tile = unit; tile < num_tiles && ok; tile += units, ++it) {
+      for (int tile = unit; tile < num_tiles && ok; tile += units)
+      for (int sg = 0; sg < segs && ok; ++sg, ++it) {
+        const int k_beg = kSegments<KIND, EPI> ? k_num * sg / segs : 0;
+        const int k_end = kSegments<KIND, EPI> ? k_num * (sg + 1) / segs : k_num;
         const int as = it % C::kAccStages;
         const uint32_t aphase = static_cast<uint32_t>(it / C::kAccStages) & 1u;
         if (!dev::mbar_wait<kPair>(&acc_empty[as], aphase ^ 1u, abort_flag, args.err)) {
@@ -483,7 +516,7 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, EPI>::kThreads, 1)
         }
         dev::tc_fence_after();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(as * BN);
-        for (int kt = 0; kt < k_num; ++kt) {
+        for (int kt = k_beg; kt < k_end; ++kt) {
           const int nstage = stage + 1 == kStages ? 0 : stage + 1;
           const uint32_t nphase = stage + 1 == kStages ? phase ^ 1u : phase;
           const uint32_t a_addr = dev::smem_u32(sA + stage * C::kABytes);
@@ -511,7 +544,7 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, EPI>::kThreads, 1)
                                                                 : dev::smem_desc(a_addr + 32 * ks, 0, 1024, 2);
             const uint64_t bdesc = (KIND == kBF16 && args.b_mn) ? dev::smem_desc(b_addr + 2048 * ks, 8192, 1024, 2)
                                                                 : dev::smem_desc(b_addr + 32 * ks, 0, 1024, 2);
-            const uint32_t acc = (kt | ks) != 0;
+            const uint32_t acc = ((kt - k_beg) | ks) != 0;
             if (KIND == kBF16) {
               if (kPair) dev::mma_f16_pair(d_tmem, adesc, bdesc, args.idesc, acc);
               else dev::mma_f16(d_tmem, adesc, bdesc, args.idesc, acc);
@@ -541,10 +574,10 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, EPI>::kThreads, 1)
       volatile int dummy = 0;
       dev::mbar_wait(drain, 0, &dummy, args.err);
     }
-  } else if (warp >= kCopyWarp) {
+  } else {
     // ------------------------------------------------ scale-factor copiers (one thread each; the pair's leader)
-    const int copier = warp - kCopyWarp;
-    if (C::kBlockScaled && lane == 0 && leader) {
+    const int copier = warp - C::kCopyFirst;
+    if (copier < C::kSfCopiers && lane == 0 && leader) {
       // NVFP4: copier c takes the k-steps c, c + 2 (1 % faster than k-steps 2c, 2c + 1)
       int stage = 0;
       uint32_t phase = 0;
@@ -574,23 +607,23 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, EPI>::kThreads, 1)
         dev::mbar_wait<kPair>(&sf_ready[last], last_phase, &dummy, args.err);
       }
     }
+  }
   } else {
     // ------------------------------------------------ epilogue warps
+    if constexpr (C::kSplitRegs) dev::registers_up<kManyRegs>();
     const int quarter = warp & 3;
-    const int half = (warp - 2) >> 2;
-    uint8_t* stg = smem + C::kSmemStage + (warp - 2) * C::kStgBytes;
+    const int half = (warp - C::kEpiFirst) >> 2;
+    uint8_t* stg = smem + C::kSmemStage + (warp - C::kEpiFirst) * C::kStgBytes;
     const float alpha = (args.alpha_a ? *args.alpha_a : 1.0f) * (args.alpha_b ? *args.alpha_b : 1.0f);
     typename EpiState<EPI>::type est;
     if constexpr (EPI == kGated) est.init(ep, stg, lane);
     if constexpr (EPI == kDgrad) est.init(stg, epi_bar + (warp - 2), lane);
-    if constexpr (EPI == kAct) est.init(ep, stg, epi_bar + 2 * (warp - 2), lane);
-    if constexpr (EPI == kActGrad) est.init(stg, epi_bar + 2 * (warp - 2), lane);
+    if constexpr (EPI == kAct) est.init(ep, stg, epi_bar + 2 * (warp - C::kEpiFirst), lane);
+    if constexpr (EPI == kActGrad) est.init(ep, stg, epi_bar + 2 * (warp - C::kEpiFirst), lane);
     int it = 0;
     for (int tile = unit; tile < num_tiles; tile += units, ++it) {
       int mt, nt;
       tile_coords(tile, args.m_tiles, args.n_tiles, mt, nt, args.raster);
-      const int as = it % C::kAccStages;
-      const uint32_t aphase = static_cast<uint32_t>(it / C::kAccStages) & 1u;
       // this warp's columns of the output, in chunks of 32 accumulator columns (kGated: of g, the
       // same of u beside them)
       int n0 = EPI == kGated ? nt * 128 + half * 64 : nt * BN + half * 128;
@@ -609,12 +642,14 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, EPI>::kThreads, 1)
       }
       if constexpr (EPI == kDgrad || EPI == kAct || EPI == kActGrad)
         if (mine) est.begin(ep, (mt * CG + static_cast<int>(rank)) * BM + quarter * 32, n0, chunks, args.M);
-      const bool acc_ok = dev::mbar_wait<kPair>(&acc_full[as], aphase, abort_flag, args.err);
+      int as = it % C::kAccStages;
+      bool acc_ok = dev::mbar_wait<kPair>(&acc_full[as], static_cast<uint32_t>(it / C::kAccStages) & 1u, abort_flag, args.err);
       if (!SPLIT && !acc_ok) break;
       dev::tc_fence_after();
       // kGated: 64 columns of g (acc[0..1]) and the same 64 of u (acc[2..3]); else 128 columns
-      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
-                             static_cast<uint32_t>(as * BN + half * (EPI == kGated ? 64 : 128));
+      const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
+                                 static_cast<uint32_t>(half * (EPI == kGated ? 64 : 128));
+      const uint32_t taddr = lane_addr + static_cast<uint32_t>(as * BN);
       uint32_t acc[4][32];
 #pragma unroll
       for (int c = 0; c < 4; ++c)
@@ -622,6 +657,34 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, EPI>::kThreads, 1)
       dev::tmem_ld_wait();
 #pragma unroll
       for (int c = 0; c < 4; ++c) dev::reg_fence(acc[c]);
+      if constexpr (kSegments<KIND, EPI>) {
+        for (int sg = 1; sg < segs && acc_ok; ++sg) {
+          // the segment before has been taken over (released as at the tile's end, below)
+          dev::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            dev::tc_fence_after();
+            if (kPair) dev::tc_commit_pair(&acc_empty[as], lead_mask);
+            else dev::mbar_arrive(&acc_empty[as]);
+          }
+          ++it;
+          as = it % C::kAccStages;
+          acc_ok = dev::mbar_wait<kPair>(&acc_full[as], static_cast<uint32_t>(it / C::kAccStages) & 1u, abort_flag, args.err);
+          acc_ok = __all_sync(0xFFFFFFFFu, acc_ok);
+          if (!acc_ok) break;
+          dev::tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t more[32];
+            dev::tmem_ld_32x32b_x32(lane_addr + static_cast<uint32_t>(as * BN + 32 * c), more);
+            dev::tmem_ld_wait();
+            dev::reg_fence(more);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) set_pair(acc[c], i, __fadd2_rn(pair_of(acc[c], i), pair_of(more, i)));
+          }
+        }
+        if (!SPLIT && !acc_ok) break;
+      }
       if constexpr (SPLIT) {
         // every load of the cluster has landed and every MMA has read it: the rings are free
         __syncwarp();
@@ -630,7 +693,7 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, EPI>::kThreads, 1)
         const bool by_half = EPI == kGated && n_split == 4;
         const int per = EPI == kGated ? 2 : 4 / n_split;     // accumulator chunks of a slice
         const int senders = by_half ? 4 : 8;                 // warps of a CTA with a slice for one pair
-        const int who = by_half ? quarter : warp - 2;
+        const int who = by_half ? quarter : warp - C::kEpiFirst;
         const uint32_t slot = dev::smem_u32(smem);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -701,12 +764,21 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, EPI>::kThreads, 1)
         if (!est.tile(ep, acc, alpha, abort_flag, args.err)) break;
         continue;
       }
+      // The operands' ring, once the last tile's MMAs have read it (SPLIT: behind the parts that were exchanged there):
+      // boxes for the epilogue warps.
+      uint8_t* fresh = nullptr;
+      int fresh_boxes = 0;
+      if ((EPI == kAct || EPI == kActGrad) && tile + units >= num_tiles) {
+        constexpr int kRing = kStages * (C::kABytes + C::kBBytes), kFrom = SPLIT ? 3 * 8 * 4096 : 0;
+        fresh_boxes = (kRing - kFrom) / kEpiWarps / 2048;
+        fresh = smem + C::kSmemA + kFrom + (warp - C::kEpiFirst) * fresh_boxes * 2048;
+      }
       if constexpr (EPI == kAct) {
-        if (!est.template tile<KIND == kMXFP8>(ep, acc, alpha, chunks, args.M, abort_flag, args.err)) break;
+        if (!est.template tile<KIND>(ep, acc, alpha, chunks, args.M, fresh, fresh_boxes, abort_flag, args.err)) break;
         continue;
       }
       if constexpr (EPI == kActGrad) {
-        if (!est.tile(ep, acc, alpha, args.M, abort_flag, args.err)) break;
+        if (!est.tile(ep, acc, alpha, args.M, fresh, fresh_boxes, abort_flag, args.err)) break;
         continue;
       }
 
@@ -777,7 +849,7 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, EPI>::kThreads, 1)
   }
 
   if constexpr (SPLIT) {
-    if (warp < 2) {   // the other warps' part in the epilogue's two barriers
+    if (warp < C::kEpiFirst) {   // the other warps' part in the epilogue's two barriers
       __syncwarp();
       dev::cluster_sync();
       dev::cluster_sync();
@@ -818,7 +890,7 @@ te_status launch_gemm(const void* A, const void* B, int64_t row_bytes, const uin
                       te_dtype out, int accumulate, int64_t M, int64_t N, int64_t K, uint32_t afmt, uint32_t bfmt,
                       cudaStream_t st, int a_mn = 0, int b_mn = 0,
                       const typename EpiParam<EPI>::type& ep = typename EpiParam<EPI>::type(), int pdl = 0,
-                      int max_split = 4) {
+                      int max_split = 4, int seg = 0) {
   using C = Cfg<KIND, CG, EPI>;
   static_assert(!SPLIT || (CG == 2 && !C::kBlockScaled), "split K: pairs, BF16 and FP8");
   static PerDevice<GemmSetup> setups;
@@ -837,6 +909,13 @@ te_status launch_gemm(const void* A, const void* B, int64_t row_bytes, const uin
   cfg.numAttrs = 1;
   te_status s = TE_OK;
   const GemmSetup* setup = setups.get(&s, [&](GemmSetup* m) {
+    if (C::kSplitRegs) {
+      // (a split of other registers than the block has would wait for ever)
+      cudaFuncAttributes fa;
+      if (cudaFuncGetAttributes(&fa, kernel_address(gemm_kernel<KIND, CG, EPI, SPLIT>)) != cudaSuccess)
+        return record_cuda(cudaGetLastError());
+      if (fa.numRegs != kLaunchRegs) return TE_ERR_UNSUPPORTED;
+    }
     return m->set(kernel_address(gemm_kernel<KIND, CG, EPI, SPLIT>), CG, SPLIT, C::kSmemTotal, cfg);
   });
   if (setup == nullptr) return s;
@@ -891,6 +970,7 @@ te_status launch_gemm(const void* A, const void* B, int64_t row_bytes, const uin
   g.b_mn = b_mn;
   g.raster = (KIND != kBF16 && g.k_tiles >= 64 && g.m_tiles != g.n_tiles) ? 1 : 0;   // >= 8 KB of K per row
   g.pdl = pdl;
+  g.seg = seg;
   g.err = err;
   const int tiles = g.m_tiles * g.n_tiles;
   g.split = 1;
@@ -903,7 +983,7 @@ te_status launch_gemm(const void* A, const void* B, int64_t row_bytes, const uin
     else if (max_split >= 2 && tiles <= setup->units && g.k_tiles >= 48) g.split = 2;
     if (g.split == 1)
       return launch_gemm<KIND, CG, EPI, false>(A, B, row_bytes, sfa, sfb, sf_katoms, alpha_a, alpha_b, bias, D, out,
-                                               accumulate, M, N, K, afmt, bfmt, st, a_mn, b_mn, ep, pdl);
+                                               accumulate, M, N, K, afmt, bfmt, st, a_mn, b_mn, ep, pdl, max_split, seg);
     attr[0].val.clusterDim.x = static_cast<unsigned>(2 * g.split);
   }
   // The fewest CTA pairs that keep the number of waves: every pair runs the same number of
