@@ -409,9 +409,12 @@ te_status te_act_bwd_bf16(const void* x, const void* w, const void* w2, const vo
     if (tx <= free_pairs) share = 4 * tx <= free_pairs ? 4 : (2 * tx <= free_pairs ? 2 : 1);
   }
   if (s == TE_OK && dx) s = gemm_bf16_tokens(dz, 0, w, 1, dx, TE_BF16, 0, T, K, F, st, kPdlChain, share);
-  if (s == TE_OK && dbias) s = reduce_dbias(workspace, T, F, dbias, dx != nullptr, st);
   if (s == TE_OK && dw)
-    s = gemm_bf16_tokens(dz, 1, x, 1, dw, dw_dtype, accumulate, F, K, T, st, dx || dbias ? kPdlWaitAtEnd : kPdlChain);
+    s = gemm_bf16_tokens(dz, 1, x, 1, dw, dw_dtype, accumulate, F, K, T, st,
+                         dx ? kPdlWaitAtEnd | kPdlTrigger : kPdlChain);
+  // (behind dW, which lets it start: between the two it would hold SMs that dW needs until dX ends, 39.5 us for 31 at
+  // 1001 tokens, K = N = 768, F = 2048)
+  if (s == TE_OK && dbias) s = reduce_dbias(workspace, T, F, dbias, dx != nullptr || dw != nullptr, st);
   return s;
 }
 
