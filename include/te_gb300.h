@@ -439,8 +439,9 @@ te_status te_gated_bwd_bf16(const void* x, const void* w, const void* w2, const 
  *      (TE_ERR_UNSUPPORTED).
  * N % 16 == 0 (N % 32 where an MXFP8 q is asked for); K % 16 == 0 (BF16, FP8) or K % 32 == 0 (MXFP8,
  * NVFP4).  T = 0 is a no-op but for the amax and 1 / scale.  Which kernel a call takes goes by its
- * sizes alone, and sums run in a fixed order, so the same call gives the same bits every time.  First
- * calls and stream captures as for the gated projections above. */
+ * sizes alone, and sums run in a fixed order, so the same call gives the same bits every time.  An output
+ * shares memory with an input, or with another output, only where it says so.  First calls and stream
+ * captures as for the gated projections above. */
 enum { TE_ACT_NONE = 2, TE_ACT_RELU = 3 };
 
 te_status te_act_gemm_bf16(const void* x, const void* w, const float* bias, int act, const void* residual, void* z,

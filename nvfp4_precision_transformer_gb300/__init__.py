@@ -4,7 +4,8 @@ The compute lives in ``libte_gb300.so`` (hand-written CUDA for sm_103a behind
 the C ABI in ``include/te_gb300.h``); this package is the thin Python side:
 ``_lib`` binds the C entry points by name, ``linear`` composes them into the
 per-recipe linear-layer steps (Fprop / Dgrad / Wgrad), ``gated`` into the gated
-feed-forward block (RMSNorm, gated projections, down projection) and ``shapes``
+feed-forward block (RMSNorm, gated projections, down projection), ``mlp`` into the one with a
+single activation (LayerNorm, linears with bias, activation and residual) and ``shapes``
 derives the GEMM shapes of a transformer layer from its configuration.
 """
 from ._lib import (  # noqa: F401

@@ -1,5 +1,5 @@
-// The linear with bias, activation and residual for a few tokens (decoding), BF16 and FP8: w is read once from HBM
-// and everything else is small, so the kernel is a stream over w.
+// The linear with bias, activation and residual for up to eight tokens of a small w (act_decodes, below), BF16 and FP8:
+// w is read once from HBM and everything else is small, so the kernel is a stream over w.
 //
 // One persistent CTA of 16 warps per SM keeps x in shared memory and has an equal share of w's rows (within one:
 // with whole 16-row units the SMs that have one unit more would be alone at the end), which it takes up to 16 rows

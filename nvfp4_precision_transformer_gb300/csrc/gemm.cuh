@@ -105,10 +105,11 @@ struct Cfg {
   // k-tile from one thread outlast the k-tile's MMAs: two copier warps, each issuing the
   // copies of half the k-steps (+29 %).  BF16 and FP8 have no scales and no copier warp.
   static constexpr int kSfCopiers = KIND == kNVFP4 ? 2 : (kBlockScaled ? 1 : 0);
-  // kAct gives its epilogue warps the registers that the other warps do not need (setmaxnreg), which goes by groups of
-  // four warps: its copiers are warps 2 and 3 and the epilogue is warps 4 to 11.  FP8 15872 x 4096 x 16384 with z, y and
-  // q 676 -> 655 us, NVFP4 15872 x 16384 x 4096 336 -> 326, BF16 4096 x 4096 x 16384 293 -> 286.
-  static constexpr bool kSplitRegs = EPI == kAct;
+  // kAct and kActGrad give their epilogue warps the registers that the other warps do not need (setmaxnreg), which goes
+  // by groups of four warps: the copiers are warps 2 and 3 and the epilogue is warps 4 to 11.  FP8 15872 x 4096 x 16384
+  // with z, y and q 676 -> 655 us, NVFP4 15872 x 16384 x 4096 336 -> 326, BF16 4096 x 4096 x 16384 293 -> 286; dz of
+  // 15872 tokens, F = 16384, N = 4096 in NVFP4 515 -> 494, of 4096 in MXFP8 203 -> 205.
+  static constexpr bool kSplitRegs = EPI == kAct || EPI == kActGrad;
   static constexpr int kEpiFirst = kSplitRegs ? 4 : 2;
   static constexpr int kCopyFirst = kSplitRegs ? 2 : kCopyWarp;
   static constexpr int kThreads = kSplitRegs ? 384 : 32 * (2 + kEpiWarps + kSfCopiers);
@@ -141,7 +142,7 @@ struct Cfg {
   static_assert(kSmemTotal <= 232448, "shared memory budget");
 };
 
-// Registers of a thread at launch and after the split, for kAct.
+// Registers of a thread at launch and after the split.
 constexpr int kLaunchRegs = 168, kFewRegs = 72, kManyRegs = 216;
 static_assert(kFewRegs + 2 * kManyRegs == 3 * kLaunchRegs, "what the block was launched with");
 
@@ -386,6 +387,7 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, EPI>::kThreads, 1)
   if constexpr (EPI == kGated) gate_rows = ep.F;
   auto b_group = [&](int nt, int h) { return EPI == kGated ? nt + h * (gate_rows >> 7) : nt * 2 + h; };
 
+  // (the split stands at the head of each side: before a point where they meet again it spilled)
   if (C::kSplitRegs ? warp < C::kEpiFirst : (warp < 2 || warp >= kCopyWarp)) {
   if constexpr (C::kSplitRegs) dev::registers_down<kFewRegs>();
   if (warp == 0) {
