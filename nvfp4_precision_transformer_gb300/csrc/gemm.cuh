@@ -108,7 +108,7 @@ struct Cfg {
   // kAct and kActGrad give their epilogue warps the registers that the other warps do not need (setmaxnreg), which goes
   // by groups of four warps: the copiers are warps 2 and 3 and the epilogue is warps 4 to 11.  FP8 15872 x 4096 x 16384
   // with z, y and q 676 -> 655 us, NVFP4 15872 x 16384 x 4096 336 -> 326, BF16 4096 x 4096 x 16384 293 -> 286; dz of
-  // 15872 tokens, F = 16384, N = 4096 in NVFP4 515 -> 494, of 4096 in MXFP8 203 -> 205.
+  // 15872 tokens, F = 16384, N = 4096 in NVFP4 515 -> 494, of 4096 in MXFP8 203 -> 205 (before the sums were packed).
   static constexpr bool kSplitRegs = EPI == kAct || EPI == kActGrad;
   static constexpr int kEpiFirst = kSplitRegs ? 4 : 2;
   static constexpr int kCopyFirst = kSplitRegs ? 2 : kCopyWarp;
