@@ -259,7 +259,8 @@ __global__ void __launch_bounds__(AstCfg<KIND, NP>::kThreads, 1)
         }
         dev::tc_fence_after();
         const uint32_t d = tmem_base + static_cast<uint32_t>(as * NP);
-        const int k_beg = w.k_num * sg / segs, k_end = w.k_num * (sg + 1) / segs;
+        const int k_beg = sg > 0 ? part_begin(w.k_num, sg, segs) : 0;
+        const int k_end = sg + 1 < segs ? part_begin(w.k_num, sg + 1, segs) : w.k_num;
         for (int kt = k_beg; kt < k_end; ++kt) {
           if (!dev::mbar_wait(&full[stage], phase, abort_flag, err) ||
               (C::kBlock && !dev::mbar_wait(&sf_ready[stage], phase, abort_flag, err))) {

@@ -86,6 +86,12 @@ __host__ __device__ inline uint64_t scale_offset(uint64_t r, uint64_t j, uint64_
   return ((r >> 7) * (kpad >> 2) + (j >> 2)) * 512u + (r & 31u) * 16u + ((r >> 5) & 3u) * 4u + (j & 3u);
 }
 
+// Where part `part` of n things in `parts` nearly equal parts begins (n of them: the end of the last).  n and parts reach
+// 2^24 and 2^21 (k-tiles and segments of a contraction), so the product takes 64 bits.
+__host__ __device__ inline int part_begin(int n, int part, int parts) {
+  return static_cast<int>(static_cast<int64_t>(n) * part / parts);
+}
+
 constexpr int kErrTimeout = TE_ERR_TIMEOUT;
 
 }  // namespace te

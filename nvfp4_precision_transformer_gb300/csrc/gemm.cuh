@@ -311,9 +311,8 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, EPI>::kThreads, 1)
   const int unit = static_cast<int>(blockIdx.x) / ctas;
   const int units = static_cast<int>(gridDim.x) / ctas;
   // this pair's k-tiles
-  const int k_lo = SPLIT ? static_cast<int>(static_cast<int64_t>(args.k_tiles) * part / args.split) : 0;
-  const int k_num =
-      SPLIT ? static_cast<int>(static_cast<int64_t>(args.k_tiles) * (part + 1) / args.split) - k_lo : args.k_tiles;
+  const int k_lo = SPLIT ? part_begin(args.k_tiles, part, args.split) : 0;
+  const int k_num = SPLIT ? part_begin(args.k_tiles, part + 1, args.split) - k_lo : args.k_tiles;
   int segs = 1;
   if constexpr (kSegments<KIND, EPI>)
     if (args.seg > 0) segs = (k_num + args.seg - 1) / args.seg;
@@ -508,8 +507,8 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, EPI>::kThreads, 1)
       };
       for (int tile = unit; tile < num_tiles && ok; tile += units)
       for (int sg = 0; sg < segs && ok; ++sg, ++it) {
-        const int k_beg = kSegments<KIND, EPI> ? k_num * sg / segs : 0;
-        const int k_end = kSegments<KIND, EPI> ? k_num * (sg + 1) / segs : k_num;
+        const int k_beg = kSegments<KIND, EPI> && sg > 0 ? part_begin(k_num, sg, segs) : 0;
+        const int k_end = kSegments<KIND, EPI> && sg + 1 < segs ? part_begin(k_num, sg + 1, segs) : k_num;
         const int as = it % C::kAccStages;
         const uint32_t aphase = static_cast<uint32_t>(it / C::kAccStages) & 1u;
         if (!dev::mbar_wait<kPair>(&acc_empty[as], aphase ^ 1u, abort_flag, args.err)) {
