@@ -169,6 +169,20 @@ te_status grads_args(ActArgs* ep, const Grads& g, int64_t T, int64_t F) {
   return s == TE_OK && g.act != TE_ACT_NONE ? boxes(&ep->z, g.z, T, F, 2) : s;
 }
 
+// dW [F, K] (+)= dZ^T X (both MN-major).  In fp32 by the forward pass's kernel, whose residual is what dW holds where it
+// is added to: its sum over the tokens is cut into segments, as every fp32 output's (kSegments in gemm.cuh; 16384 tokens
+// in one piece are 2e-5 short).
+te_status weight_grad(const void* dz, const void* x, void* dw, te_dtype dt, int accumulate, int64_t T, int64_t K, int64_t F,
+                      cudaStream_t st, int pdl) {
+  if (dt != TE_F32) return gemm_bf16_tokens(dz, 1, x, 1, dw, dt, 0, F, K, T, st, pdl);
+  ActArgs ep = {};
+  const Outputs o = {nullptr, TE_ACT_NONE, accumulate ? dw : nullptr, nullptr, dw, TE_F32, nullptr};
+  const te_status s = act_args(&ep, o, F, K);
+  if (s != TE_OK) return s;
+  return launch_gemm<kBF16, 2, kAct, true>(dz, x, T * 2, nullptr, nullptr, 0, nullptr, nullptr, nullptr, nullptr, TE_F32, 0,
+                                           F, K, T, 1u, 1u, st, 1, 1, ep, pdl, 4, kSegment<kBF16>);
+}
+
 // No tokens: dbias = 0.
 te_status empty_dbias(float* dbias, int64_t F, cudaStream_t st) {
   if (dbias && cudaMemsetAsync(dbias, 0, static_cast<size_t>(F) * sizeof(float), st) != cudaSuccess)
@@ -410,8 +424,7 @@ te_status te_act_bwd_bf16(const void* x, const void* w, const void* w2, const vo
   }
   if (s == TE_OK && dx) s = gemm_bf16_tokens(dz, 0, w, 1, dx, TE_BF16, 0, T, K, F, st, kPdlChain, share);
   if (s == TE_OK && dw)
-    s = gemm_bf16_tokens(dz, 1, x, 1, dw, dw_dtype, accumulate, F, K, T, st,
-                         dx ? kPdlWaitAtEnd | kPdlTrigger : kPdlChain);
+    s = weight_grad(dz, x, dw, dw_dtype, accumulate, T, K, F, st, dx ? kPdlWaitAtEnd | kPdlTrigger : kPdlChain);
   // (behind dW, which lets it start: between the two it would hold SMs that dW needs until dX ends, 39.5 us for 31 at
   // 1001 tokens, K = N = 768, F = 2048)
   if (s == TE_OK && dbias) s = reduce_dbias(workspace, T, F, dbias, dx != nullptr || dw != nullptr, st);

@@ -259,7 +259,7 @@ __device__ __forceinline__ void tile_coords(int tile, int m_tiles, int n_tiles, 
 // Segments (kAct, kActGrad; args.seg > 0).  The tensor cores round each addition to an accumulator towards zero, so
 // that a long sum shrinks by about 1.7e-8 of itself with every 16 terms in BF16 (relative error of fp32 outputs
 // 1.0e-6 at K = 1024, 4.4e-6 at 4096, 1.9e-5 at 16384; FP8 and MXFP8, whose products are short, 1.2e-6 at 16384; NVFP4
-// below 5e-8).  Where an output is fp32 (y, the sums of dz) a contraction is therefore cut into segments, each added
+// below 5e-8).  Where an output is fp32 (y, the sums of dz, dW) a contraction is therefore cut into segments, each added
 // up in an accumulator of its own, which the epilogue warps take over and add to the sum of those before it in fp32
 // registers, rounding to nearest.  BF16 and FP8 have a second accumulator that is filled meanwhile.
 // K = 832 in BF16 (fp32 outputs within 8.1e-7; dZ of 15872 tokens, F = 16384, N = 4096 takes 1249 us, uncut 1207, with
