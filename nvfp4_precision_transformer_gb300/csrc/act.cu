@@ -264,7 +264,7 @@ te_status te_act_gemm_fp8(const uint8_t* x, te_dtype fx, const uint8_t* w, te_dt
   }
   if (q_amax && (s = zero_amax(q_amax, st)) != TE_OK) return s;
   return launch_gemm<kFP8, 2, kAct, true>(x, w, K, nullptr, nullptr, 0, x_scale_inv, w_scale_inv, nullptr, nullptr,
-                                          TE_BF16, 0, T, N, K, fp8_code(fx), fp8_code(fw), st, 0, 0, ep, kPdlChain, 4, ep.y_f32 ? kSegment<kFP8> : 0);
+                                          TE_BF16, 0, T, N, K, fp8_code(fx), fp8_code(fw), st, 0, 0, ep, kPdlChain, 4, kSegment<kFP8>);
 }
 
 te_status te_act_gemm_mxfp8(const uint8_t* x, te_dtype fx, const uint8_t* sx, const uint8_t* w, te_dtype fw,
@@ -297,7 +297,7 @@ te_status te_act_gemm_mxfp8(const uint8_t* x, te_dtype fx, const uint8_t* sx, co
   ep.s_rows = static_cast<int>((T + 127) / 128 * 128);
   return launch_gemm<kMXFP8, 2, kAct>(x, w, K, sx, sw, (K / 32 + 3) / 4, nullptr, nullptr, nullptr, nullptr, TE_BF16, 0,
                                       T, N, K, fp8_code(fx), fp8_code(fw), static_cast<cudaStream_t>(stream), 0, 0, ep,
-                                      kPdlChain, 4, ep.y_f32 ? kSegment<kMXFP8> : 0);
+                                      kPdlChain, 4, kSegment<kMXFP8>);
 }
 
 te_status te_act_gemm_nvfp4(const uint8_t* x, const uint8_t* sx, const float* gx, const uint8_t* w, const uint8_t* sw,

@@ -126,7 +126,7 @@ __device__ __forceinline__ void ast_emit(const FewArgs& a, uint32_t (&v)[NT], fl
   }
 }
 
-// seg: k-tiles that are added up in tensor memory where y is fp32 (0: all; kSegments in gemm.cuh has the reason); the
+// seg: k-tiles that are added up in tensor memory (0: all; kSegments in gemm.cuh has the reason and the rule); the
 // two accumulators take turns with segments as with tiles.
 template <int KIND, int NP, bool SPLIT>
 __global__ void __launch_bounds__(AstCfg<KIND, NP>::kThreads, 1)
@@ -481,7 +481,7 @@ te_status launch_act_stream(const FewArgs& a, uint32_t xfmt, uint32_t wfmt, cuda
   uint32_t idesc = make_idesc(KIND, wfmt, xfmt, 128);
   idesc = (idesc & ~(0x3Fu << 17)) | (static_cast<uint32_t>(NP >> 3) << 17);
   const int grid = split > 1 ? split * tiles : (tiles < num_sms() ? tiles : num_sms());
-  const int seg = a.y_f32 ? kSegment<KIND> : 0;
+  const int seg = KIND == kBF16 && !a.y_f32 ? 0 : kSegment<KIND>;   // as in gemm_kernel
   if (a.amax && (s = zero_amax(a.amax, st)) != TE_OK) return s;
   const dim3 g(static_cast<unsigned>(grid), 1, 1), block(C::kThreads, 1, 1);
   const cudaError_t e =

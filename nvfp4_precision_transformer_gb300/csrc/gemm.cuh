@@ -259,11 +259,18 @@ __device__ __forceinline__ void tile_coords(int tile, int m_tiles, int n_tiles, 
 // Segments (kAct, kActGrad; args.seg > 0).  The tensor cores round each addition to an accumulator towards zero, so
 // that a long sum shrinks by about 1.7e-8 of itself with every 16 terms in BF16 (relative error of fp32 outputs
 // 1.0e-6 at K = 1024, 4.4e-6 at 4096, 1.9e-5 at 16384; FP8 and MXFP8, whose products are short, 1.2e-6 at 16384; NVFP4
-// below 5e-8).  Where an output is fp32 (y, the sums of dz, dW) a contraction is therefore cut into segments, each added
-// up in an accumulator of its own, which the epilogue warps take over and add to the sum of those before it in fp32
-// registers, rounding to nearest.  BF16 and FP8 have a second accumulator that is filled meanwhile.
-// K = 832 in BF16 (fp32 outputs within 8.1e-7; dZ of 15872 tokens, F = 16384, N = 4096 takes 1249 us, uncut 1207, with
-// K = 768 1289), 8192 in 8 bits (5.0e-7).
+// below 5e-8).  Where an output is fp32 (y, the amax of q, the sums of dz, dW) a contraction is therefore cut into segments,
+// each added up in an accumulator of its own, which the epilogue warps take over and add to the sum of those before it in
+// fp32 registers, rounding to nearest.  BF16 and FP8 have a second accumulator that is filled meanwhile.
+// FP8 and MXFP8 are always cut, so z and q do not depend on the other outputs: 8192 elements (relative error 5.0e-7) cost
+// nothing in FP8 (K = 16384, N = 4096, 15872 tokens 586 us, uncut 586) and 1 % in MXFP8 (643, uncut 635).
+// BF16, whose segments are short, is cut in the backward pass (dz does not depend on whether its sums are asked for) and
+// where y is fp32: uncut, a bf16 output is far within its own rounding, and cut it would cost 3 to 6 % (4096 tokens, K =
+// 16384, N = 4096 307 -> 327 us).  13 k-tiles keep the error within 8e-7 at every K (terms of both signs; of one sign
+// 1.7e-6, uncut 7.9e-5 at 16384).  Errors at K = 1024, 2048, 4096, 8192, 16384, and us of y in fp32 at 4096 tokens, K = N = 4096, and of dz at 15872 tokens, F = 16384, N = 4096:
+//   10 k-tiles 4.7e-7 4.7e-7 5.5e-7 6.0e-7 6.0e-7  92.4  1338     13  4.7e-7 6.5e-7 7.8e-7 7.9e-7 7.9e-7  88.3  1295
+//   16         9.9e-7 1.0e-6 9.9e-7 1.0e-6 1.0e-6  87.3  1325     22  9.9e-7 1.0e-6 1.4e-6 1.4e-6 1.4e-6  86.5  1247
+//   uncut      9.9e-7 2.1e-6 4.4e-6 9.1e-6 1.9e-5  84.9  1241
 template <int KIND>
 constexpr int kSegment = KIND == kBF16 ? 13 : (KIND == kNVFP4 ? 0 : 64);   // k-tiles
 template <int KIND, int EPI>

@@ -11,6 +11,9 @@ import torch
 
 import nvfp4_precision_transformer_gb300 as te
 from tests import gpu_util as G
+from tests.test_gpu_act import forward
+from tests.test_gpu_act_forms import form
+from tests.test_gpu_gated import Out
 
 SEGMENT = {"bf16": 13 * 64, "fp8": 64 * 128, "mxfp8": 64 * 128}      # elements
 GROUP = {"bf16": 2 ** 18 + 15, "fp8": 2 ** 15 + 15, "mxfp8": 2 ** 15 + 15}
@@ -26,6 +29,23 @@ def _pattern(kind):
         v[1:30:4] = 256.0                                       # 8 x 256 x 16
         v[30] = 0.9375
     return v
+
+
+def _codes(t, kind):
+    return t.bfloat16() if kind == "bf16" else t.to(torch.float8_e4m3fn).view(torch.uint8)
+
+
+def operands(kind, T, K, N):
+    """x and w on the GPU, their product in 64 bits, and the products' factors of the rows and columns."""
+    rows = torch.exp2(-torch.arange(T, device=G.DEV).remainder(3).float())
+    cols = torch.exp2(-torch.arange(N, device=G.DEV).remainder(2).float())
+    x = _codes(rows[:, None] * (1.0 if kind == "bf16" else 16.0), kind).expand(T, K).contiguous()
+    w = _codes(cols[:, None] * _pattern(kind).to(G.DEV)[None, :], kind).repeat(1, K // TERMS[kind])
+    return x, w, float(GROUP[kind]) * (K // TERMS[kind]) * (rows.double()[:, None] * cols.double()[None, :])
+
+
+def scales(R, C):
+    return torch.full((te.te_scale_bytes(te.E8M0, R, C),), 127, dtype=torch.uint8, device=G.DEV)
 
 
 def segments(kind, K):
@@ -63,3 +83,40 @@ def test_weight_gradient_in_fp32(T, K, F):
         G.check_no_device_error()
         total = want + before.double() if "accumulate" in kw else want
         assert bool(((dw.double() - total).abs() <= allowed("bf16", T, total)).all()), (kw, float((dw.double() / total - 1).abs().max()))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,N,what", [(24, 10256, "stream"), (2080, 272, "pair shared"), (2080, 3344, "pair")])
+def test_amax_of_the_8_bit_output(T, N, what):
+    """An fp32 output too, whether y is there or not."""
+    K = 131072
+    x, w, want = operands("fp8", T, K, N)
+    q, y, amax, one = G.u8(T, N), torch.zeros(T, N, dtype=torch.bfloat16, device=G.DEV), G.scalar(-1.0), G.scalar(1.0)
+    for kw in (dict(), dict(y=y)):
+        def call(stream=None):
+            te.te_act_gemm_fp8(x, te.E4M3, w, te.E4M3, one, one, te.ACT_NONE, q=q, q_scale=one, q_amax=amax, stream=stream, **kw)
+
+        call()
+        torch.cuda.synchronize()
+        G.check_no_device_error()
+        top = want.max()
+        assert bool((amax.double() - top).abs() <= allowed("fp8", K, top)), amax.item() / top.item() - 1
+        assert form(call)[0] == what
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["fp8", "mxfp8", "nvfp4"])
+@pytest.mark.parametrize("T,K,N", [(24, 32768, 4096), (300, 32768, 1056), (2080, 16512, 3360)])
+def test_outputs_do_not_depend_on_one_another(kind, T, K, N):
+    """z and q, bit for bit, with y in bf16, in fp32 and without it."""
+    sets = [("z", "bias"), ("z", "y", "bias"), ("z", "y32", "bias")]
+    if kind != "nvfp4":
+        sets += [("q", "bias"), ("z", "q", "y32", "bias")]
+    first, ops = {}, None
+    for outs in sets:
+        o = forward(kind, T, K, N, "gelu", outs, ops=ops)
+        ops = (o["x"], o["w"])
+        for n in ("z", "q", "s", "amax"):
+            if o.get(n) is not None:
+                v = o[n].t if isinstance(o[n], Out) else o[n]
+                assert torch.equal(first.setdefault(n, v), v), (outs, n)
