@@ -690,19 +690,20 @@ def te_act_dgrad_nvfp4(dy, sd, gd, w2, sw, gw, z, act: int, dz, dbias=None, work
 
 def te_act_bwd_bf16(x, w, w2, dy, z, act: int, dz, dbias=None, workspace=None, dx=None, dw=None, accumulate: int = 0,
                     stream=None):
-    """The BF16 backward pass: dz and dbias from dy [T, N] and w2 [N, F], then dx = dz w and dw (+)= dz^T x."""
+    """The BF16 backward pass: dz and dbias from dy [T, N] and w2 [N, F], then dx = dz w and dw (+)= dz^T x.  x may be None
+    where dw is, w where dx is."""
     fn = "te_act_bwd_bf16"
     dev = _device()
-    T, K, F = _act_shape(fn, x, w)
-    if dy.dim() != 2:
-        raise ValueError(f"{fn}: dy has shape {tuple(dy.shape)}, expected [T, N]")
-    N = dy.shape[1]
+    if dy.dim() != 2 or w2.dim() != 2:
+        raise ValueError(f"{fn}: dy {tuple(dy.shape)} and w2 {tuple(w2.shape)} are not [T, N] and [N, F]")
+    (T, N), F = dy.shape, w2.shape[1]
+    K = next((t.shape[1] for t in (x, w) if t is not None and t.dim() == 2), 0)
     own = _act_dz(fn, dev, T, F, z, act, dz, dbias, workspace)
     _check(fn, lib().te_act_bwd_bf16(
-        _need(fn, dev, "x", x, _bf16, (T, K)), _need(fn, dev, "w", w, _bf16, (F, K)), _need(fn, dev, "w2", w2, _bf16, (N, F)),
-        _need(fn, dev, "dy", dy, _bf16, (T, N)), *own, _need(fn, dev, "dx", dx, _bf16, (T, K), True),
-        _need(fn, dev, "dw", dw, (_bf16, _f32), (F, K), True), BF16 if dw is None else _out_dtype(dw), int(accumulate), T, K, F,
-        N, _stream(stream, dev)))
+        _need(fn, dev, "x", x, _bf16, (T, K), dw is None), _need(fn, dev, "w", w, _bf16, (F, K), dx is None),
+        _need(fn, dev, "w2", w2, _bf16, (N, F)), _need(fn, dev, "dy", dy, _bf16, (T, N)), *own,
+        _need(fn, dev, "dx", dx, _bf16, (T, K), True), _need(fn, dev, "dw", dw, (_bf16, _f32), (F, K), True),
+        BF16 if dw is None else _out_dtype(dw), int(accumulate), T, K, F, N, _stream(stream, dev)))
 
 
 def te_scale_bytes(scale_fmt: int, rows: int, cols: int) -> int:
