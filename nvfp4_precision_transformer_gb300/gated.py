@@ -26,6 +26,14 @@ from .linear import DelayedState
 RECIPES = ("bf16", "fp8_delayed", "mxfp8")
 FWD_SLOTS = ("y", "w", "h", "w2")
 BWD_SLOTS = ("dout", "dgu")
+NORM_COLS = 16384       # the most columns that the norms' kernels take
+
+
+def _need16(fn: str, dev: int, name: str, t, dtype, shape, optional: bool = False) -> None:
+    """``L._need``, and the 16-byte boundary that the kernels start from."""
+    at = L._need(fn, dev, name, t, dtype, shape, optional)
+    if at is not None and at % 16:
+        raise ValueError(f"{fn}: {name} does not start on a 16-byte boundary")
 
 
 class _Block:
@@ -49,6 +57,14 @@ class _Block:
             self.slots.update({n: self.bwd.slot(i) for i, n in enumerate(bwd)})
             self.te_recipe = L.te_recipe(L.E4M3, L.E5M2, history_len, L.ALGO_MAX, 0, 1)
         self.step_idx = 0
+
+    @staticmethod
+    def _check_norm(K: int, eps: float) -> None:
+        """What the norm, which is not the first launch of a pass, would refuse."""
+        if K > NORM_COLS:
+            raise ValueError(f"K {K} is more than the {NORM_COLS} columns of the norm")
+        if not 0.0 <= eps <= torch.finfo(torch.float32).max:
+            raise ValueError(f"eps {eps} is not a finite number >= 0")
 
     def _end_step(self) -> None:
         """The scales of the next step."""

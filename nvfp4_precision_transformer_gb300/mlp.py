@@ -17,7 +17,7 @@ from __future__ import annotations
 import torch
 
 from . import _lib as L
-from .gated import RECIPES, _Block
+from .gated import RECIPES, _Block, _need16
 
 FWD_SLOTS = ("n", "w1", "h", "w2")
 BWD_SLOTS = ("dy", "dz")
@@ -30,8 +30,9 @@ class MLP(_Block):
     ``backward(dy)`` takes its gradient and leaves ``dx`` (the gradient of x and of residual alike), ``dgamma``,
     ``dbeta``, ``dw1``, ``db1``, ``dw2`` and ``db2``.
 
-    x, residual and dy are contiguous bf16 [tokens, K], tokens, K and F multiples of 16 (32 in MXFP8); w1 and w2 bf16, or
-    fp32 where the recipe quantizes them; gamma, beta, b1, b2 fp32.  Anything else is refused before the first launch.
+    x, residual and dy are contiguous bf16 [tokens, K], tokens, K and F multiples of 16 (32 in MXFP8), K at most 16384; w1
+    and w2 bf16, or fp32 where the recipe quantizes them; gamma, beta, b1, b2 fp32; all on 16-byte boundaries.  Anything
+    else is refused before the first launch.
     Where residual is None, x itself is what the backward pass reads as s: it has to keep its values until then."""
 
     def __init__(self, gamma: torch.Tensor, beta: torch.Tensor, w1: torch.Tensor, b1: torch.Tensor, w2: torch.Tensor,
@@ -45,6 +46,7 @@ class MLP(_Block):
         step = 32 if recipe == "mxfp8" else 16
         if tokens <= 0 or tokens % step or K % step or F % step:
             raise ValueError(f"{tokens} tokens, K {K} and F {F} are not multiples of {step}")
+        self._check_norm(K, eps)
         if act not in (L.ACT_NONE, L.ACT_RELU, L.ACT_SILU, L.ACT_GELU):
             raise ValueError(f"act {act} is no activation")
         self.gamma, self.beta, self.w1, self.b1, self.w2, self.b2 = gamma, beta, w1, b1, w2, b2
@@ -71,15 +73,15 @@ class MLP(_Block):
         for name, dtype, shape in (("gamma", torch.float32, (self.K,)), ("beta", torch.float32, (self.K,)),
                                    ("w1", weight, (self.F, self.K)), ("b1", torch.float32, (self.F,)),
                                    ("w2", weight, (self.K, self.F)), ("b2", torch.float32, (self.K,))):
-            L._need(fn, dev, name, getattr(self, name), dtype, shape)
+            _need16(fn, dev, name, getattr(self, name), dtype, shape)
 
     # ---- passes ----------------------------------------------------------------------------------
     def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None) -> torch.Tensor:
         E4, shape = L.E4M3, (self.T, self.K)
         fn, dev = "MLP.forward", L._device()
         self._check_weights(fn, dev)
-        L._need(fn, dev, "x", x, torch.bfloat16, shape)
-        L._need(fn, dev, "residual", residual, torch.bfloat16, shape, True)
+        _need16(fn, dev, "x", x, torch.bfloat16, shape)
+        _need16(fn, dev, "residual", residual, torch.bfloat16, shape, True)
         self.s = x if residual is None else self._s
         norm = dict(residual=residual, res_out=None if residual is None else self.s, y=self.n, mu=self.mu, rsigma=self.rsigma)
         up, down = dict(y=self.h, z=self.z, bias=self.b1), dict(y=self.y, bias=self.b2, residual=self.s)
@@ -110,7 +112,7 @@ class MLP(_Block):
         if self.s is None:
             raise RuntimeError("MLP.backward before MLP.forward")
         self._check_weights(fn, dev)
-        L._need(fn, dev, "dy", dy, torch.bfloat16, (self.T, self.K))
+        _need16(fn, dev, "dy", dy, torch.bfloat16, (self.T, self.K))
         grads = dict(dbias=self.db1, workspace=self.workspace)
         if self.recipe == "fp8_delayed":
             scale, _, amax = self.slots["dy"]
