@@ -111,8 +111,8 @@ class GatedMLP(_Block):
     the next block's input.  ``backward(dout, dr)`` takes their gradients (dr may be None) and leaves
     ``dx`` (the gradient of x and of residual alike), ``dgamma``, ``dw`` and ``dw2``.
 
-    x, residual (or None) and dr are contiguous bf16 [tokens, K]; w, w2 and dout too, or fp32 where the
-    recipe quantizes them.  Anything else is refused before the first launch."""
+    x, residual (or None) and dr are contiguous bf16 [tokens, K], K at most 16384; w, w2 and dout too, or fp32 where
+    the recipe quantizes them; all on 16-byte boundaries.  Anything else is refused before the first launch."""
 
     def __init__(self, gamma: torch.Tensor, w: torch.Tensor, w2: torch.Tensor, tokens: int, recipe: str = "bf16",
                  act: int = L.ACT_SILU, eps: float = 1e-5, history_len: int = 16):
@@ -125,6 +125,7 @@ class GatedMLP(_Block):
                              "[K], [2 F, K] and [K, F]")
         self.gamma, self.w, self.w2 = gamma, w, w2
         self.T, self.K, self.F, self.recipe, self.act, self.eps = tokens, K, F, recipe, act, eps
+        self._check_norm(K, eps)
         self._check_weights("GatedMLP", L._device())
         dev, T = w.device, tokens
         bf, f32 = (dict(dtype=t, device=dev) for t in (torch.bfloat16, torch.float32))
@@ -140,10 +141,10 @@ class GatedMLP(_Block):
     # ---- checks: before the first launch of a pass, whose calls take addresses and sizes as they are ----
     def _operand(self, fn: str, dev: int, name: str, t: torch.Tensor, shape: tuple) -> None:
         """A tensor that the BF16 GEMMs or the quantizers (which take fp32 too) read."""
-        L._need(fn, dev, name, t, torch.bfloat16 if self.recipe == "bf16" else (torch.bfloat16, torch.float32), shape)
+        _need16(fn, dev, name, t, torch.bfloat16 if self.recipe == "bf16" else (torch.bfloat16, torch.float32), shape)
 
     def _check_weights(self, fn: str, dev: int) -> None:
-        L._need(fn, dev, "gamma", self.gamma, torch.float32, (self.K,))
+        _need16(fn, dev, "gamma", self.gamma, torch.float32, (self.K,))
         self._operand(fn, dev, "w", self.w, (2 * self.F, self.K))
         self._operand(fn, dev, "w2", self.w2, (self.K, self.F))
 
@@ -152,8 +153,8 @@ class GatedMLP(_Block):
         E4, tokens = L.E4M3, (self.T, self.K)
         fn, dev = "GatedMLP.forward", L._device()
         self._check_weights(fn, dev)
-        L._need(fn, dev, "x", x, torch.bfloat16, tokens)
-        L._need(fn, dev, "residual", residual, torch.bfloat16, tokens, True)
+        _need16(fn, dev, "x", x, torch.bfloat16, tokens)
+        _need16(fn, dev, "residual", residual, torch.bfloat16, tokens, True)
         if self.recipe == "bf16":
             L.te_rmsnorm_fp8(x, self.gamma, self.eps, E4, residual=residual, res_out=self.r, y=self.y, rsigma=self.rsigma)
             L.te_gated_gemm_bf16(self.y, self.w, self.act, h=self.h, gu=self.gu)
@@ -180,7 +181,7 @@ class GatedMLP(_Block):
         fn, dev = "GatedMLP.backward", L._device()
         self._check_weights(fn, dev)
         self._operand(fn, dev, "dout", dout, (self.T, self.K))
-        L._need(fn, dev, "dr", dr, torch.bfloat16, (self.T, self.K), True)
+        _need16(fn, dev, "dr", dr, torch.bfloat16, (self.T, self.K), True)
         if self.recipe == "bf16":
             L.te_gemm_bf16(dout, self.h, self.dw2, None, MN, MN)
             L.te_gated_bwd_bf16(self.y, self.w, self.w2, dout, self.gu, self.act, self.dgu, dx=self.dy, dw=self.dw)
