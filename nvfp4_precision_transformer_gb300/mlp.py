@@ -21,6 +21,7 @@ from .gated import RECIPES, _Block, _need16
 
 FWD_SLOTS = ("n", "w1", "h", "w2")
 BWD_SLOTS = ("dy", "dz")
+CAST_ELEMENTS = 1 << 34     # a quantizer takes fewer
 
 
 class MLP(_Block):
@@ -47,6 +48,9 @@ class MLP(_Block):
         if tokens <= 0 or tokens % step or K % step or F % step:
             raise ValueError(f"{tokens} tokens, K {K} and F {F} are not multiples of {step}")
         self._check_norm(K, eps)
+        # (dy, and under the other recipes h and dz, go through the quantizers)
+        if tokens * (K if recipe == "bf16" else max(K, F)) >= CAST_ELEMENTS:
+            raise ValueError(f"{tokens} tokens of K {K} and F {F} are more than a quantizer takes, {CAST_ELEMENTS - 1} elements")
         if act not in (L.ACT_NONE, L.ACT_RELU, L.ACT_SILU, L.ACT_GELU):
             raise ValueError(f"act {act} is no activation")
         self.gamma, self.beta, self.w1, self.b1, self.w2, self.b2 = gamma, beta, w1, b1, w2, b2

@@ -51,3 +51,17 @@ def test_tensors_off_their_boundary(launches, recipe):  # noqa: F811
     with pytest.raises(ValueError, match="dy"):
         b.backward(off(32, 64))
     assert len(launches) == n and b.step_idx == 0
+
+
+@pytest.mark.parametrize("recipe", RECIPES)
+def test_the_quantizers_limit(launches, monkeypatch, recipe):  # noqa: F811
+    """2^34 elements of dy or, where it is quantized, of h."""
+    wide = dict(w1=gpu(1 << 14, 64), b1=gpu(1 << 14, dtype=torch.float32), w2=gpu(64, 1 << 14))
+    cases = [dict(tokens=1 << 28, **params())]
+    if recipe != "bf16":
+        cases.append(dict(tokens=1 << 20, **params(**wide)))
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: pytest.fail("allocates before it refuses"))
+    for kw in cases:
+        with pytest.raises(ValueError, match="quantizer"):
+            MLP(recipe=recipe, **kw)
+    assert launches == []
