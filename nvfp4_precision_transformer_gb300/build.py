@@ -7,6 +7,7 @@ arithmetic.  The result lands next to this file and is git-ignored.
 from __future__ import annotations
 
 import os
+import re
 import shutil
 import subprocess
 from concurrent.futures import ThreadPoolExecutor
@@ -17,7 +18,7 @@ LIB = os.path.join(HERE, "libte_gb300.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--cudart", "shared"]
 UNITS = {"host.cu": [], "quant.cu": ["-fmad=false"], "norm.cu": [], "layernorm.cu": [], "gemm.cu": [], "gated.cu": [],
-         "act.cu": []}
+         "act.cu": ["-Xptxas", "-v"]}
 
 
 def _nvcc() -> str:
@@ -25,6 +26,19 @@ def _nvcc() -> str:
         if cand and os.path.exists(cand):
             return cand
     raise RuntimeError("nvcc not found")
+
+
+def check_registers(log: str) -> int:
+    """The kernels whose warps hand registers to one another (gemm_kernel with the epilogues kAct and kActGrad) have the
+    number at launch that their split adds up to: with another one the launcher would refuse every call.  ``log`` is what
+    ptxas -v says; returns how many such kernels there are."""
+    with open(os.path.join(CSRC, "gemm.cuh")) as f:
+        want = int(re.search(r"kLaunchRegs = (\d+)", f.read())[1])
+    found = re.findall(r"Compiling entry function '(\S*gemm_kernelILi\dELi2ELi[34]E\S*)'.*?Used (\d+) registers", log, re.S)
+    bad = [f"{name}: {n}" for name, n in found if int(n) != want]
+    if bad or not found:
+        raise RuntimeError(f"registers at launch other than {want}: {bad or 'no such kernel found'}")
+    return len(found)
 
 
 def build(verbose: bool = False, out_dir: str | None = None) -> str:
@@ -39,6 +53,8 @@ def build(verbose: bool = False, out_dir: str | None = None) -> str:
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed for {unit}:\n{r.stderr}")
+        if unit == "act.cu":
+            check_registers(r.stderr)
         if verbose:
             print(" ".join(cmd))
         return obj
