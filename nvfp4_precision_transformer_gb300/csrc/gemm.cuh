@@ -393,7 +393,9 @@ __global__ void __launch_bounds__(Cfg<KIND, CG, EPI>::kThreads, 1)
   if constexpr (EPI == kGated) gate_rows = ep.F;
   auto b_group = [&](int nt, int h) { return EPI == kGated ? nt + h * (gate_rows >> 7) : nt * 2 + h; };
 
-  // (the split stands at the head of each side: before a point where they meet again it spilled)
+  // (the split stands at the head of each side: before a point where they meet again it spilled more.  Bytes that are
+  // still stored: kAct in BF16 234, shared 306, in FP8 shared 112, kActGrad 72 to 104, none in the others.  They are the
+  // epilogue's: with 56 and 224 registers kActGrad has none or, shared, 148, with 104 and 200 it has 512 to 1344)
   if (C::kSplitRegs ? warp < C::kEpiFirst : (warp < 2 || warp >= kCopyWarp)) {
   if constexpr (C::kSplitRegs) dev::registers_down<kFewRegs>();
   if (warp == 0) {

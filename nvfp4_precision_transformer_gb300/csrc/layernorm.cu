@@ -13,9 +13,11 @@
 //   mu = sum of sum_w / C,   sum of (s - mu)^2 = sum of (M2_w + n_w (mu_w - mu)^2),
 // without the cancellation of sum(s^2) - C mu^2.  All sums are fp32 in a fixed order.
 //
-// 15872 x 4096 bf16: x + residual to s, y, MXFP8 94 us (587 MB, 6.2 TB/s), x to FP8 52 us (195 MB, 3.8: the arithmetic of
-// a row is no longer hidden where a row moves so little), backward with dres 85 us with the columns' sums (520 MB, 6.1).
-// gamma and beta read again for each row, from L1: kept in shared memory the first took 101.5 us.  Two rows ahead: no gain.
+// 15872 x 4096 bf16: x + residual to s, y, MXFP8 94 us (587 MB, 6.2 TB/s), x to bf16 53 (260 MB, 4.9) and to FP8 51 to 52
+// (195 MB, 3.8): the arithmetic of a row is no longer hidden where a row moves so little; backward with dres 85 us with the
+// columns' sums (520 MB, 6.1).  gamma and beta read again for each row, from L1: kept in shared memory the first took
+// 101.5 us.  Two rows ahead: no gain.  At 128 registers the forward kernels of fp32 rows store up to 88 bytes a thread, the
+// backward ones past 8192 columns 52 (bf16) and 96 (fp32), the others none.
 #include "norm_rows.cuh"
 
 namespace te {
