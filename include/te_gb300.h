@@ -493,7 +493,8 @@ te_status te_act_dgrad_nvfp4(const uint8_t* dy, const uint8_t* sd, const float* 
  * w2 [N, F], then (each nullable) dx bf16 [T, K] = dz w and dw [F, K] = dz^T x (dw_dtype TE_BF16 or
  * TE_F32; accumulate = 1 with TE_F32: dw += dz^T x; dbias is overwritten all the same), both from dz as
  * written, in bf16.  w [F, K] is read for dx and x for dw; each may be NULL where it is not read (K is then
- * of no account where neither is).  K, F, N multiples of 16.  T = 0: dw = 0 (kept with accumulate), dbias = 0. */
+ * of no account where neither is).  K, F, N multiples of 16; K at most 2^30, with dw in fp32 2^29.  T = 0: dw = 0
+ * (kept with accumulate), dbias = 0. */
 te_status te_act_bwd_bf16(const void* x, const void* w, const void* w2, const void* dy, const void* z, int act, void* dz,
                           float* dbias, float* workspace, size_t workspace_bytes, void* dx, void* dw, te_dtype dw_dtype,
                           int accumulate, int64_t T, int64_t K, int64_t F, int64_t N, void* stream);

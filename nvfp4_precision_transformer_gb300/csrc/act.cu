@@ -397,6 +397,7 @@ te_status te_act_bwd_bf16(const void* x, const void* w, const void* w2, const vo
   if (s != TE_OK) return s;
   if ((dx || dw) && (K <= 0 || K % 16 || K > (int64_t(1) << 30))) return TE_ERR_SHAPE;
   if (dw && dw_dtype != TE_BF16 && dw_dtype != TE_F32) return TE_ERR_DTYPE;
+  if (dw && dw_dtype == TE_F32 && K > (int64_t(1) << 29)) return TE_ERR_SHAPE;   // (columns are counted in bytes)
   if (accumulate != 0 && accumulate != 1) return TE_ERR_ARG;
   if (dw && accumulate && dw_dtype != TE_F32) return TE_ERR_DTYPE;
   if (!aligned16(dx) || !aligned16(dw)) return TE_ERR_ALIGN;

@@ -267,7 +267,8 @@ __device__ __forceinline__ void tile_coords(int tile, int m_tiles, int n_tiles, 
 // BF16, whose segments are short, is cut in the backward pass (dz does not depend on whether its sums are asked for) and
 // where y is fp32: uncut, a bf16 output is far within its own rounding, and cut it would cost 3 to 6 % (4096 tokens, K =
 // 16384, N = 4096 307 -> 327 us).  13 k-tiles keep the error within 8e-7 at every K (terms of both signs; of one sign
-// 1.7e-6, uncut 7.9e-5 at 16384).  Errors at K = 1024, 2048, 4096, 8192, 16384, and us of y in fp32 at 4096 tokens, K = N = 4096, and of dz at 15872 tokens, F = 16384, N = 4096:
+// 1.7e-6, uncut 7.9e-5 at 16384).  Errors at K = 1024, 2048, 4096, 8192, 16384, and us of y in fp32 at 4096 tokens, K =
+// N = 4096, and of dz at 15872 tokens, F = 16384, N = 4096:
 //   10 k-tiles 4.7e-7 4.7e-7 5.5e-7 6.0e-7 6.0e-7  92.4  1338     13  4.7e-7 6.5e-7 7.8e-7 7.9e-7 7.9e-7  88.3  1295
 //   16         9.9e-7 1.0e-6 9.9e-7 1.0e-6 1.0e-6  87.3  1325     22  9.9e-7 1.0e-6 1.4e-6 1.4e-6 1.4e-6  86.5  1247
 //   uncut      9.9e-7 2.1e-6 4.4e-6 9.1e-6 1.9e-5  84.9  1241
