@@ -322,6 +322,7 @@ te_status te_layernorm_bwd(const void* dy, const void* s, te_dtype in_dtype, int
  * Common: A [M, K], B [N, K] contraction-major; D [M, N] row-major of out_dtype
  * (TE_BF16, round-to-nearest-even, or TE_F32); bias (nullable) device fp32 [N];
  * fp32 accumulation in tensor memory; epilogue D = alpha * acc + bias.
+ * M, N and K at most 2^30, N at most 2^29 where an fp32 D is not added to.
  * accumulate = 1 (out_dtype TE_F32 only, else TE_ERR_DTYPE): D += alpha * acc + bias,
  * the Wgrad form that adds into an fp32 main gradient (the pages' fp8_wgrad /
  * weight-gradient path of "Introduction to FP8 training using Transformer Engine",

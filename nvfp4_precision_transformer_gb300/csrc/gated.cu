@@ -259,6 +259,7 @@ te_status te_gated_bwd_bf16(const void* x, const void* w, const void* w2, const 
   if (dw && dw_dtype != TE_BF16 && dw_dtype != TE_F32) return TE_ERR_DTYPE;
   if (accumulate != 0 && accumulate != 1) return TE_ERR_ARG;
   if (dw && accumulate && dw_dtype != TE_F32) return TE_ERR_DTYPE;
+  if (dw && dw_dtype == TE_F32 && !accumulate && K > (int64_t(1) << 29)) return TE_ERR_SHAPE;   // as te_gemm_bf16
   if (!aligned16(dx) || !aligned16(dw)) return TE_ERR_ALIGN;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (T == 0) {

@@ -11,6 +11,8 @@ te_status check_gemm(const void* A, const void* B, const void* D, te_dtype out, 
   if (accumulate && out != TE_F32) return TE_ERR_DTYPE;
   if (M < 0 || N < 0 || K <= 0 || M % 16 || N % 16 || K % k_multiple) return TE_ERR_SHAPE;
   if (M > (int64_t(1) << 30) || N > (int64_t(1) << 30) || K > (int64_t(1) << 30)) return TE_ERR_SHAPE;
+  // (an fp32 D is stored by the byte of its row, in 32 bits; added to, by the element)
+  if (out == TE_F32 && !accumulate && N > (int64_t(1) << 29)) return TE_ERR_SHAPE;
   if (M * N == 0) return TE_OK;
   if (!A || !B || !D) return TE_ERR_NULL;
   if (!aligned16(A) || !aligned16(B) || !aligned16(D)) return TE_ERR_ALIGN;
